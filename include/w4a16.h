@@ -67,8 +67,11 @@ typedef enum {
     W4A16_ERR_TIMEOUT = 5,       /* device: a bounded wait gave up (kernel returned early) */
     W4A16_ERR_BAD_OFFSETS = 6,   /* device: expert_offsets not 0 = o[0] <= ... <= o[E] = R */
     W4A16_ERR_WORKSPACE = 7,     /* workspace missing or smaller than w4a16_workspace_bytes */
-    W4A16_ERR_BAD_ROUTING = 8    /* device: a top-k expert id outside [0, E), or a combine row
+    W4A16_ERR_BAD_ROUTING = 8,   /* device: a top-k expert id outside [0, E), or a combine row
                                     outside [0, R) */
+    W4A16_ERR_BAD_CACHE = 9      /* device: a page outside the cache, a length that is negative or
+                                    past its row of the page table, or a rotary position outside
+                                    the table */
 } w4a16_status;
 
 /*
@@ -347,6 +350,124 @@ W4A16_API w4a16_status w4a16_blocks_linear(int32_t format, const uint16_t* x, co
 W4A16_API w4a16_status w4a16_blocks_dequant(int32_t format, const uint8_t* blocks, int64_t N, int64_t K, float* w,
                                             void* stream);
 
+/*
+ * Attention over a paged cache, and what fills it.
+ *
+ * Element types: fp16 or bf16 (uint16_t bit patterns), the same for queries,
+ * keys, values, cache and output of a call. Every row of head_dim elements is
+ * contiguous and starts on a 16-byte boundary; every stride is in elements
+ * and a multiple of 8, so q, k and v may be views of one fused projection.
+ */
+#define W4A16_DTYPE_F16 1
+#define W4A16_DTYPE_BF16 2
+
+/*
+ * Rotary positions. Pair i of a head turns by the angle whose cosine and sine
+ * are table[p * rotary_dim + i] and table[p * rotary_dim + rotary_dim / 2 + i]
+ * for its position p:  (a, b) -> (a cos - b sin, b cos + a sin), in fp32,
+ * rounded once. The pair is elements (i, i + rotary_dim / 2), or (2i, 2i + 1)
+ * where `interleaved` is set; elements from rotary_dim on are left as they are.
+ */
+typedef struct {
+    const float* table;       /* device, fp32 [rows, rotary_dim], 16-byte aligned */
+    int64_t rows;
+    int32_t rotary_dim;       /* multiple of 16, at most head_dim and 256 */
+    int32_t interleaved;
+    const int32_t* positions; /* device, int32 [axes, T]; w4a16_kv_append also takes NULL:
+                                 each token's place in its sequence (axes is then 1) */
+    int32_t axes;             /* 1 to 4 */
+    const uint8_t* pair_axes; /* host, [rotary_dim / 2]: the axis whose position turns each
+                                 pair; NULL: axis 0 turns all */
+} w4a16_rotary;
+
+/*
+ * out[t, h] = x[t, h] turned by token t's positions. x and out are
+ * [T, heads, head_dim] with the given strides; out may be x (the same strides),
+ * and may not overlap it otherwise. head_dim is a multiple of 16, at most 1024.
+ * A position outside the table is reported (W4A16_ERR_BAD_CACHE) and its pairs
+ * are copied unturned.
+ */
+W4A16_API w4a16_status w4a16_rope(int32_t dtype, const uint16_t* x, int64_t x_row_stride, int64_t x_head_stride,
+                                  uint16_t* out, int64_t out_row_stride, int64_t out_head_stride, int64_t T,
+                                  int32_t heads, int32_t head_dim, const w4a16_rotary* rotary, void* stream);
+
+/*
+ * A cache of `pages` pages of `page_size` tokens, and the batch of sequences
+ * that a call appends or attends with. Element d of head g of a page's slot is
+ * at page * page_stride + slot * slot_stride + g * head_stride + d in both k
+ * and v. Place p of sequence b is in slot p % page_size of page
+ * page_table[b * page_table_stride + p / page_size]; entries that no place
+ * below kv_lens[b] needs are never used. Sequence b's new tokens are rows
+ * q_offsets[b] <= t < q_offsets[b + 1] of the call (0 = q_offsets[0] <= ... <=
+ * q_offsets[batch] = T), and kv_lens[b] counts its cached tokens with the new
+ * ones among them: row t has the place kv_lens[b] - (q_offsets[b + 1] - t).
+ */
+typedef struct {
+    uint16_t* k;               /* device, 16-byte aligned */
+    uint16_t* v;
+    int64_t pages, page_stride, slot_stride, head_stride;
+    const int32_t* page_table; /* device, int32 */
+    int64_t page_table_stride;
+    int32_t max_pages;         /* entries of a row of the page table */
+    int32_t page_size;         /* a multiple of 16; max_pages * page_size <= 2^30 */
+    const int32_t* q_offsets;  /* device, int32 [batch + 1] */
+    const int32_t* kv_lens;    /* device, int32 [batch] */
+    int32_t batch, kv_heads;
+    int32_t head_dim;          /* 64 or 128 */
+    int32_t dtype;
+} w4a16_paged_cache;
+
+/*
+ * Stores k and v ([T, kv_heads, head_dim], strided) into the cache at each
+ * row's place, k turned by `rotary` (NULL: as it is), and writes q
+ * ([T, heads, head_dim], strided) turned alike to q_out (contiguous; may be q
+ * if q is contiguous). q NULL: keys and values only. One launch. A row whose
+ * place is negative (kv_lens shorter than its new tokens) is not stored, nor is one
+ * whose page or length is out of range (W4A16_ERR_BAD_CACHE) or that no
+ * sequence holds (W4A16_ERR_BAD_OFFSETS).
+ */
+W4A16_API w4a16_status w4a16_kv_append(const w4a16_paged_cache* cache, int64_t T, const uint16_t* k,
+                                       int64_t k_row_stride, int64_t k_head_stride, const uint16_t* v,
+                                       int64_t v_row_stride, int64_t v_head_stride, const uint16_t* q,
+                                       int64_t q_row_stride, int64_t q_head_stride, int32_t heads, uint16_t* q_out,
+                                       const w4a16_rotary* rotary, void* stream);
+
+/* Each row sees only the places up to its own (else: all of its sequence). */
+#define W4A16_CAUSAL 1u
+
+/*
+ * out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, g]) v[j, g] over the
+ * places j of row t's sequence that it sees, g = h / (heads / kv_heads): below
+ * kv_lens[b], with W4A16_CAUSAL up to its own place p, and with window > 0
+ * (which needs W4A16_CAUSAL) above p - window. A row that sees nothing gets
+ * out = 0. lse (fp32 [T, heads], or NULL) is the natural logarithm of the
+ * softmax's sum, -infinity for such a row. Pages that hold only places no row of a
+ * sequence sees, and slots past its last place, are never multiplied in, whatever
+ * they hold. Places that some rows of a sequence see and others do not must
+ * hold finite values.
+ *
+ * q is [T, heads, head_dim] with the given strides, out contiguous.
+ * max_q_len is at least the number of new tokens of every sequence (more:
+ * W4A16_ERR_BAD_OFFSETS, and that sequence's rows are not written).
+ * Scores, softmax and sums are in fp32; the softmax weights are rounded to
+ * the element type for the products with v; out is rounded once. Sequences
+ * with few rows are split over their length and joined through `workspace`,
+ * in a fixed order: results are deterministic.
+ * workspace: device buffer of at least
+ * w4a16_paged_attention_workspace_bytes(...) bytes, zero-filled once before
+ * its first use (w4a16_workspace_init), not shared with the linear layers'
+ * calls; every call leaves it ready for the next, of any shape that it is large enough for.
+ */
+W4A16_API w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int64_t T, const uint16_t* q,
+                                             int64_t q_row_stride, int64_t q_head_stride, int32_t heads,
+                                             int64_t max_q_len, uint32_t flags, int32_t window, float scale,
+                                             uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
+/* Bytes of workspace w4a16_paged_attention needs on the current device; 0 if none. */
+W4A16_API size_t w4a16_paged_attention_workspace_bytes(int64_t T, int32_t batch, int32_t heads, int32_t kv_heads,
+                                                       int32_t head_dim, int64_t max_q_len);
+
 /* Bytes of workspace w4a16_linear (E = 1) or w4a16_grouped_linear (E experts,
  * M = R rows) needs for this problem on the current device; 0 if none. */
 W4A16_API size_t w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group, int32_t E);
@@ -358,8 +479,10 @@ W4A16_API w4a16_status w4a16_workspace_init(void* workspace, size_t workspace_by
 
 /* Synchronizes `stream`, then reads and clears the current device's sticky
  * error word: W4A16_OK, W4A16_ERR_TIMEOUT (a bounded wait in the GEMV or the
- * GEMM gave up), W4A16_ERR_BAD_OFFSETS (w4a16_grouped_linear) or
- * W4A16_ERR_BAD_ROUTING (w4a16_moe_dispatch, w4a16_moe_combine). The word
+ * GEMM gave up), W4A16_ERR_BAD_OFFSETS (w4a16_grouped_linear, or the query
+ * offsets of w4a16_kv_append and w4a16_paged_attention),
+ * W4A16_ERR_BAD_ROUTING (w4a16_moe_dispatch, w4a16_moe_combine) or
+ * W4A16_ERR_BAD_CACHE (w4a16_rope, w4a16_kv_append, w4a16_paged_attention). The word
  * keeps the first error raised since it was last cleared. */
 W4A16_API w4a16_status w4a16_device_status(void* stream);
 

@@ -160,3 +160,73 @@ def test_blocks_validation(lib):
     assert lib.w4a16_blocks_dequant(Q4K, p, 8, 256, q, None) == 3
     assert lib.w4a16_blocks_dequant(Q4K, p, 0, 256, p, None) == 0
     assert lib.w4a16_blocks_dequant(Q51, p, 8, 0, p, None) == 0
+
+
+def _cache_struct(**kw):
+    import w4a16_group_quantized_linear_gb300 as w4
+
+    p = 1 << 20
+    d = dict(k=p, v=p, pages=4, page_stride=16 * 128, slot_stride=128, head_stride=64, page_table=p,
+             page_table_stride=4, max_pages=4, page_size=16, q_offsets=p, kv_lens=p, batch=2, kv_heads=2, head_dim=64,
+             dtype=1)
+    d.update(kw)
+    return w4._PagedCache(**d)
+
+
+def _attend(lib, T=2, heads=4, q=1 << 20, out=1 << 20, lse=None, q_len=1, flags=1, window=0, scale=0.1, row=256,
+            head=64, **kw):
+    c = _cache_struct(**kw)
+    return lib.w4a16_paged_attention(ctypes.byref(c), T, q, row, head, heads, q_len, flags, window, scale, out, lse,
+                                     None, 0, None)
+
+
+def test_paged_attention_validation(lib):
+    """All host checks come before any device work."""
+    assert _attend(lib, T=0) == 0
+    assert _attend(lib, T=-1) == 1 and _attend(lib, heads=3) == 1 and _attend(lib, heads=0) == 1
+    assert _attend(lib, flags=2) == 1 and _attend(lib, window=-1) == 1 and _attend(lib, flags=0, window=4) == 1
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert _attend(lib, scale=scale) == 1
+    assert _attend(lib, q=None) == 1 and _attend(lib, out=None) == 1 and _attend(lib, q_len=0) == 1
+    assert _attend(lib, q=(1 << 20) + 8) == 3 and _attend(lib, k=(1 << 20) + 2) == 3
+    assert _attend(lib, lse=(1 << 20) + 2) == 3
+    assert _attend(lib, row=60) == 1 and _attend(lib, head=-64) == 1
+    assert _attend(lib, dtype=0) == 2 and _attend(lib, head_dim=96) == 2 and _attend(lib, page_size=24) == 2
+    assert _attend(lib, max_pages=1 << 28) == 2
+    assert _attend(lib, page_size=0) == 1 and _attend(lib, batch=0) == 1 and _attend(lib, kv_heads=0) == 1
+    assert _attend(lib, slot_stride=100) == 1 and _attend(lib, page_table=None) == 1 and _attend(lib, v=None) == 1
+    assert lib.w4a16_paged_attention(None, 2, None, 0, 0, 4, 1, 1, 0, 0.1, None, None, None, 0, None) == 1
+    assert lib.w4a16_paged_attention_workspace_bytes(0, 1, 4, 2, 64, 1) == 0
+    assert lib.w4a16_paged_attention_workspace_bytes(1, 1, 4, 3, 64, 1) == 0
+
+
+def test_rope_and_append_validation(lib):
+    import w4a16_group_quantized_linear_gb300 as w4
+
+    p = 1 << 20
+
+    def rotary(**kw):
+        d = dict(table=p, rows=8, rotary_dim=64, interleaved=0, positions=p, axes=1, pair_axes=None)
+        d.update(kw)
+        return ctypes.byref(w4._Rotary(**d))
+
+    def rope(dtype=1, x=p, out=p, T=2, heads=4, D=64, row=256, **kw):
+        return lib.w4a16_rope(dtype, x, row, 64, out, 256, 64, T, heads, D, rotary(**kw), None)
+
+    assert rope(T=0) == 0 and rope(heads=0) == 0
+    assert rope(dtype=7) == 2 and rope(T=-1) == 1 and rope(row=4) == 1 and rope(D=24) == 2
+    assert rope(x=None) == 1 and rope(out=p + 8) == 3 and rope(table=p + 4) == 3 and rope(table=None) == 1
+    assert rope(rotary_dim=80) == 1 and rope(rotary_dim=24) == 2 and rope(rotary_dim=0) == 1
+    assert rope(positions=None) == 1 and rope(axes=5) == 2 and rope(axes=0) == 1
+    assert rope(pair_axes=b"\1" * 32) == 1
+    assert lib.w4a16_rope(1, p, 256, 64, p, 256, 64, 2, 4, 64, None, None) == 1
+
+    def append(k=p, q=None, q_out=None, heads=0, T=2, r=None, row=128, **kw):
+        c = _cache_struct(**kw)
+        return lib.w4a16_kv_append(ctypes.byref(c), T, k, row, 64, p, 128, 64, q, 256, 64, heads, q_out, r, None)
+
+    assert append(T=0) == 0
+    assert append(k=None) == 1 and append(row=4) == 1 and append(k=p + 2) == 3
+    assert append(q=p, heads=4) == 1 and append(q=p, heads=4, q_out=p + 2) == 3
+    assert append(r=rotary(positions=None, axes=3)) == 1 and append(r=rotary(rotary_dim=128)) == 1
+    assert append(dtype=3) == 2 and append(kv_lens=None) == 1

@@ -4,6 +4,10 @@ y = x W^T with int4-symmetric weights (nibble q+8, even k in the low nibble),
 one fp16 scale per group of 32/64/128 input features and fp16 activations
 (LLM170 page, introduction: "W4A16 (int4 sym g128, f16 activations)").
 
+Around the layer: the routed experts' dispatch, GGUF block formats, and the
+attention that sits between a decoder's projections (rotary positions, a paged
+key/value cache and attention over it, fp16 or bf16).
+
 This module is a thin ctypes binding over the C ABI of ``libw4a16.so``
 (declared in ``include/w4a16.h``): it checks tensor dtypes and shapes,
 allocates outputs with PyTorch and passes raw device pointers and the current
@@ -22,6 +26,7 @@ import torch
 
 __all__ = ["pack", "unpack", "linear", "linear_gated", "grouped_linear", "grouped_linear_gather", "moe_route",
            "moe_dispatch", "moe_combine", "blocks_row_bytes", "blocks_linear", "blocks_dequant", "BLOCK_FORMATS",
+           "rope_table", "rope", "kv_append", "paged_attention",
            "workspace_bytes", "device_status", "STATIC_WEIGHTS",
            "W4A16Error", "lib", "LIB_PATH", "EXPORTS", "STATUS"]
 
@@ -29,9 +34,25 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw4a16.so
 
 STATUS = {0: "W4A16_OK", 1: "W4A16_ERR_INVALID_ARG", 2: "W4A16_ERR_UNSUPPORTED", 3: "W4A16_ERR_MISALIGNED",
           4: "W4A16_ERR_CUDA", 5: "W4A16_ERR_TIMEOUT", 6: "W4A16_ERR_BAD_OFFSETS", 7: "W4A16_ERR_WORKSPACE",
-          8: "W4A16_ERR_BAD_ROUTING"}
+          8: "W4A16_ERR_BAD_ROUTING", 9: "W4A16_ERR_BAD_CACHE"}
 
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+
+
+class _Rotary(ctypes.Structure):
+    """w4a16_rotary"""
+    _fields_ = [("table", _P), ("rows", _I64), ("rotary_dim", _I32), ("interleaved", _I32), ("positions", _P),
+                ("axes", _I32), ("pair_axes", ctypes.c_char_p)]
+
+
+class _PagedCache(ctypes.Structure):
+    """w4a16_paged_cache"""
+    _fields_ = [("k", _P), ("v", _P), ("pages", _I64), ("page_stride", _I64), ("slot_stride", _I64),
+                ("head_stride", _I64), ("page_table", _P), ("page_table_stride", _I64), ("max_pages", _I32),
+                ("page_size", _I32), ("q_offsets", _P), ("kv_lens", _P), ("batch", _I32), ("kv_heads", _I32),
+                ("head_dim", _I32), ("dtype", _I32)]
+
+
 # name -> (restype, argtypes); mirrors include/w4a16.h
 EXPORTS = {
     "w4a16_pack": (_I32, [_P, _I64, _I64, _I32, _P, _P, _P]),
@@ -52,6 +73,11 @@ EXPORTS = {
     "w4a16_blocks_row_bytes": (_I64, [_I32, _I64]),
     "w4a16_blocks_linear": (_I32, [_I32, _P, _P, _P, _I64, _I64, _I64, _P]),
     "w4a16_blocks_dequant": (_I32, [_I32, _P, _I64, _I64, _P, _P]),
+    "w4a16_rope": (_I32, [_I32, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, _P]),
+    "w4a16_kv_append": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P]),
+    "w4a16_paged_attention": (_I32, [_P, _I64, _P, _I64, _I64, _I32, _I64, ctypes.c_uint32, _I32, ctypes.c_float,
+                                     _P, _P, _P, _SZ, _P]),
+    "w4a16_paged_attention_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32, _I64]),
     "w4a16_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
     "w4a16_workspace_init": (_I32, [_P, _SZ, _P]),
     "w4a16_device_status": (_I32, [_P]),
@@ -63,6 +89,12 @@ EXPORTS = {
 
 # flags of w4a16_linear_ex / w4a16_linear_gated_ex (include/w4a16.h)
 STATIC_WEIGHTS = 1
+
+# flag of w4a16_paged_attention
+CAUSAL = 1
+
+# element types of the attention operators (W4A16_DTYPE_* in include/w4a16.h)
+_DTYPES = {torch.float16: 1, torch.bfloat16: 2}
 
 # GGUF block formats (W4A16_FORMAT_* in include/w4a16.h)
 BLOCK_FORMATS = {"q4_k": 1, "q5_1": 2}
@@ -137,14 +169,14 @@ def _out(out, shape, device: torch.device, K: int):
     return out
 
 
-# one zero-initialised workspace per (device, stream), grown on demand
+# one zero-initialised workspace per (device, stream, kind of call), grown on demand
 _ws: dict = {}
 
 
-def _workspace(dev: torch.device, stream, nbytes: int):
+def _workspace(dev: torch.device, stream, nbytes: int, kind: str = "linear"):
     if nbytes == 0:
         return None
-    key = (dev.index, stream.value)
+    key = (dev.index, stream.value, kind)
     buf = _ws.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
@@ -389,6 +421,186 @@ def moe_combine(y_sorted: torch.Tensor, row_of: torch.Tensor, topk_weights: torc
     _check(lib().w4a16_moe_combine(_ptr(y_sorted), R, _ptr(row_of), _ptr(topk_weights), T, k, N, _ptr(out),
                                    _stream(y_sorted.device)), "w4a16_moe_combine")
     return out
+
+
+def rope_table(rows: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The angles of :func:`rope` and :func:`kv_append`: fp32 [rows, rotary_dim],
+    cos(p * base^(-2i / rotary_dim)) for pair i in the first half of row p and
+    the sine in the second, formed in 64 bits and rounded once. A table of any
+    other frequencies in the same layout serves as well."""
+    pair = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * base ** (-pair / rotary_dim)
+    return torch.cat((angle.cos(), angle.sin()), dim=1).float()
+
+
+def _heads(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
+    """A [tokens, heads, head_dim] tensor whose heads' rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 3-d torch.float16 or torch.bfloat16 CUDA tensor")
+    if t.stride(2) != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name}: expected the type and device of the other tensors")
+    return t
+
+
+def _same_heads_out(out, x: torch.Tensor, name: str):
+    """A contiguous result of x's shape: new, or the caller's."""
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _heads(out, name, x)
+    if out.shape != x.shape or not out.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous and of the input's shape")
+    return out
+
+
+def _int32(t: torch.Tensor, name: str, dim: int, device: torch.device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or t.device != device:
+        raise ValueError(f"{name}: expected a {dim}-d torch.int32 tensor on the other tensors' device")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t
+
+
+def _rotary(table, positions, pair_axes, interleaved: bool, T: int, device: torch.device) -> _Rotary:
+    _need(table, "table", torch.float32, 2)
+    if table.device != device:
+        raise ValueError("table: must be on the other tensors' device")
+    axes = 1
+    if positions is not None:
+        if isinstance(positions, torch.Tensor) and positions.dim() == 1:
+            positions = positions[None]
+        _int32(positions, "positions", 2, device)
+        if positions.shape[1] != T or not positions.is_contiguous():
+            raise ValueError("positions: expected contiguous [T] or [axes, T]")
+        axes = positions.shape[0]
+    if pair_axes is not None:
+        pair_axes = bytes(pair_axes)
+        if 2 * len(pair_axes) != table.shape[1]:
+            raise ValueError("pair_axes: expected one axis per pair, rotary_dim / 2 of them")
+    return _Rotary(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0,
+                   None if positions is None else positions.data_ptr(), axes, pair_axes)
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, pair_axes=None, interleaved: bool = False,
+         out: torch.Tensor | None = None) -> torch.Tensor:
+    """x turned by its tokens' positions: x fp16 or bf16 [T, heads, head_dim]
+    (a view of a fused projection will do), positions int32 [T] or [axes, T],
+    table fp32 [rows, rotary_dim] (:func:`rope_table`); elements past rotary_dim
+    are copied. Pair i is elements (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+    ``interleaved``. ``pair_axes`` gives the axis (0 to 3) whose position turns
+    each pair (time, height and width of a video's patches, say); without it
+    axis 0 turns all. ``out`` may be x itself."""
+    _heads(x, "x")
+    T, H, D = x.shape
+    r = _rotary(table, positions, pair_axes, interleaved, T, x.device)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _heads(out, "out", x)
+        if out.shape != x.shape:
+            raise ValueError("out: must have x's shape")
+    _check(lib().w4a16_rope(_DTYPES[x.dtype], _ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0),
+                            out.stride(1), T, H, D, ctypes.byref(r), _stream(x.device)), "w4a16_rope")
+    return out
+
+
+def _cache(k_cache, v_cache, page_table, q_offsets, kv_lens, like: torch.Tensor) -> _PagedCache:
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{name}: expected a 4-d tensor of the other tensors' type and device")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if k_cache.stride(3) != 1:
+        raise ValueError("k_cache, v_cache: the last dimension must be contiguous")
+    _int32(page_table, "page_table", 2, like.device)
+    _int32(q_offsets, "q_offsets", 1, like.device)
+    _int32(kv_lens, "kv_lens", 1, like.device)
+    B = kv_lens.shape[0]
+    if page_table.shape[0] != B or q_offsets.shape[0] != B + 1:
+        raise ValueError("page_table [B, max_pages], q_offsets [B + 1] and kv_lens [B] must agree")
+    pages, size, G, D = k_cache.shape
+    sp, ss, sh, _ = k_cache.stride()
+    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, sp, ss, sh, page_table.data_ptr(),
+                       page_table.stride(0), page_table.shape[1], size, q_offsets.data_ptr(), kv_lens.data_ptr(), B,
+                       G, D, _DTYPES[like.dtype])
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              page_table: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor,
+              q: torch.Tensor | None = None, table: torch.Tensor | None = None,
+              positions: torch.Tensor | None = None, pair_axes=None, interleaved: bool = False,
+              q_out: torch.Tensor | None = None):
+    """Stores the new tokens' k and v (fp16 or bf16 [T, kv_heads, head_dim]) into
+    the paged cache and, with ``table``, turns k and q by their rotary positions
+    on the way (``positions`` and the rest as in :func:`rope`; without
+    ``positions`` each token's place in its sequence). Returns the turned q
+    [T, heads, head_dim] (contiguous; ``q_out`` if given), or None without q.
+
+    The cache is [pages, page_size, kv_heads, head_dim] in any strides with
+    contiguous rows (page_size a multiple of 16, head_dim 64 or 128). Sequence
+    b's new tokens are rows q_offsets[b] to q_offsets[b + 1] of k, v and q;
+    kv_lens[b] counts its cached tokens with these among them; its place p lives in
+    slot p % page_size of page page_table[b, p // page_size]. All three are int32
+    on the device: a captured graph follows their values."""
+    _heads(k, "k")
+    _heads(v, "v", k)
+    T, G, D = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    c = _cache(k_cache, v_cache, page_table, q_offsets, kv_lens, k)
+    if (c.kv_heads, c.head_dim) != (G, D):
+        raise ValueError("the cache must have k's heads and head_dim")
+    H, sq = 0, (0, 0, 0)
+    if q is not None:
+        _heads(q, "q", k)
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q must be [T, heads, head_dim]")
+        H, sq = q.shape[1], q.stride()
+        q_out = _same_heads_out(q_out, q, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    r = None
+    if table is not None:
+        r = ctypes.byref(_rotary(table, positions, pair_axes, interleaved, T, k.device))
+    elif positions is not None or pair_axes is not None:
+        raise ValueError("positions and pair_axes need table")
+    _check(lib().w4a16_kv_append(ctypes.byref(c), T, _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
+                                 v.stride(1), _ptr(q) if q is not None else None, sq[0], sq[1], H,
+                                 _ptr(q_out) if q is not None else None, r, _stream(k.device)), "w4a16_kv_append")
+    return q_out
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    q_offsets: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int, causal: bool = True,
+                    window: int = 0, scale: float | None = None, out: torch.Tensor | None = None,
+                    return_lse: bool = False):
+    """Attention of the new tokens' queries (fp16 or bf16 [T, heads, head_dim])
+    over the paged cache of :func:`kv_append`: softmax(scale q k^T) v per row,
+    heads in groups of heads / kv_heads sharing a cached head. A row sees its sequence's
+    places up to its own (all of them with ``causal=False``), the last ``window``
+    of them where that is not 0. ``max_q_len`` is at least the longest sequence's number
+    of new tokens (it chooses the kernels; the lengths themselves stay on the
+    device). ``scale`` defaults to head_dim^-1/2. A row that sees nothing gets 0.
+
+    Returns out [T, heads, head_dim], or (out, lse) with ``return_lse``: lse
+    fp32 [T, heads] is the natural logarithm of the softmax's sum."""
+    _heads(q, "q")
+    T, H, D = q.shape
+    c = _cache(k_cache, v_cache, page_table, q_offsets, kv_lens, q)
+    if c.head_dim != D or c.kv_heads == 0 or H % c.kv_heads != 0:
+        raise ValueError("the cache must have q's head_dim, and heads must be a multiple of its heads")
+    out = _same_heads_out(out, q, "out")
+    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
+    st = _stream(q.device)
+    h = lib()
+    ws = _workspace(q.device, st, int(h.w4a16_paged_attention_workspace_bytes(T, c.batch, H, c.kv_heads, D,
+                                                                               max_q_len)), "attention")
+    _check(h.w4a16_paged_attention(ctypes.byref(c), T, _ptr(q), q.stride(0), q.stride(1), H, max_q_len,
+                                   CAUSAL if causal else 0, window, D ** -0.5 if scale is None else scale, _ptr(out),
+                                   _ptr(lse) if return_lse else None, _ptr(ws) if ws is not None else None,
+                                   ws.numel() if ws is not None else 0, st), "w4a16_paged_attention")
+    return (out, lse) if return_lse else out
 
 
 def device_status(raise_on_error: bool = True) -> int:

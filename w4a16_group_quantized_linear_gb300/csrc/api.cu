@@ -139,6 +139,8 @@ const char* w4a16_status_string(w4a16_status status) {
         case W4A16_ERR_BAD_OFFSETS: return "W4A16_ERR_BAD_OFFSETS: expert offsets are not a partition of the rows";
         case W4A16_ERR_WORKSPACE: return "W4A16_ERR_WORKSPACE: workspace missing or too small";
         case W4A16_ERR_BAD_ROUTING: return "W4A16_ERR_BAD_ROUTING: an expert id or a combine row is out of range";
+        case W4A16_ERR_BAD_CACHE:
+            return "W4A16_ERR_BAD_CACHE: a page, a cached length or a rotary position is out of range";
     }
     return "W4A16: unknown status";
 }

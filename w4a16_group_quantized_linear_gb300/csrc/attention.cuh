@@ -1,0 +1,160 @@
+// Declarations shared by the attention operators: 16-bit element types, the
+// paged cache as the kernels see it, and the launch helper.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.cuh"
+#include "sm100_ptx.cuh"
+
+namespace w4a16 {
+
+// ------------------------------------------------------- 16-bit elements --
+
+struct Fp16 {
+    static constexpr int kDtype = W4A16_DTYPE_F16;
+    __device__ static __forceinline__ float2 unpack(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&v));
+    }
+    __device__ static __forceinline__ uint32_t pack(float lo, float hi) {  // round to nearest even
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+
+struct Bf16 {
+    static constexpr int kDtype = W4A16_DTYPE_BF16;
+    __device__ static __forceinline__ float2 unpack(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    }
+    __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+
+// ---------------------------------------------------------------- cache --
+
+// The paged cache and the batch that is appended to it or attends over it.
+// Strides are in elements; element (page, slot, head, d) of either cache sits
+// at page * page_stride + slot * slot_stride + head * head_stride + d.
+struct CacheArgs {
+    uint16_t* k;
+    uint16_t* v;
+    int64_t pages, page_stride, slot_stride, head_stride;
+    const int32_t* table;   // [batch, table_stride], max_pages entries used of each row
+    int64_t table_stride;
+    int32_t page_size, max_pages;
+    const int32_t* q_offsets;  // [batch + 1]
+    const int32_t* kv_lens;    // [batch]
+    int32_t batch, kv_heads, head_dim;
+    int64_t T;
+    unsigned int* err;
+};
+
+// Cached tokens of sequence b, held to what its row of the page table can name.
+__device__ __forceinline__ int cache_length(const CacheArgs& c, int b) {
+    const int n = __ldg(c.kv_lens + b);
+    const int64_t most = (int64_t)c.max_pages * c.page_size;
+    if (n < 0 || n > most) {
+        raise_device_error(c.err, W4A16_ERR_BAD_CACHE);
+        return n < 0 ? 0 : (int)most;
+    }
+    return n;
+}
+
+// The sequence of token t, or -1 (reported) where the offsets are not a partition of the tokens.
+__device__ __forceinline__ int sequence_of(const CacheArgs& c, int64_t t, int& first, int& count) {
+    int b;
+    if (c.T == c.batch) {
+        b = (int)t;  // one token each, unless a sequence is empty
+        first = __ldg(c.q_offsets + b);
+        count = __ldg(c.q_offsets + b + 1) - first;
+        if (first == t && count == 1) return b;
+    }
+    int lo = 0, hi = c.batch - 1;  // the last b with q_offsets[b] <= t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(c.q_offsets + mid) <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    b = lo;
+    first = __ldg(c.q_offsets + b);
+    const int next = __ldg(c.q_offsets + b + 1);
+    count = next - first;
+    if (first < 0 || t < first || t >= next) {
+        raise_device_error(c.err, W4A16_ERR_BAD_OFFSETS);
+        return -1;
+    }
+    return b;
+}
+
+// Reports offsets that are not 0 = o[0] <= ... <= o[batch] = T; called by all
+// threads of one block of a launch.
+__device__ __forceinline__ void check_offsets(const CacheArgs& c) {
+    bool ok = true;
+    for (int b = threadIdx.x; b < c.batch; b += blockDim.x) {
+        const int o = __ldg(c.q_offsets + b), next = __ldg(c.q_offsets + b + 1);
+        ok = ok && o <= next && (b > 0 || o == 0) && (b < c.batch - 1 || next == c.T);
+    }
+    if (!ok) raise_device_error(c.err, W4A16_ERR_BAD_OFFSETS);
+}
+
+// Page that holds place p of sequence b, or -1 (reported) for an entry outside the cache.
+__device__ __forceinline__ int64_t page_of(const CacheArgs& c, int b, int p) {
+    const int32_t page = __ldg(c.table + b * c.table_stride + p / c.page_size);
+    if (page < 0 || page >= c.pages) {
+        raise_device_error(c.err, W4A16_ERR_BAD_CACHE);
+        return -1;
+    }
+    return page;
+}
+
+// ------------------------------------------------------------------ host --
+
+// Launches a kernel that may start while the one before it on the stream is
+// still running (it waits for that one's results itself, before it reads).
+template <typename... KArgs, typename... Args>
+w4a16_status launch_overlapped(const char* what, void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem,
+                               cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attrs[1];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...), what);
+}
+
+w4a16_status rope_launch(const DeviceInfo& dev, int dtype, const uint16_t* x, int64_t x_row_stride,
+                         int64_t x_head_stride, uint16_t* out, int64_t out_row_stride, int64_t out_head_stride,
+                         int64_t T, int heads, int head_dim, const w4a16_rotary* rotary, cudaStream_t st);
+w4a16_status append_launch(const DeviceInfo& dev, int dtype, const CacheArgs& c, const uint16_t* q,
+                           int64_t q_row_stride, int64_t q_head_stride, int heads, uint16_t* q_out,
+                           const uint16_t* k, int64_t k_row_stride, int64_t k_head_stride, const uint16_t* v,
+                           int64_t v_row_stride, int64_t v_head_stride, const w4a16_rotary* rotary,
+                           cudaStream_t st);
+
+struct AttentionArgs {
+    CacheArgs c;
+    const uint16_t* q;
+    int64_t q_row_stride, q_head_stride;
+    uint16_t* out;  // [T, heads, head_dim]
+    float* lse;     // [T, heads] or nullptr
+    int32_t heads;
+    int32_t causal, window;  // window 0: no lower limit
+    float scale_log2;        // softmax scale times log2(e)
+    int64_t max_q_len;
+};
+
+w4a16_status attention_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, void* workspace,
+                              size_t workspace_bytes, cudaStream_t st);
+size_t attention_workspace_bytes(const DeviceInfo& dev, int64_t T, int batch, int heads, int kv_heads, int head_dim,
+                                 int64_t max_q_len);
+
+}  // namespace w4a16
