@@ -1,7 +1,6 @@
-// Attention of new tokens over a paged cache: out = softmax(scale q k^T) v per
-// row, over the places the row sees, in one pass with the running maximum and
-// sum of the softmax. One warp per (token, query head), the head's elements
-// spread over its lanes.
+// Attention of new tokens over a paged cache: which kernel serves which
+// sequences, and a plain kernel for those of more rows than attention_step.cu
+// takes: one warp per (token, query head), the head's elements spread over its lanes.
 #include "attention.cuh"
 
 namespace w4a16 {
@@ -10,7 +9,7 @@ namespace {
 constexpr int kWarps = 4;
 
 template <class E, int D>
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const __grid_constant__ AttentionArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     if (blockIdx.x == 0) check_offsets(a.c);
@@ -23,6 +22,7 @@ __global__ void __launch_bounds__(kWarps * 32) attention_kernel(const __grid_con
     int first, count;
     const int b = sequence_of(a.c, t, first, count);
     if (b < 0) return;
+    if (count * (a.heads / a.c.kv_heads) < min_rows) return;
     if (count > a.max_q_len) {
         raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
         return;
@@ -75,18 +75,34 @@ __global__ void __launch_bounds__(kWarps * 32) attention_kernel(const __grid_con
 
 }  // namespace
 
-size_t attention_workspace_bytes(const DeviceInfo&, int64_t, int, int, int, int, int64_t) { return 0; }
+size_t attention_workspace_bytes(const DeviceInfo& dev, int64_t T, int batch, int heads, int kv_heads, int head_dim,
+                                 int64_t max_q_len) {
+    return attention_step_workspace_bytes(dev, head_dim);
+}
 
-w4a16_status attention_launch(const DeviceInfo&, int dtype, const AttentionArgs& a, void*, size_t, cudaStream_t st) {
+w4a16_status attention_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, void* workspace,
+                              size_t workspace_bytes, cudaStream_t st) {
+    const int64_t ratio = a.heads / a.c.kv_heads, most = a.max_q_len * ratio;
+    if (workspace_bytes < attention_step_workspace_bytes(dev, a.c.head_dim) || !workspace) return W4A16_ERR_WORKSPACE;
+    // where every sequence has the same number of new tokens, one kernel takes them all
+    const bool alike = a.c.T == a.c.batch * a.max_q_len;
+    const bool step = most <= kStepRows || (ratio <= kStepRows && !alike);
+    const bool rest = most > kStepRows;
+    if (step) {
+        const w4a16_status s =
+            attention_step_launch(dev, dtype, a, (int)(most < kStepRows ? most : kStepRows), workspace, st);
+        if (s != W4A16_OK || !rest) return s;
+    }
     const int64_t blocks = (a.c.T * a.heads + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return W4A16_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks);
     const bool f16 = dtype == W4A16_DTYPE_F16;
+    const int min_rows = step ? kStepRows + 1 : 0;
     if (a.c.head_dim == 64)
         return launch_overlapped("paged_attention", f16 ? attention_kernel<Fp16, 64> : attention_kernel<Bf16, 64>, grid,
-                                 kWarps * 32, 0, st, a);
+                                 kWarps * 32, 0, st, a, min_rows);
     return launch_overlapped("paged_attention", f16 ? attention_kernel<Fp16, 128> : attention_kernel<Bf16, 128>, grid,
-                             kWarps * 32, 0, st, a);
+                             kWarps * 32, 0, st, a, min_rows);
 }
 
 }  // namespace w4a16

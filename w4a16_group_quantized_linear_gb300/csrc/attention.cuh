@@ -152,6 +152,22 @@ struct AttentionArgs {
     int64_t max_q_len;
 };
 
+// 2^x of the special-function unit (2 ulp), results below the normal range to zero.
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr size_t align_up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Sequences of up to kStepRows rows per cached head (attention_step.cu). max_rows
+// is at least the rows of each of these sequences.
+constexpr int kStepRows = 16;
+w4a16_status attention_step_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, int max_rows,
+                                   void* workspace, cudaStream_t st);
+size_t attention_step_workspace_bytes(const DeviceInfo& dev, int head_dim);
+
 w4a16_status attention_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, void* workspace,
                               size_t workspace_bytes, cudaStream_t st);
 size_t attention_workspace_bytes(const DeviceInfo& dev, int64_t T, int batch, int heads, int kv_heads, int head_dim,
