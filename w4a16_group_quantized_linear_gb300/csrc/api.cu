@@ -343,16 +343,18 @@ W4A16_API w4a16_status w4a16_test_set_hooks(uint64_t wait_limit_ns, int32_t issu
     w4a16_status a = cuda_status(gemv_set_test_hooks(h), "test hooks (gemv)");
     if (a == W4A16_OK) a = cuda_status(gemm_set_test_hooks(h), "test hooks (gemm)");
     if (a == W4A16_OK) a = cuda_status(split_set_test_hooks(h), "test hooks (gemm g32)");
+    if (a == W4A16_OK) a = cuda_status(attention_set_test_hooks(h), "test hooks (attention)");
     return a;
 }
 
 W4A16_API w4a16_status w4a16_test_tmem_counters(uint64_t* allocs, uint64_t* frees) {
-    TestCounters c{}, d{};
+    TestCounters c{}, d{}, e{};
     w4a16_status a = cuda_status(gemm_get_test_counters(&c), "test counters");
     if (a == W4A16_OK) a = cuda_status(split_get_test_counters(&d), "test counters (gemm g32)");
+    if (a == W4A16_OK) a = cuda_status(attention_get_test_counters(&e), "test counters (attention)");
     if (a != W4A16_OK) return a;
-    *allocs = c.tmem_allocs + d.tmem_allocs;
-    *frees = c.tmem_frees + d.tmem_frees;
+    *allocs = c.tmem_allocs + d.tmem_allocs + e.tmem_allocs;
+    *frees = c.tmem_frees + d.tmem_frees + e.tmem_frees;
     return W4A16_OK;
 }
 #endif

@@ -159,6 +159,16 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// Equal runs of a work list over the thread blocks: the first `more` take base + 1 units.
+struct Shares {
+    int64_t base, more;
+    __device__ __forceinline__ int64_t start(int64_t c) const { return c * base + min(c, more); }
+    __device__ __forceinline__ int64_t owner(int64_t unit) const {
+        const int64_t cut = more * (base + 1);
+        return unit < cut ? unit / (base + 1) : more + (unit - cut) / base;
+    }
+};
+
 constexpr size_t align_up(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Sequences of up to kStepRows rows per cached head (attention_step.cu). max_rows
@@ -167,6 +177,11 @@ constexpr int kStepRows = 16;
 w4a16_status attention_step_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, int max_rows,
                                    void* workspace, cudaStream_t st);
 size_t attention_step_workspace_bytes(const DeviceInfo& dev, int head_dim);
+
+// Sequences of at least min_rows rows per cached head (attention_tile.cu).
+w4a16_status attention_tile_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, int min_rows,
+                                   void* workspace, cudaStream_t st);
+size_t attention_tile_workspace_bytes(const DeviceInfo& dev, int head_dim);
 
 w4a16_status attention_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, void* workspace,
                               size_t workspace_bytes, cudaStream_t st);

@@ -125,16 +125,6 @@ __device__ __forceinline__ void load_sequence(const AttentionArgs& a, int b, int
     s.blocks = max(1, (s.length + kBlock - 1) / kBlock - s.block);
 }
 
-// Where the work list's units go: the first `more` thread blocks take base + 1 of them.
-struct Shares {
-    int64_t base, more;
-    __device__ __forceinline__ int64_t start(int64_t c) const { return c * base + min(c, more); }
-    __device__ __forceinline__ int64_t owner(int64_t unit) const {
-        const int64_t cut = more * (base + 1);
-        return unit < cut ? unit / (base + 1) : more + (unit - cut) / base;
-    }
-};
-
 // A position in the work list, as a warp walks it.
 struct Cursor {
     int b, g, block, end;  // block of the sequence, and one past the item's last
