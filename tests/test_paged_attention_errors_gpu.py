@@ -43,8 +43,9 @@ def _tmem(lib):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("lens", [[(300, 2000)], [(40, 9000)], [(200, 200), (100, 700)]])
-def test_wait_times_out_and_next_call_is_correct(hooks, cuda_device, lens, D):
+@pytest.mark.parametrize("lens,limits", [([(300, 4000)], (0, 1, 2, 3)), ([(40, 30000)], (0, 1, 2, 3)),
+                                         ([(200, 200), (100, 700)], (0, 1))])   # a block for each SM at most
+def test_wait_times_out_and_next_call_is_correct(hooks, cuda_device, lens, limits, D):
     import torch
 
     import w4a16_group_quantized_linear_gb300 as w4
@@ -63,7 +64,7 @@ def test_wait_times_out_and_next_call_is_correct(hooks, cuda_device, lens, D):
         return lib.w4a16_paged_attention(ctypes.byref(c), T, w4._ptr(b.q), b.q.stride(0), b.q.stride(1), 10, b.max_q,
                                          1, 0, D ** -0.5, w4._ptr(out), None, w4._ptr(ws), n, st)
 
-    for issue_limit in (0, 1, 2, 3):   # nothing; k; k and v; the next k
+    for issue_limit in limits:   # nothing; k; k and v; the next k
         a0, f0 = _tmem(lib)
         assert lib.w4a16_test_set_hooks(SHORT_NS, issue_limit) == 0
         assert call() == 0
