@@ -23,10 +23,14 @@
 //                   it is in work, and writes the result.
 //   warp 8          TMA: k and v blocks into a ring of shared memory, one box per page piece and
 //                   64 elements. Pages that hold nothing to see are not read:
-//                   a box outside the cache reads as zeros.
-//   warp 9          MMA issue (warps 10 and 11 only fill the warpgroup): p v of block j, then q k of block j + 1, for one half
-//                   and then the other. Slots past a sequence's last place are zeroed in
-//                   the v block first (0 times whatever they hold might not be 0).
+//                   a box outside the cache reads as zeros. Slots past a
+//                   sequence's last place are zeroed in the v block (0 times
+//                   whatever they hold might not be 0).
+//   warp 9          MMA issue: p v of block j, then q k of block j + 1, for one half
+//                   and then the other.
+//   warp 10         lays out the work: each tile's rows, blocks and sharers, a few tiles
+//                   ahead, so that the others keep none of it in registers (warp 11 only
+//                   fills the warpgroup).
 //
 // TMEM: scores (and p) of the halves in columns [0, 128) and [128, 256), o in
 // [256, 256 + D) and [256 + D, 256 + 2 D).
@@ -51,9 +55,10 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;      // places per block: MMA N of the scores, K of the output
 constexpr int kThreads = 384;
 // Registers: a launch of 384 threads has 168 each; the two softmax warpgroups
-// hold a row of 128 scores a thread and take 216, the third keeps 72 (2 * 216 + 72 = 3 * 168).
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+// hold a row of 128 scores a thread and take 208, the third keeps 88 (2 * 208 + 88 = 3 * 168).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
+constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutCol = 256;
 constexpr float kSlack = 8.0f;   // how far a score may pass the running maximum (log2)
@@ -85,15 +90,30 @@ struct Layout {
 
 constexpr int kMaxStages = 12;
 
+// A tile, or a stretch of its blocks, for the warps to work on.
+struct Entry {
+    int b, g, first, count, length;
+    int low;                   // first place that any row of the tile sees
+    int from, to;              // blocks
+    int begin[2], end[2];      // of them, those that the halves see
+    int c0, c1;                // the thread blocks that share the tile
+    int last;
+    int64_t row;               // first row of the tile
+};
+
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];  // ring
+    uint64_t v_clean;     // a v block's slots past the sequence's last place are zero
     uint64_t q_full[2];   // a half's queries are in shared memory
     uint64_t s_full[2];   // a half's scores are in TMEM (and its o is up to date)
-    uint64_t p_full[2];   // a half's p is in TMEM
+    uint64_t p_part[2];   // the first 64 columns of a half's p are in TMEM
+    uint64_t p_full[2];   // and all of it
     uint64_t o_done[2];   // a half's o is complete for the tile
     uint64_t part_in[2];  // a half's threads have written their part
     uint64_t part_out[2]; // whether it was the last of its tile is known
+    uint64_t work_full[kEntries], work_empty[kEntries];
     uint64_t mma_done;
+    Entry work[kEntries];
     uint32_t tmem;
     int abort;
     int last[2];
@@ -156,8 +176,6 @@ struct Segment {
     int from, to;         // the stretch
     __device__ __forceinline__ int begin_of(int w) const { return max(w ? half1.block : half0.block, from); }
     __device__ __forceinline__ int end_of(int w) const { return min(w ? half1.end : half0.end, to); }
-    __device__ __forceinline__ bool active(int w, int j) const { return j >= begin_of(w) && j < end_of(w); }
-    __device__ __forceinline__ int count_of(int w) const { return max(0, end_of(w) - begin_of(w)); }
 };
 
 __device__ __forceinline__ void set_tile(const AttentionArgs& a, Segment& s) {
@@ -199,6 +217,22 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// Waits for the phase with the given parity, as ptx::mbar_wait does, but looks
+// at the clock and the abort flag only every 32 polls: a read of the timer
+// takes longer than a warp's share of a block may.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    uint64_t since = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        const uint64_t now = ptx::globaltimer_ns();
+        if (since == 0) since = now;
+        else if (now - since > limit_ns) return false;
+    }
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -207,6 +241,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// Slots of a block's last page piece that are past the sequence's `past` places in the block.
+__device__ __forceinline__ int tail_rows(int past, int box) {
+    return past > 0 && past < kBlock ? (box - (past & (box - 1))) & (box - 1) : 0;  // box: a power of two
 }
 
 // v block as the B operand of p v: 64-element slabs of 128-byte rows, a row per
@@ -225,6 +264,14 @@ template <class E>
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major) {
     const uint32_t type = E::kDtype == W4A16_DTYPE_BF16 ? 1u : 0u;
     return ptx::idesc_f16_f32(kHalf, n) | (type << 7) | (type << 10) | ((b_n_major ? 1u : 0u) << 16);
+}
+
+// One lane of a converged warp, always the same one: true for it alone. (With a
+// lane chosen by comparison the issue of one MMA took 115 cycles, not 64.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -382,11 +429,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < 2; ++w) {
                 ptx::mbar_init(&bars->q_full[w], kHalf);
                 ptx::mbar_init(&bars->s_full[w], 1);
+                ptx::mbar_init(&bars->p_part[w], kHalf / 32);
                 ptx::mbar_init(&bars->p_full[w], kHalf / 32);
                 ptx::mbar_init(&bars->o_done[w], 1);
                 ptx::mbar_init(&bars->part_in[w], kHalf);
                 ptx::mbar_init(&bars->part_out[w], 1);
             }
+            for (int i = 0; i < kEntries; ++i) {
+                ptx::mbar_init(&bars->work_full[i], 1);
+                ptx::mbar_init(&bars->work_empty[i], 10);  // load, MMA and softmax warps
+            }
+            ptx::mbar_init(&bars->v_clean, 1);
             ptx::mbar_init(&bars->mma_done, 1);
             bars->abort = 0;
             ptx::fence_mbar_init();
@@ -404,153 +457,272 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem;
     volatile int* abort = &bars->abort;
-    int64_t left = run.end - run.begin;  // units of this run from the segment on
     bool ok = true;
+    // entry k of the work, for this warp to read; false if it gave up
+    auto entry = [&](int k) {
+        if (ok && !wait_bar(&bars->work_full[k % kEntries], (k / kEntries) & 1, abort, wait_limit())) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+    };
+    auto done_with = [&](int k) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
+    };
 
     if (warp >= kLoadWarp) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-      if (warp == kLoadWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    }
+    if (warp == kPlanWarp) {
+        // -------------------------------------------------------------- plan
+        int64_t left = run.end - run.begin, unit = run.begin;
+        for (int k = 0; ok; ++k) {
+            if (k >= kEntries &&
+                !wait_bar(&bars->work_empty[k % kEntries], (k / kEntries - 1) & 1, abort, wait_limit()))
+                ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int n = seg.to - seg.from;
+            if (lane == 0) {
+                Entry& e = bars->work[k % kEntries];
+                e.b = seg.b;
+                e.g = seg.g;
+                e.row = (int64_t)seg.tile * kTile;
+                e.first = seg.s.first;
+                e.count = seg.s.count;
+                e.length = seg.s.length;
+                e.low = seg.low;
+                e.from = seg.from;
+                e.to = seg.to;
+                e.begin[0] = seg.begin_of(0);
+                e.begin[1] = seg.begin_of(1);
+                e.end[0] = max(e.begin[0], seg.end_of(0));
+                e.end[1] = max(e.begin[1], seg.end_of(1));
+                const int64_t item = unit - (seg.from - seg.block);
+                e.c0 = (int)run.shares.owner(item);
+                e.c1 = (int)run.shares.owner(item + (seg.end - seg.block) - 1);
+                e.last = left == n;
+                ptx::mbar_arrive(&bars->work_full[k % kEntries]);
+            }
+            left -= n;
+            unit += n;
+            if (left == 0) break;
+            next_segment(x, left, seg);
+        }
+        if (!ok && lane == 0) fail(x, bars);
+    } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------- loads
         const int pieces = kBlock / x.box;
         const int piece = lane / L::kSlabs, slab = lane % L::kSlabs;
         int issued = 0;
-        while (ok) {
-            for (int j = seg.from; ok && j < seg.to; ++j) {
+        // v block `dirty` (its number in the ring's order; -1: none): slots past
+        // the last place are zeroed once it is there, as 0 times what they hold might not be 0
+        int dirty = -1, dirty_row = 0, dirty_rows = 0;
+        auto clean = [&] {
+            const int st = dirty % L::kStages;
+            ok = ok && wait_bar(&bars->full[st], (dirty / L::kStages) & 1, abort, wait_limit());
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                for (int c = lane; c < dirty_rows * (D / 8); c += 32) {
+                    const int row = dirty_row + c / (D / 8), part = c % (D / 8);
+                    *reinterpret_cast<uint4*>(ring + st * L::kStageBytes + (part >> 3) * L::kSlabBytes + row * 128 +
+                                              (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bars->v_clean);
+            }
+            dirty = -1;
+        };
+        for (int k = 0; entry(k); ++k) {
+            const Entry& e = bars->work[k % kEntries];
+            const int to = e.to, length = e.length, low = e.low, b = e.b, g = e.g;
+            for (int j = e.from; ok && j < to; ++j) {
                 const int p = j * kBlock + piece * x.box;
                 int64_t page = a.c.pages;  // outside the cache: zeros
-                if (piece < pieces && p < seg.s.length && p + x.box > seg.low) {
-                    page = page_of(a.c, seg.b, p);
+                if (piece < pieces && p < length && p + x.box > low) {
+                    page = page_of(a.c, b, p);
                     if (page < 0) page = a.c.pages;
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const int st = issued % L::kStages, round = issued / L::kStages;
-                    ok = may_issue(issued) &&
-                         (round == 0 || ptx::mbar_wait(&bars->empty[st], (round - 1) & 1, abort, wait_limit()));
+                    if (dirty >= 0 && round > 0 &&
+                        !__all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->empty[st], (round - 1) & 1)))
+                        clean();
+                    ok = ok && may_issue(issued) &&
+                         (round == 0 || wait_bar(&bars->empty[st], (round - 1) & 1, abort, wait_limit()));
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->full[st], L::kStageBytes);
                     __syncwarp();
                     if (piece < pieces)
                         tma_load_4d(ring + st * L::kStageBytes + slab * L::kSlabBytes + piece * x.box * 128,
-                                    kv ? &map_v : &map_k, &bars->full[st], slab * 64, p % a.c.page_size, seg.g,
+                                    kv ? &map_v : &map_k, &bars->full[st], slab * 64, p % a.c.page_size, g,
                                     (int)page);
                     ++issued;
                 }
+                const int past = length - j * kBlock, rows = tail_rows(past, x.box);
+                if (ok && rows > 0) {
+                    if (dirty >= 0) clean();
+                    dirty = issued - 1;
+                    dirty_row = past;
+                    dirty_rows = rows;
+                }
             }
-            left -= seg.to - seg.from;
-            if (!ok || left == 0) break;
-            next_segment(x, left, seg);
+            const bool last = e.last;
+            done_with(k);
+            if (!ok || last) break;
         }
+        if (ok && dirty >= 0) clean();
         if (!ok && lane == 0) {
             fail(x, bars);
             volatile int never = 0;  // our own copies land before the thread block ends
             for (int i = max(0, issued - L::kStages); i < issued; ++i)
-                ptx::mbar_wait(&bars->full[i % L::kStages], (i / L::kStages) & 1, &never, kDrainLimitNs);
+                wait_bar(&bars->full[i % L::kStages], (i / L::kStages) & 1, &never, kDrainLimitNs);
         }
         __syncwarp();
-      } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp) {
         // --------------------------------------------------------------- MMA
+        // One thread. The tensor core's queue holds about 200 cycles of products, so what
+        // this thread does between two of them is kept below that: everything about the block
+        // after next is worked out in the middle of a round, not at its turn.
         constexpr uint32_t kIdescS = idesc<E>(kBlock, false), kIdescO = idesc<E>(D, true);
-        const uint32_t smem_u = ptx::smem_u32(smem), ring_u = ptx::smem_u32(ring);
-        int used = 0;                  // ring stages taken
-        int nq[2] = {0, 0}, np[2] = {0, 0};
-        auto wait = [&](uint64_t* bar, int n) {  // for its n-th completion, from 0
-            if (ok && !ptx::mbar_wait(bar, n & 1, abort, wait_limit())) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            ptx::tc_fence_after();
-            return ok;
-        };
-        auto scores = [&](int w, int st) {
-            if (lane == 0) {
-                const uint64_t q = ptx::smem_desc_sw128(smem_u + w * L::kStageBytes);
-                const uint64_t k = ptx::smem_desc_sw128(ring_u + st * L::kStageBytes);
+        if (elect_one()) {
+            const uint32_t ring_u = ptx::smem_u32(ring);
+            const uint64_t q_desc = ptx::smem_desc_sw128(ptx::smem_u32(smem));
+            const uint64_t k_desc = ptx::smem_desc_sw128(ring_u), v_desc = desc_v(ring_u, L::kSlabBytes);
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (!ptx::mbar_try_wait(bar, parity) && !wait_bar(bar, parity, abort, wait_limit())) ok = false;
+                ptx::tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int w, uint32_t st) {
+                const uint64_t q = q_desc + (uint64_t)(w * (L::kStageBytes >> 4));
+                const uint64_t k = k_desc + (uint64_t)(st * (L::kStageBytes >> 4));
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint64_t at = (uint64_t)(((ks >> 2) * L::kSlabBytes + (ks & 3) * 32) >> 4);
                     mma_ss(tmem + w * kBlock, q + at, k + at, kIdescS, ks > 0);
                 }
                 ptx::mma_commit(&bars->s_full[w]);
-            }
-            __syncwarp();
-        };
-        auto output = [&](int w, int st, bool first, bool last) {
-            if (lane == 0) {
-                const uint64_t v = desc_v(ring_u + st * L::kStageBytes, L::kSlabBytes);
+            };
+            // p v; where p is not complete yet, the first half of the contraction goes ahead
+            auto output = [&](int w, uint32_t st, uint32_t parity, bool first, bool last) {
+                const uint64_t v = v_desc + (uint64_t)(st * (L::kStageBytes >> 4));
+                const uint32_t o = tmem + kOutCol + w * D, p = tmem + w * kBlock;
+                if (!wait(&bars->p_part[w], parity)) return false;
+                ptx::mma_f16_ts(o, p, v, kIdescO, !first);
 #pragma unroll
-                for (int kk = 0; kk < kBlock / 16; ++kk)
-                    ptx::mma_f16_ts(tmem + kOutCol + w * D, tmem + w * kBlock + kk * 8, v + (uint64_t)((kk * 2048) >> 4),
-                                    kIdescO, !first || kk > 0);
+                for (int kk = 1; kk < kBlock / 32; ++kk)
+                    ptx::mma_f16_ts(o, p + kk * 8, v + (uint64_t)((kk * 2048) >> 4), kIdescO, 1u);
+                if (!wait(&bars->p_full[w], parity)) return false;
+#pragma unroll
+                for (int kk = kBlock / 32; kk < kBlock / 16; ++kk)
+                    ptx::mma_f16_ts(o, p + kk * 8, v + (uint64_t)((kk * 2048) >> 4), kIdescO, 1u);
                 if (last) ptx::mma_commit(&bars->o_done[w]);
+                return true;
+            };
+            // what a block needs of its entry
+            struct View {
+                int to, length, begin0, end0, begin1, end1, last;
+            };
+            auto view = [&](int k) {
+                const Entry& e = bars->work[k % kEntries];
+                return View{e.to, e.length, e.begin[0], e.end[0], e.begin[1], e.end[1], e.last};
+            };
+            auto advance = [](uint32_t& st, uint32_t& parity) {
+                if (++st == L::kStages) {
+                    st = 0;
+                    parity ^= 1u;
+                }
+            };
+            int k = 0;                                // entry of the block whose p v comes next
+            int j = 0, i = 0;                         // that block, and the one whose scores come next
+            uint32_t vst = 0, vparity = 0, kst = 0, kparity = 0;  // their ring stages
+            uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0, clean_parity = 0;
+            bool turn = false, more = true;           // the two are of different entries; there is a second one
+            View cur{}, nxt{};
+            auto plan = [&] {
+                vst = kst;
+                vparity = kparity;
+                advance(vst, vparity);
+                kst = vst;
+                kparity = vparity;
+                advance(kst, kparity);
+                i = j + 1;
+                turn = i == cur.to;
+                more = !turn || !cur.last;
+                if (turn && more && wait(&bars->work_full[(k + 1) % kEntries], ((k + 1) / kEntries) & 1)) {
+                    nxt = view(k + 1);
+                    i = bars->work[(k + 1) % kEntries].from;
+                }
+            };
+            if (wait(&bars->work_full[0], 0)) {  // the first block's scores
+                cur = nxt = view(0);
+                j = bars->work[0].from;
+                wait(&bars->full[0], 0);
+                if (ok && j >= cur.begin0 && j < cur.end0 && wait(&bars->q_full[0], 0)) {
+                    scores(0, 0);
+                    q_parity0 = 1;
+                }
+                if (ok && j >= cur.begin1 && j < cur.end1 && wait(&bars->q_full[1], 0)) {
+                    scores(1, 0);
+                    q_parity1 = 1;
+                }
+                ptx::mma_commit(&bars->empty[0]);
+                plan();
             }
-            __syncwarp();
-        };
-        // the first block's scores
-        int j = seg.from;
-        wait(&bars->full[0], 0);
-        used = 1;
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-            if (ok && seg.active(w, j) && wait(&bars->q_full[w], nq[w]++)) scores(w, 0);
-        if (lane == 0) ptx::mma_commit(&bars->empty[0]);
-        Segment nxt = seg;
-        while (ok) {
-            // block j of seg, and the block after it: block i of nxt
-            int i = j + 1;
-            bool more = true;
-            const bool turn = i == seg.to;
-            if (turn) {
-                left -= seg.to - seg.from;
-                more = left > 0;
+            while (ok) {
+                if (!wait(&bars->full[vst], vparity)) break;
+                if (tail_rows(cur.length - j * kBlock, x.box) > 0) {
+                    if (!wait(&bars->v_clean, clean_parity)) break;
+                    clean_parity ^= 1u;
+                }
+                if (j >= cur.begin0 && j < cur.end0) {
+                    if (!output(0, vst, p_parity0, j == cur.begin0, j == cur.end0 - 1)) break;
+                    p_parity0 ^= 1u;
+                }
                 if (more) {
-                    next_segment(x, left, nxt);
-                    i = nxt.from;
+                    if (!wait(&bars->full[kst], kparity)) break;
+                    if (i >= nxt.begin0 && i < nxt.end0) {
+                        if (i == nxt.begin0) {
+                            if (!wait(&bars->q_full[0], q_parity0)) break;
+                            q_parity0 ^= 1u;
+                        }
+                        scores(0, kst);
+                    }
                 }
-            }
-            const int vst = used % L::kStages, vround = used / L::kStages;
-            const int kst = (used + 1) % L::kStages, kround = (used + 1) / L::kStages;
-            wait(&bars->full[vst], vround);
-            // slots past the last place, in a page that holds it
-            const int past = seg.s.length - j * kBlock;
-            if (ok && past > 0 && past < kBlock && past % x.box != 0) {
-                const int upto = (past + x.box - 1) / x.box * x.box;
-                for (int k = lane; k < (upto - past) * (D / 8); k += 32) {
-                    const int row = past + k / (D / 8), piece = k % (D / 8);
-                    *reinterpret_cast<uint4*>(ring + vst * L::kStageBytes + (piece >> 3) * L::kSlabBytes + row * 128 +
-                                              (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
+                if (j >= cur.begin1 && j < cur.end1) {
+                    if (!output(1, vst, p_parity1, j == cur.begin1, j == cur.end1 - 1)) break;
+                    p_parity1 ^= 1u;
                 }
-                ptx::fence_proxy_async_shared();
-                __syncwarp();
-            }
-            bool k_ready = false;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                if (ok && seg.active(w, j) && wait(&bars->p_full[w], np[w]++))
-                    output(w, vst, j == seg.begin_of(w), j == seg.end_of(w) - 1);
-                if (w == 1 && lane == 0) ptx::mma_commit(&bars->empty[vst]);
-                if (more && !k_ready) {
-                    wait(&bars->full[kst], kround);
-                    k_ready = true;
+                ptx::mma_commit(&bars->empty[vst]);
+                if (!more) break;
+                // the round after this one, while the products above are queued
+                const bool second = i >= nxt.begin1 && i < nxt.end1;
+                if (second && i == nxt.begin1) {
+                    if (!wait(&bars->q_full[1], q_parity1)) break;
+                    q_parity1 ^= 1u;
                 }
-                if (ok && more && nxt.active(w, i) &&
-                    (i != nxt.begin_of(w) || wait(&bars->q_full[w], nq[w]++)))
-                    scores(w, kst);
+                const uint32_t st = kst;
+                if (turn) {
+                    ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
+                    ++k;
+                    cur = nxt;
+                }
+                j = i;
+                plan();
+                if (!ok) break;
+                if (second) scores(1, st);
+                ptx::mma_commit(&bars->empty[st]);
             }
-            if (more && lane == 0) ptx::mma_commit(&bars->empty[kst]);
-            used += 2;
-            if (!more) break;
-            if (turn) seg = nxt;
-            j = i;
-        }
-        if (lane == 0) {
             if (!ok) fail(x, bars);
             ptx::mma_commit(&bars->mma_done);
             volatile int never = 0;
-            ptx::mbar_wait(&bars->mma_done, 0, &never, kDrainLimitNs);
+            wait_bar(&bars->mma_done, 0, &never, kDrainLimitNs);
         }
         __syncwarp();
-      }
-    } else {
+    } else if (warp < kLoadWarp) {
         // ----------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int w = warp >> 2;
@@ -559,18 +731,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_addr = lane_base + w * kBlock, o_addr = lane_base + kOutCol + w * D;
         const uint32_t q_smem = ptx::smem_u32(smem) + w * L::kStageBytes;
         int ns = 0, no = 0, nj = 0;
-        // this half's queries of a tile, 16 bytes a lane; rows past the sequence's are zeros
-        auto load_q = [&](const Segment& s) {
+        // this half's queries of an entry, 16 bytes a lane; rows past the sequence's are zeros
+        auto load_q = [&](const Entry& e) {
             constexpr int kPieces = D / 8, kRowsPer = 32 / kPieces;
             const int piece = lane % kPieces;
 #pragma unroll 4
             for (int i = 0; i < 32 / kRowsPer; ++i) {
                 const int r = (warp & 3) * 32 + i * kRowsPer + lane / kPieces;
-                const int64_t at = (int64_t)s.tile * kTile + w * kHalf + r;
+                const int64_t at = e.row + w * kHalf + r;
                 const int64_t token = at / ratio;
-                const bool real = token < s.s.count;
-                const uint16_t* src = a.q + (real ? (s.s.first + token) * a.q_row_stride +
-                                                        (s.g * ratio + at % ratio) * a.q_head_stride + piece * 8
+                const bool real = token < e.count;
+                const uint16_t* src = a.q + (real ? (e.first + token) * a.q_row_stride +
+                                                        (e.g * ratio + at % ratio) * a.q_head_stride + piece * 8
                                                   : 0);
                 ptx::cp_async_16(q_smem + (piece >> 3) * L::kSlabBytes + r * 128 + (((piece & 7) ^ (r & 7)) << 4), src,
                                  real ? 16u : 0u);
@@ -581,41 +753,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::fence_proxy_async_shared();
             ptx::mbar_arrive(&bars->q_full[w]);
         };
-        if (seg.count_of(w) > 0) {
-            load_q(seg);
+        if (entry(0) && bars->work[0].end[w] > bars->work[0].begin[w]) {
+            load_q(bars->work[0]);
             q_ready();
         }
-        int64_t unit = run.begin;  // of the segment's first block
-        while (true) {
-            const int begin = seg.begin_of(w), n = seg.count_of(w);
-            left -= seg.to - seg.from;
-            Segment nxt = seg;
-            if (left > 0) next_segment(x, left, nxt);
-            const bool load_next = left > 0 && nxt.count_of(w) > 0;
-            const int64_t at = (int64_t)seg.tile * kTile + w * kHalf + row;
-            const int64_t token = at / ratio;
-            const bool real = token < seg.s.count;
-            const int place = seg.s.length - seg.s.count + (int)token;
-            const int low = a.window > 0 ? max(0, place - a.window + 1) : 0;
-            const int high = !real ? 0 : a.causal ? min(seg.s.length, place + 1) : seg.s.length;
+        for (int k = 0; ok; ++k) {
+            const Entry& e = bars->work[k % kEntries];
+            const Entry& next = bars->work[(k + 1) % kEntries];
+            const bool last = e.last;
+            const int begin = e.begin[w], end = e.end[w];
+            int low, high;
+            {
+                const int64_t token = (e.row + w * kHalf + row) / ratio;
+                const int place = e.length - e.count + (int)token;
+                low = a.window > 0 ? max(0, place - a.window + 1) : 0;
+                high = token >= e.count ? 0 : a.causal ? min(e.length, place + 1) : e.length;
+            }
+            bool load_next = false;
             float m = -INFINITY;
             float2 sum = make_float2(0.0f, 0.0f);
-            for (int j = begin; j < begin + n; ++j) {
-                if (!ptx::mbar_wait(&bars->s_full[w], ns & 1, abort, wait_limit())) ok = false;
+            for (int j = begin; j < end; ++j) {
+                if (!wait_bar(&bars->s_full[w], ns & 1, abort, wait_limit())) ok = false;
                 ++ns;
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 ptx::tc_fence_after();
-                if (j == begin + n - 1 && load_next) load_q(nxt);  // the last scores are formed: q may go
+                if (j == end - 1 && !last) {  // the last scores are formed: q may go
+                    if (!entry(k + 1)) break;
+                    load_next = next.end[w] > next.begin[w];
+                    if (load_next) load_q(next);
+                }
                 uint32_t s[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_addr + c * 32, s[c]);
                 ptx::tmem_ld_wait();
-                const int p0 = j * kBlock;
-                if (__any_sync(0xffffffffu, low > p0 || high < p0 + kBlock)) {
-                    const int lo = low - p0, hi = high - p0;
+                const int lo = low - j * kBlock, hi = high - j * kBlock;
+                if (__any_sync(0xffffffffu, lo > 0 || hi < kBlock)) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -657,39 +830,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float2 e = fma2(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), c2,
+                        float2 v = fma2(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), c2,
                                         m2);
-                        e.x = fast_exp2(e.x);
-                        e.y = fast_exp2(e.y);
-                        sum = add2(sum, e);
-                        p[i] = E::pack(e.x, e.y);
+                        v.x = fast_exp2(v.x);
+                        v.y = fast_exp2(v.y);
+                        sum = add2(sum, v);
+                        p[i] = E::pack(v.x, v.y);
                     }
                     ptx::tmem_st_32x32b_x16(s_addr + c * 16, p);
+                    if (c & 1) {
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(c == 1 ? &bars->p_part[w] : &bars->p_full[w]);
+                    }
                 }
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->p_full[w]);
             }
             if (!ok) break;
-            if (load_next) {
-                if (n == 0) load_q(nxt);
-                q_ready();
+            if (begin == end && !last) {
+                if (!entry(k + 1)) break;
+                load_next = next.end[w] > next.begin[w];
+                if (load_next) load_q(next);
             }
+            if (load_next) q_ready();
             // ---- the tile's result, or this thread block's part of it
-            if (n > 0) {
-                if (!ptx::mbar_wait(&bars->o_done[w], no & 1, abort, wait_limit())) ok = false;
+            if (end > begin) {
+                if (!wait_bar(&bars->o_done[w], no & 1, abort, wait_limit())) ok = false;
                 ++no;
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 ptx::tc_fence_after();
             }
-            float l = sum.x + sum.y;
-            const int64_t item = unit - (seg.from - seg.block);
-            const int64_t c0 = run.shares.owner(item), c1 = run.shares.owner(item + (seg.end - seg.block) - 1);
-            const int64_t out_row = (seg.s.first + token) * a.heads + seg.g * ratio + at % ratio;
+            const float l = sum.x + sum.y;
+            const int64_t at = e.row + w * kHalf + row;
+            const int64_t token = at / ratio;
+            const bool real = token < e.count;
+            const int64_t out_row = (e.first + token) * a.heads + e.g * ratio + at % ratio;
+            const int c0 = e.c0, c1 = e.c1;
             auto write32 = [&](int d, const float (&v)[32], float scale) {
                 uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + d);
 #pragma unroll
@@ -702,18 +879,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto write_lse = [&](float top, float total) {
                 if (a.lse) a.lse[out_row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
             };
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (c0 == blockIdx.x ? 1 : 0);
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x ? 1 : 0);
             const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
                 uint32_t r[32];
                 float v[32];
-                if (n > 0) {
+                if (end > begin) {
                     ptx::tmem_ld_32x32b_x32(o_addr + d, r);
                     ptx::tmem_ld_wait();
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = n > 0 ? __uint_as_float(r[i]) : 0.0f;
+                for (int i = 0; i < 32; ++i) v[i] = end > begin ? __uint_as_float(r[i]) : 0.0f;
                 if (c0 == c1) {
                     if (real) write32(d, v, inv);
                 } else {
@@ -729,19 +906,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __stcg(x.stats + slot * kTile + w * kHalf + row, make_float2(m, l));
                 __threadfence();
                 ptx::mbar_arrive(&bars->part_in[w]);
-                if (row == 0 && ptx::mbar_wait(&bars->part_in[w], nj & 1, abort, wait_limit())) {
+                if (row == 0 && wait_bar(&bars->part_in[w], nj & 1, abort, wait_limit())) {
                     const int done = ptx::atom_add_acq_rel_gpu(x.counters + 2 * c0 + w, 1);
-                    bars->last[w] = done == (int)(c1 - c0);
+                    bars->last[w] = done == c1 - c0;
                     if (bars->last[w]) x.counters[2 * c0 + w] = 0;
                     ptx::mbar_arrive(&bars->part_out[w]);
                 }
                 __syncwarp();
-                if (!ptx::mbar_wait(&bars->part_out[w], nj & 1, abort, wait_limit())) ok = false;
+                if (!wait_bar(&bars->part_out[w], nj & 1, abort, wait_limit())) ok = false;
                 ++nj;
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 if (bars->last[w]) {
                     __threadfence();
                     const float2* st = x.stats + w * kHalf + row;
@@ -770,9 +945,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (real) write_lse(top, total);
                 }
             }
-            if (left == 0) break;
-            unit += seg.to - seg.from;
-            seg = nxt;
+            done_with(k);
+            if (last) break;
         }
         ptx::cp_async_wait_all();
     }
