@@ -103,7 +103,7 @@ struct Entry {
 
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];  // ring
-    uint64_t v_clean;     // a v block's slots past the sequence's last place are zero
+    uint64_t v_clean[kMaxStages];  // the slots past the last place of the v block in a stage are zero
     uint64_t q_full[2];   // a half's queries are in shared memory
     uint64_t s_full[2];   // a half's scores are in TMEM (and its o is up to date)
     uint64_t p_part[2];   // the first 64 columns of a half's p are in TMEM
@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < L::kStages; ++i) {
                 ptx::mbar_init(&bars->full[i], 1);
                 ptx::mbar_init(&bars->empty[i], 1);
+                ptx::mbar_init(&bars->v_clean[i], 1);
             }
             for (int w = 0; w < 2; ++w) {
                 ptx::mbar_init(&bars->q_full[w], kHalf);
@@ -439,7 +440,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_init(&bars->work_full[i], 1);
                 ptx::mbar_init(&bars->work_empty[i], 10);  // load, MMA and softmax warps
             }
-            ptx::mbar_init(&bars->v_clean, 1);
             ptx::mbar_init(&bars->mma_done, 1);
             bars->abort = 0;
             ptx::fence_mbar_init();
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::fence_proxy_async_shared();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->v_clean);
+                if (lane == 0) ptx::mbar_arrive(&bars->v_clean[st]);
             }
             dirty = -1;
         };
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int k = 0;                                // entry of the block whose p v comes next
             int j = 0, i = 0;                         // that block, and the one whose scores come next
             uint32_t vst = 0, vparity = 0, kst = 0, kparity = 0;  // their ring stages
-            uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0, clean_parity = 0;
+            uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0, clean_parities = 0;
             bool turn = false, more = true;           // the two are of different entries; there is a second one
             View cur{}, nxt{};
             auto plan = [&] {
@@ -675,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok) {
                 if (!wait(&bars->full[vst], vparity)) break;
                 if (tail_rows(cur.length - j * kBlock, x.box) > 0) {
-                    if (!wait(&bars->v_clean, clean_parity)) break;
-                    clean_parity ^= 1u;
+                    if (!wait(&bars->v_clean[vst], clean_parities >> vst & 1u)) break;
+                    clean_parities ^= 1u << vst;
                 }
                 if (j >= cur.begin0 && j < cur.end0) {
                     if (!output(0, vst, p_parity0, j == cur.begin0, j == cur.end0 - 1)) break;
