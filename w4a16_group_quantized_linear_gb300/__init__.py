@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -176,7 +177,7 @@ _ws: dict = {}
 def _workspace(dev: torch.device, stream, nbytes: int, kind: str = "linear"):
     if nbytes == 0:
         return None
-    key = (dev.index, stream.value, kind)
+    key = (dev.index, stream.value or 0, kind)
     buf = _ws.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
@@ -433,53 +434,70 @@ def rope_table(rows: int, rotary_dim: int, base: float = 10000.0, device="cuda")
     return torch.cat((angle.cos(), angle.sin()), dim=1).float()
 
 
-def _heads(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
-    """A [tokens, heads, head_dim] tensor whose heads' rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 3 or not t.is_cuda:
+# The calls below are made once per layer and token, so their checks ask each
+# tensor for little: its device index (-1 off the GPU), type, shape and strides.
+_CACHE = struct.Struct("PPqqqqPqiiPPiiii")  # _PagedCache
+_ROTARY = struct.Struct("PqiiPiP")          # _Rotary
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None, index: int = -1):
+    """(shape, strides) of a [tokens, heads, head_dim] tensor whose heads' rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.ndim != 3:
         raise ValueError(f"{name}: expected a 3-d torch.float16 or torch.bfloat16 CUDA tensor")
-    if t.stride(2) != 1 and t.shape[2] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if dtype is None:
+        if t.dtype not in _DTYPES or not t.is_cuda:
+            raise ValueError(f"{name}: expected a 3-d torch.float16 or torch.bfloat16 CUDA tensor")
+    elif t.dtype != dtype or t.get_device() != index:
         raise ValueError(f"{name}: expected the type and device of the other tensors")
-    return t
+    shape, stride = t.shape, t.stride()
+    if stride[2] != 1 and shape[2] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return shape, stride
 
 
-def _same_heads_out(out, x: torch.Tensor, name: str):
+def _rows_out(out, x: torch.Tensor, shape, name: str, index: int):
     """A contiguous result of x's shape: new, or the caller's."""
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _heads(out, name, x)
-    if out.shape != x.shape or not out.is_contiguous():
+        return torch.empty(shape, dtype=x.dtype, device=x.device)
+    if _rows(out, name, x.dtype, index)[0] != shape or not out.is_contiguous():
         raise ValueError(f"{name}: must be contiguous and of the input's shape")
     return out
 
 
-def _int32(t: torch.Tensor, name: str, dim: int, device: torch.device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or t.device != device:
+def _int32(t: torch.Tensor, name: str, dim: int, index: int):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.ndim != dim or t.get_device() != index:
         raise ValueError(f"{name}: expected a {dim}-d torch.int32 tensor on the other tensors' device")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t
+    return shape, stride
 
 
-def _rotary(table, positions, pair_axes, interleaved: bool, T: int, device: torch.device) -> _Rotary:
-    _need(table, "table", torch.float32, 2)
-    if table.device != device:
-        raise ValueError("table: must be on the other tensors' device")
-    axes = 1
+def _rotary(table, positions, pair_axes, interleaved: bool, T: int, index: int):
+    """(packed w4a16_rotary, what it points to)"""
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.float32 or table.ndim != 2 \
+            or table.get_device() != index or not table.is_contiguous():
+        raise ValueError("table: expected a contiguous 2-d torch.float32 tensor on the other tensors' device")
+    rows, dim = table.shape
+    axes, at, axis_of, axis_ptr = 1, 0, None, 0
     if positions is not None:
-        if isinstance(positions, torch.Tensor) and positions.dim() == 1:
+        if isinstance(positions, torch.Tensor) and positions.ndim == 1:
             positions = positions[None]
-        _int32(positions, "positions", 2, device)
-        if positions.shape[1] != T or not positions.is_contiguous():
+        shape, stride = _int32(positions, "positions", 2, index)
+        axes = shape[0]
+        if shape[1] != T or (axes > 1 and T > 0 and stride[0] != T):
             raise ValueError("positions: expected contiguous [T] or [axes, T]")
-        axes = positions.shape[0]
+        at = positions.data_ptr()
     if pair_axes is not None:
-        pair_axes = bytes(pair_axes)
-        if 2 * len(pair_axes) != table.shape[1]:
+        axis_of = bytes(pair_axes)
+        if 2 * len(axis_of) != dim:
             raise ValueError("pair_axes: expected one axis per pair, rotary_dim / 2 of them")
-    return _Rotary(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0,
-                   None if positions is None else positions.data_ptr(), axes, pair_axes)
+        axis_ptr = ctypes.cast(axis_of, _P).value
+    return _ROTARY.pack(table.data_ptr(), rows, dim, 1 if interleaved else 0, at, axes, axis_ptr), axis_of
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, pair_axes=None, interleaved: bool = False,
@@ -491,39 +509,49 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, pair_axe
     ``interleaved``. ``pair_axes`` gives the axis (0 to 3) whose position turns
     each pair (time, height and width of a video's patches, say); without it
     axis 0 turns all. ``out`` may be x itself."""
-    _heads(x, "x")
-    T, H, D = x.shape
-    r = _rotary(table, positions, pair_axes, interleaved, T, x.device)
+    shape, sx = _rows(x, "x")
+    index = x.get_device()
+    T, H, D = shape
+    if positions is None:
+        raise ValueError("positions: expected contiguous [T] or [axes, T]")
+    r, keep = _rotary(table, positions, pair_axes, interleaved, T, index)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out, so = torch.empty(shape, dtype=x.dtype, device=x.device), (H * D, D)
     else:
-        _heads(out, "out", x)
-        if out.shape != x.shape:
+        out_shape, so = _rows(out, "out", x.dtype, index)
+        if out_shape != shape:
             raise ValueError("out: must have x's shape")
-    _check(lib().w4a16_rope(_DTYPES[x.dtype], _ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0),
-                            out.stride(1), T, H, D, ctypes.byref(r), _stream(x.device)), "w4a16_rope")
+    status = (_lib or lib()).w4a16_rope(_DTYPES[x.dtype], x.data_ptr(), sx[0], sx[1], out.data_ptr(), so[0], so[1], T,
+                                        H, D, r, _raw_stream(index))
+    if status:
+        raise W4A16Error(status, "w4a16_rope")
     return out
 
 
-def _cache(k_cache, v_cache, page_table, q_offsets, kv_lens, like: torch.Tensor) -> _PagedCache:
+def _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, dtype, index: int):
+    """(packed w4a16_paged_cache, batch, kv_heads, head_dim)"""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype != like.dtype or t.device != like.device:
+        if not isinstance(t, torch.Tensor) or t.ndim != 4 or t.dtype != dtype or t.get_device() != index:
             raise ValueError(f"{name}: expected a 4-d tensor of the other tensors' type and device")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    shape, stride = k_cache.shape, k_cache.stride()
+    if v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    if k_cache.stride(3) != 1:
+    if stride[3] != 1:
         raise ValueError("k_cache, v_cache: the last dimension must be contiguous")
-    _int32(page_table, "page_table", 2, like.device)
-    _int32(q_offsets, "q_offsets", 1, like.device)
-    _int32(kv_lens, "kv_lens", 1, like.device)
-    B = kv_lens.shape[0]
-    if page_table.shape[0] != B or q_offsets.shape[0] != B + 1:
+    table_shape, table_stride = _int32(page_table, "page_table", 2, index)
+    B = _int32(kv_lens, "kv_lens", 1, index)[0][0]
+    if table_shape[0] != B or _int32(q_offsets, "q_offsets", 1, index)[0][0] != B + 1:
         raise ValueError("page_table [B, max_pages], q_offsets [B + 1] and kv_lens [B] must agree")
-    pages, size, G, D = k_cache.shape
-    sp, ss, sh, _ = k_cache.stride()
-    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, sp, ss, sh, page_table.data_ptr(),
-                       page_table.stride(0), page_table.shape[1], size, q_offsets.data_ptr(), kv_lens.data_ptr(), B,
-                       G, D, _DTYPES[like.dtype])
+    pages, size, G, D = shape
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), pages, stride[0], stride[1], stride[2],
+                       page_table.data_ptr(), table_stride[0], table_shape[1], size, q_offsets.data_ptr(),
+                       kv_lens.data_ptr(), B, G, D, _DTYPES[dtype]), B, G, D
+
+
+def _cache(k_cache, v_cache, page_table, q_offsets, kv_lens, like: torch.Tensor) -> _PagedCache:
+    """The checked arguments as the C structure, for callers of the C ABI."""
+    return _PagedCache.from_buffer_copy(
+        _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, like.dtype, like.get_device())[0])
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -543,31 +571,34 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     kv_lens[b] counts its cached tokens with these among them; its place p lives in
     slot p % page_size of page page_table[b, p // page_size]. All three are int32
     on the device: a captured graph follows their values."""
-    _heads(k, "k")
-    _heads(v, "v", k)
-    T, G, D = k.shape
-    if v.shape != k.shape:
+    shape, sk = _rows(k, "k")
+    index, dtype = k.get_device(), k.dtype
+    v_shape, sv = _rows(v, "v", dtype, index)
+    if v_shape != shape:
         raise ValueError("k and v must have the same shape")
-    c = _cache(k_cache, v_cache, page_table, q_offsets, kv_lens, k)
-    if (c.kv_heads, c.head_dim) != (G, D):
+    T, G, D = shape
+    c, _, cache_heads, cache_dim = _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, dtype, index)
+    if cache_heads != G or cache_dim != D:
         raise ValueError("the cache must have k's heads and head_dim")
-    H, sq = 0, (0, 0, 0)
+    H, sq, q_ptr, out_ptr = 0, (0, 0), 0, 0
     if q is not None:
-        _heads(q, "q", k)
-        if q.shape[0] != T or q.shape[2] != D:
+        q_shape, sq = _rows(q, "q", dtype, index)
+        if q_shape[0] != T or q_shape[2] != D:
             raise ValueError("q must be [T, heads, head_dim]")
-        H, sq = q.shape[1], q.stride()
-        q_out = _same_heads_out(q_out, q, "q_out")
+        H = q_shape[1]
+        q_out = _rows_out(q_out, q, q_shape, "q_out", index)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    r = None
+    r = keep = None
     if table is not None:
-        r = ctypes.byref(_rotary(table, positions, pair_axes, interleaved, T, k.device))
+        r, keep = _rotary(table, positions, pair_axes, interleaved, T, index)
     elif positions is not None or pair_axes is not None:
         raise ValueError("positions and pair_axes need table")
-    _check(lib().w4a16_kv_append(ctypes.byref(c), T, _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
-                                 v.stride(1), _ptr(q) if q is not None else None, sq[0], sq[1], H,
-                                 _ptr(q_out) if q is not None else None, r, _stream(k.device)), "w4a16_kv_append")
+    status = (_lib or lib()).w4a16_kv_append(c, T, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], q_ptr,
+                                             sq[0], sq[1], H, out_ptr, r, _raw_stream(index))
+    if status:
+        raise W4A16Error(status, "w4a16_kv_append")
     return q_out
 
 
@@ -585,21 +616,26 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
     Returns out [T, heads, head_dim], or (out, lse) with ``return_lse``: lse
     fp32 [T, heads] is the natural logarithm of the softmax's sum."""
-    _heads(q, "q")
-    T, H, D = q.shape
-    c = _cache(k_cache, v_cache, page_table, q_offsets, kv_lens, q)
-    if c.head_dim != D or c.kv_heads == 0 or H % c.kv_heads != 0:
+    shape, sq = _rows(q, "q")
+    index = q.get_device()
+    T, H, D = shape
+    c, B, G, cache_dim = _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, q.dtype, index)
+    if cache_dim != D or G == 0 or H % G != 0:
         raise ValueError("the cache must have q's head_dim, and heads must be a multiple of its heads")
-    out = _same_heads_out(out, q, "out")
+    out = _rows_out(out, q, shape, "out", index)
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
-    st = _stream(q.device)
-    h = lib()
-    ws = _workspace(q.device, st, int(h.w4a16_paged_attention_workspace_bytes(T, c.batch, H, c.kv_heads, D,
-                                                                               max_q_len)), "attention")
-    _check(h.w4a16_paged_attention(ctypes.byref(c), T, _ptr(q), q.stride(0), q.stride(1), H, max_q_len,
-                                   CAUSAL if causal else 0, window, D ** -0.5 if scale is None else scale, _ptr(out),
-                                   _ptr(lse) if return_lse else None, _ptr(ws) if ws is not None else None,
-                                   ws.numel() if ws is not None else 0, st), "w4a16_paged_attention")
+    st = _raw_stream(index)
+    h = _lib or lib()
+    need = h.w4a16_paged_attention_workspace_bytes(T, B, H, G, D, max_q_len)
+    ws = _ws.get((index, st, "attention"))
+    if need and (ws is None or ws.numel() < need):
+        ws = _workspace(q.device, ctypes.c_void_p(st), need, "attention")
+    status = h.w4a16_paged_attention(c, T, q.data_ptr(), sq[0], sq[1], H, max_q_len, CAUSAL if causal else 0, window,
+                                     D ** -0.5 if scale is None else scale, out.data_ptr(),
+                                     lse.data_ptr() if return_lse else 0, ws.data_ptr() if need else 0,
+                                     ws.numel() if need else 0, st)
+    if status:
+        raise W4A16Error(status, "w4a16_paged_attention")
     return (out, lse) if return_lse else out
 
 
