@@ -36,6 +36,23 @@ struct Bf16 {
 
 // ---------------------------------------------------------------- cache --
 
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery's method
+// for a divisor known before the loop; here the host knows it).
+struct FastDiv {
+    uint32_t d, mul, shift;
+    __device__ __forceinline__ int quotient(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+    __device__ __forceinline__ int remainder(int n) const { return n - quotient(n) * (int)d; }
+};
+
+inline FastDiv fast_div(int divisor) {
+    FastDiv f{(uint32_t)divisor, 0, 0};
+    while ((1ull << f.shift) < f.d) ++f.shift;
+    f.mul = (uint32_t)((1ull << 32) * ((1ull << f.shift) - f.d) / f.d + 1);
+    return f;
+}
+
 // The paged cache and the batch that is appended to it or attends over it.
 // Strides are in elements; element (page, slot, head, d) of either cache sits
 // at page * page_stride + slot * slot_stride + head * head_stride + d.
@@ -46,6 +63,7 @@ struct CacheArgs {
     const int32_t* table;   // [batch, table_stride], max_pages entries used of each row
     int64_t table_stride;
     int32_t page_size, max_pages;
+    FastDiv by_page;  // the page size
     const int32_t* q_offsets;  // [batch + 1]
     const int32_t* kv_lens;    // [batch]
     int32_t batch, kv_heads, head_dim;
@@ -53,9 +71,8 @@ struct CacheArgs {
     unsigned int* err;
 };
 
-// Cached tokens of sequence b, held to what its row of the page table can name.
-__device__ __forceinline__ int cache_length(const CacheArgs& c, int b) {
-    const int n = __ldg(c.kv_lens + b);
+// Cached tokens of a sequence (n of kv_lens), held to what its row of the page table can name.
+__device__ __forceinline__ int cache_length(const CacheArgs& c, int n) {
     const int64_t most = (int64_t)c.max_pages * c.page_size;
     if (n < 0 || n > most) {
         raise_device_error(c.err, W4A16_ERR_BAD_CACHE);
@@ -103,7 +120,7 @@ __device__ __forceinline__ void check_offsets(const CacheArgs& c) {
 
 // Page that holds place p of sequence b, or -1 (reported) for an entry outside the cache.
 __device__ __forceinline__ int64_t page_of(const CacheArgs& c, int b, int p) {
-    const int32_t page = __ldg(c.table + b * c.table_stride + p / c.page_size);
+    const int32_t page = __ldg(c.table + b * c.table_stride + c.by_page.quotient(p));
     if (page < 0 || page >= c.pages) {
         raise_device_error(c.err, W4A16_ERR_BAD_CACHE);
         return -1;
@@ -146,7 +163,8 @@ struct AttentionArgs {
     int64_t q_row_stride, q_head_stride;
     uint16_t* out;  // [T, heads, head_dim]
     float* lse;     // [T, heads] or nullptr
-    int32_t heads;
+    int32_t heads, ratio;   // ratio: query heads per cached head
+    FastDiv by_ratio;       // T * ratio fits 31 bits
     int32_t causal, window;  // window 0: no lower limit
     float scale_log2;        // softmax scale times log2(e)
     int64_t max_q_len;
@@ -161,11 +179,15 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 // Equal runs of a work list over the thread blocks: the first `more` take base + 1 units.
 struct Shares {
-    int64_t base, more;
-    __device__ __forceinline__ int64_t start(int64_t c) const { return c * base + min(c, more); }
-    __device__ __forceinline__ int64_t owner(int64_t unit) const {
-        const int64_t cut = more * (base + 1);
-        return unit < cut ? unit / (base + 1) : more + (unit - cut) / base;
+    int64_t base;
+    int more;
+    __device__ __forceinline__ int64_t start(int c) const { return c * base + min(c, more); }
+    // the thread block whose run holds the unit, looked for from block c on (a few steps: an
+    // item is seldom cut into many parts, and a division here costs more)
+    __device__ __forceinline__ int owner(int64_t unit, int c) const {
+        while (start(c) > unit) --c;
+        while (start(c + 1) <= unit) ++c;
+        return c;
     }
 };
 

@@ -62,6 +62,7 @@ CacheArgs cache_args(const w4a16_paged_cache& c, int64_t T, unsigned int* err) {
     a.table_stride = c.page_table_stride;
     a.page_size = c.page_size;
     a.max_pages = c.max_pages;
+    a.by_page = fast_div(c.page_size);
     a.q_offsets = c.q_offsets;
     a.kv_lens = c.kv_lens;
     a.batch = c.batch;
@@ -146,6 +147,7 @@ w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int64_t T, co
         return W4A16_ERR_INVALID_ARG;
     if (T == 0) return W4A16_OK;
     if (!q || !out || max_q_len == 0) return W4A16_ERR_INVALID_ARG;
+    if (T * (heads / cache->kv_heads) > 0x7ffffc00LL) return W4A16_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3u)) return W4A16_ERR_MISALIGNED;
     const DeviceInfo* dev;
     s = check_device(&dev);
@@ -158,6 +160,8 @@ w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int64_t T, co
     a.out = out;
     a.lse = lse;
     a.heads = heads;
+    a.ratio = heads / cache->kv_heads;
+    a.by_ratio = fast_div(a.ratio);
     a.causal = (flags & W4A16_CAUSAL) ? 1 : 0;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;

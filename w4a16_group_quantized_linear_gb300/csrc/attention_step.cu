@@ -35,6 +35,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;               // places per warp step
 constexpr int kBlock = kWarps * kStep;  // places per block of the work list
 constexpr int kBlocksPerSm = 2;
+constexpr int kLeast = 1;               // blocks of a run, if the list has fewer than every SM could take
 constexpr int kRingBytes = 24 * 1024;   // per warp
 constexpr float kSlack = 8.0f;          // how far a score may pass the running maximum (log2)
 
@@ -112,17 +113,24 @@ struct Sequence {
 };
 
 __device__ __forceinline__ void load_sequence(const AttentionArgs& a, int b, int max_rows, Sequence& s) {
-    s.first = __ldg(a.c.q_offsets + b);
-    s.count = __ldg(a.c.q_offsets + b + 1) - s.first;
+    const int first = __ldg(a.c.q_offsets + b), next = __ldg(a.c.q_offsets + b + 1), length = __ldg(a.c.kv_lens + b);
+    s.first = first;
+    s.count = next - first;
     s.blocks = 0;
-    const int ratio = a.heads / a.c.kv_heads;
-    if (s.count <= 0 || s.count > a.max_q_len || (int64_t)s.count * ratio > max_rows || s.first < 0 ||
-        (int64_t)s.first + s.count > a.c.T)
-        return;
-    s.length = cache_length(a.c, b);
+    if (first < 0 || next > a.c.T || s.count <= 0 || s.count > a.max_q_len || s.count * a.ratio > max_rows) return;
+    s.length = cache_length(a.c, length);
     s.low = a.window > 0 ? max(0, s.length - s.count - a.window + 1) : 0;
     s.block = s.low / kBlock;
     s.blocks = max(1, (s.length + kBlock - 1) / kBlock - s.block);
+}
+
+// This thread block's run of `total` units.
+__device__ __forceinline__ void share_out(int64_t total, Shares& shares, int64_t& begin, int64_t& end) {
+    const int runs = (int)min((int64_t)gridDim.x, (total + kLeast - 1) / kLeast);
+    shares.base = runs ? total / runs : 0;
+    shares.more = runs ? (int)(total - shares.base * runs) : 0;
+    begin = blockIdx.x < runs ? shares.start(blockIdx.x) : total;
+    end = blockIdx.x < runs ? shares.start(blockIdx.x + 1) : total;
 }
 
 // A position in the work list, as a warp walks it.
@@ -153,81 +161,69 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     constexpr int kKs = D / 16;  // k-steps of the scores; 16-element tiles of the output
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t s_sum[kWarps];
-    __shared__ int64_t s_found[2];
+    __shared__ int s_found[2];
     __shared__ float2 s_stats[kWarps][kRows];
     __shared__ int s_last;
     const AttentionArgs& a = arg.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp = lane >> 2, quad = lane & 3;
-    const int ratio = a.heads / a.c.kv_heads;
+    const int ratio = a.ratio;
 
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     if (blockIdx.x == 0) check_offsets(a.c);
 
-    // the length of the work list, and the item in which this thread block's run starts
-    int64_t total = 0;
-    for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
-        Sequence s;
-        int64_t n = 0;
-        if (b0 + tid < a.c.batch) {
-            load_sequence(a, b0 + tid, kRows, s);
-            n = s.blocks;
-            if (blockIdx.x == 0 && s.count > a.max_q_len) raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
-        }
-        total += n;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    if (lane == 0) s_sum[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
-    total *= a.c.kv_heads;
-    __syncthreads();
+    // the length of the work list, then the item in which this thread block's
+    // run starts; one round does for both while there are no more sequences than threads
     Shares shares;
-    shares.base = total / gridDim.x;
-    shares.more = total % gridDim.x;
-    const int64_t run_begin = shares.start(blockIdx.x), run_end = shares.start(blockIdx.x + 1);
-    if (run_begin >= run_end) return;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
-        Sequence s;
-        int64_t n = 0;
-        if (b0 + tid < a.c.batch) {
-            load_sequence(a, b0 + tid, kRows, s);
-            n = (int64_t)s.blocks * a.c.kv_heads;
-        }
-        int64_t upto = n;  // inclusive sum over the threads
+    int64_t run_begin = 0, run_end = 0;
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+        int64_t before = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
+            Sequence s;
+            int64_t n = 0;
+            if (b0 + tid < a.c.batch) {
+                load_sequence(a, b0 + tid, kRows, s);
+                n = (int64_t)s.blocks * a.c.kv_heads;
+                if (blockIdx.x == 0 && s.count > a.max_q_len) raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
+            }
+            int64_t upto = n;  // inclusive sum over the threads
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += v;
-        }
-        if (lane == 31) s_sum[warp] = upto;
-        __syncthreads();
-        int64_t all = 0;
-        upto += before;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += v;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = upto;
+            __syncthreads();
+            upto += before;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) upto += s_sum[w];
-            all += s_sum[w];
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) upto += s_sum[w];
+                before += s_sum[w];
+            }
+            if (round == 0 && a.c.batch <= kThreads) {
+                share_out(before, shares, run_begin, run_end);
+                round = 1;
+            }
+            if (round == 1 && run_begin >= upto - n && run_begin < upto) {
+                s_found[0] = b0 + tid;
+                s_found[1] = (int)(run_begin - (upto - n));
+            }
+            if (round == 1 && before > run_begin) break;
         }
-        if (run_begin >= upto - n && run_begin < upto) {
-            s_found[0] = b0 + tid;
-            s_found[1] = run_begin - (upto - n);
-        }
-        before += all;
-        __syncthreads();
-        if (before > run_begin) break;
+        if (round == 0) share_out(before, shares, run_begin, run_end);
+        if (run_begin >= run_end) return;
     }
+    __syncthreads();
 
     Cursor at;  // of the computation
-    at.b = (int)s_found[0];
+    at.b = s_found[0];
     load_sequence(a, at.b, kRows, at.s);
-    at.g = (int)(s_found[1] / at.s.blocks);
-    at.block = at.s.block + (int)(s_found[1] % at.s.blocks);
+    at.g = s_found[1] / at.s.blocks;
+    at.block = at.s.block + s_found[1] % at.s.blocks;
     at.end = at.s.block + at.s.blocks;
     Cursor to = at;  // of the loads, which run ahead
     int64_t to_load = run_end - run_begin;
@@ -250,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             }
             const int page = __shfl_sync(0xffffffffu, my_page, to.block - pages_from);
             const int p0 = to.block * kBlock + warp * kStep;
-            const int64_t base = (int64_t)page * a.c.page_stride + (int64_t)(p0 % a.c.page_size) * a.c.slot_stride +
+            const int64_t base = (int64_t)page * a.c.page_stride + (int64_t)a.c.by_page.remainder(p0) * a.c.slot_stride +
                                  (int64_t)to.g * a.c.head_stride;
             const uint32_t dst = ring_u + stage * 2 * L::kHalfStage;
             constexpr int kRowsPer = 32 / L::kChunks;  // rows per instruction
@@ -282,8 +278,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         for (int n = 0; n < NT; ++n) {
             const int r = n * 8 + grp;
             const bool real = r < at.s.count * ratio;
-            const int64_t t = at.s.first + r / ratio;
-            const uint16_t* q = a.q + t * a.q_row_stride + (int64_t)(at.g * ratio + r % ratio) * a.q_head_stride;
+            const int64_t t = at.s.first + a.by_ratio.quotient(r);
+            const uint16_t* q =
+                a.q + t * a.q_row_stride + (int64_t)(at.g * ratio + a.by_ratio.remainder(r)) * a.q_head_stride;
 #pragma unroll
             for (int ks = 0; ks < kKs; ++ks)
 #pragma unroll
@@ -292,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = n * 8 + quad * 2 + j;
-                const int place = at.s.length - at.s.count + row / ratio;
+                const int place = at.s.length - at.s.count + a.by_ratio.quotient(row);
                 low[n][j] = a.window > 0 ? max(0, place - a.window + 1) : 0;
                 high[n][j] = row < at.s.count * ratio ? (a.causal ? min(at.s.length, place + 1) : at.s.length) : 0;
                 m[n][j] = -INFINITY;
@@ -379,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     // here) and writes the result, or the part for the last of its thread blocks to join.
     float* join = reinterpret_cast<float*>(smem + kWarps * kRingBytes);
     auto write_row = [&](int r, int d, float (&acc)[8], float top, float sum) {
-        const int64_t row = (int64_t)(at.s.first + r / ratio) * a.heads + at.g * ratio + r % ratio;
+        const int64_t row = (int64_t)(at.s.first + a.by_ratio.quotient(r)) * a.heads + at.g * ratio +
+                            a.by_ratio.remainder(r);
         const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
         uint4 w;
         w.x = E::pack(acc[0] * inv, acc[1] * inv);
@@ -390,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     };
     auto finish_item = [&](int64_t item_begin, int64_t item_end) {
-        const int64_t c0 = shares.owner(item_begin), c1 = shares.owner(item_end - 1);
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (c0 == blockIdx.x ? 1 : 0);
+        const int c0 = shares.owner(item_begin, blockIdx.x), c1 = shares.owner(item_end - 1, blockIdx.x);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x ? 1 : 0);
         const int rows = at.s.count * ratio;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -456,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         __syncthreads();
         if (tid == 0) {
             const int done = ptx::atom_add_acq_rel_gpu(arg.counters + c0, 1);
-            s_last = done == (int)(c1 - c0);
+            s_last = done == c1 - c0;
             if (s_last) arg.counters[c0] = 0;
         }
         __syncthreads();
@@ -465,12 +463,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         for (int i = tid; i < rows * L::kChunks; i += kThreads) {
             const int r = i / L::kChunks, d = i % L::kChunks * 8;
             float top = -INFINITY, sum = 0.0f, acc[8];
-            for (int64_t c = c0; c <= c1; ++c)
-                top = fmaxf(top, __ldcg(arg.stats + (2 * c + (c == c0)) * kRows + r).x);
+#pragma unroll 8
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(arg.stats + (2 * c + (c == c0)) * kRows + r).x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
-#pragma unroll 4
-            for (int64_t c = c0; c <= c1; ++c) {
+#pragma unroll 8
+            for (int c = c0; c <= c1; ++c) {
                 const int64_t part = (2 * c + (c == c0)) * kRows + r;
                 const float2 st = __ldcg(arg.stats + part);
                 const float4* src = reinterpret_cast<const float4*>(arg.parts + part * D + d);

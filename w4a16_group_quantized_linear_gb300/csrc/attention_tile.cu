@@ -98,7 +98,7 @@ struct Entry {
     int begin[2], end[2];      // of them, those that the halves see
     int c0, c1;                // the thread blocks that share the tile
     int last;
-    int64_t row;               // first row of the tile
+    int row;                   // first row of the tile
 };
 
 struct Bars {
@@ -136,15 +136,13 @@ struct Sequence {
 
 __device__ __forceinline__ void load_sequence(const TileArgs& x, int b, Sequence& s) {
     const AttentionArgs& a = x.a;
-    s.first = __ldg(a.c.q_offsets + b);
-    s.count = __ldg(a.c.q_offsets + b + 1) - s.first;
+    const int first = __ldg(a.c.q_offsets + b), next = __ldg(a.c.q_offsets + b + 1), length = __ldg(a.c.kv_lens + b);
+    s.first = first;
+    s.count = next - first;
     s.tiles = 0;
-    const int ratio = a.heads / a.c.kv_heads;
-    if (s.count <= 0 || s.count > a.max_q_len || (int64_t)s.count * ratio < x.min_rows || s.first < 0 ||
-        (int64_t)s.first + s.count > a.c.T)
-        return;
-    s.length = cache_length(a.c, b);
-    s.tiles = (int)(((int64_t)s.count * ratio + kTile - 1) / kTile);
+    if (first < 0 || next > a.c.T || s.count <= 0 || s.count > a.max_q_len || s.count * a.ratio < x.min_rows) return;
+    s.length = cache_length(a.c, length);
+    s.tiles = (s.count * a.ratio + kTile - 1) / kTile;
 }
 
 // The places that rows [r0, r1) of a sequence see together, and their blocks.
@@ -152,13 +150,11 @@ struct Range {
     int low, block, end;  // block == end: none
 };
 
-__device__ __forceinline__ Range range_of(const AttentionArgs& a, int count, int length, int64_t r0, int64_t r1) {
-    const int ratio = a.heads / a.c.kv_heads;
-    const int64_t rows = (int64_t)count * ratio;
-    if (r1 > rows) r1 = rows;
+__device__ __forceinline__ Range range_of(const AttentionArgs& a, int count, int length, int r0, int r1) {
     Range r{0, 0, 0};
+    r1 = min(r1, count * a.ratio);
     if (r0 >= r1) return r;
-    const int first = length - count + (int)(r0 / ratio), last = length - count + (int)((r1 - 1) / ratio);
+    const int first = length - count + a.by_ratio.quotient(r0), last = length - count + a.by_ratio.quotient(r1 - 1);
     const int high = a.causal ? min(length, last + 1) : length;
     if (high <= 0) return r;
     r.low = a.window > 0 ? max(0, first - a.window + 1) : 0;
@@ -179,7 +175,7 @@ struct Segment {
 };
 
 __device__ __forceinline__ void set_tile(const AttentionArgs& a, Segment& s) {
-    const int64_t r = (int64_t)s.tile * kTile;
+    const int r = s.tile * kTile;
     s.half0 = range_of(a, s.s.count, s.s.length, r, r + kHalf);
     s.half1 = range_of(a, s.s.count, s.s.length, r + kHalf, r + kTile);
     const bool first = s.half0.end > s.half0.block, second = s.half1.end > s.half1.block;
@@ -303,100 +299,110 @@ __device__ __forceinline__ void fail(const TileArgs& x, Bars* bars) {
     raise_device_error(x.a.c.err, W4A16_ERR_TIMEOUT);
 }
 
-// The list's length, and where this thread block's run starts in it. All
-// threads; scratch: 5 * kThreads ints of shared memory. Returns false where there is no run.
 struct Run {
     Shares shares;
     int64_t begin, end;
 };
 
-__device__ bool find_run(const TileArgs& x, int* scratch, Run& run, Segment& at) {
+// The list's length, and where this thread block's run starts in it. All
+// threads; scratch: 3 * kThreads ints of shared memory. Returns false where
+// there is no run. Sequences a thread each, then their tiles a thread each;
+// one round does for both questions while neither are more than the threads.
+__device__ __forceinline__ bool find_run(const TileArgs& x, int* scratch, Run& run, Segment& at) {
     __shared__ int64_t s_sum[kThreads / 32];
-    __shared__ int64_t s_found[3];
+    __shared__ int s_found[3];
     int* s_first = scratch;  // first tile of each sequence of this round
-    int* s_count = scratch + kThreads + 1;
+    int* s_count = scratch + kThreads;
     int* s_length = s_count + kThreads;
     const AttentionArgs& a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    auto scan = [&](int64_t v, int64_t& all) {  // inclusive, over the threads
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, v, d);
-            if (lane >= d) v += u;
-        }
-        __syncthreads();
-        if (lane == 31) s_sum[warp] = v;
-        __syncthreads();
-        all = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) v += s_sum[w];
-            all += s_sum[w];
-        }
-        return v;
+    auto share_out = [&](int64_t total) {
+        run.shares.base = total / gridDim.x;
+        run.shares.more = (int)(total - run.shares.base * gridDim.x);
+        run.begin = run.shares.start(blockIdx.x);
+        run.end = run.shares.start(blockIdx.x + 1);
     };
-    int64_t total = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t before = 0;
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+        int64_t before = 0;  // units of the tiles so far
+#pragma unroll 1
         for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
             Sequence s;
             s.tiles = 0;
             if (b0 + tid < a.c.batch) {
                 load_sequence(x, b0 + tid, s);
-                if (blockIdx.x == 0 && pass == 0 && s.count > a.max_q_len)
-                    raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
+                if (blockIdx.x == 0 && s.count > a.max_q_len) raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
             }
-            int64_t tiles;
-            const int64_t upto = scan(s.tiles, tiles);  // T rows at most: tiles fit an int
-            s_first[tid] = (int)(upto - s.tiles);
-            s_count[tid] = s.count;
-            s_length[tid] = s.length;
-            __syncthreads();
-            for (int64_t i0 = 0; i0 < tiles; i0 += kThreads) {
-                const int64_t i = i0 + tid;
-                int64_t n = 0;
-                int lo = 0;
-                if (i < tiles) {
-                    int hi = kThreads - 1;  // the last sequence that starts at or before tile i
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (s_first[mid] <= i) lo = mid;
-                        else hi = mid - 1;
+            int tiles = 0;
+            // what is summed: first the sequences' tiles, then the units of the tiles, kThreads at a time
+#pragma unroll 1
+            for (int i0 = -kThreads; i0 < tiles; i0 += kThreads) {
+                int64_t n = s.tiles;
+                int lo = 0, tile = 0;
+                if (i0 >= 0) {
+                    n = 0;
+                    if (i0 + tid < tiles) {
+                        int hi = kThreads - 1;  // the last sequence that starts at or before the tile
+                        while (lo < hi) {
+                            const int mid = (lo + hi + 1) >> 1;
+                            if (s_first[mid] <= i0 + tid) lo = mid;
+                            else hi = mid - 1;
+                        }
+                        Segment t;
+                        tile = t.tile = i0 + tid - s_first[lo];
+                        t.s.count = s_count[lo];
+                        t.s.length = s_length[lo];
+                        set_tile(a, t);
+                        n = (int64_t)(t.end - t.block) * a.c.kv_heads;
                     }
-                    Segment t;
-                    t.tile = (int)(i - s_first[lo]);
-                    t.s.count = s_count[lo];
-                    t.s.length = s_length[lo];
-                    set_tile(a, t);
-                    n = (int64_t)(t.end - t.block) * a.c.kv_heads;
                 }
-                int64_t all;
-                const int64_t sum = before + scan(n, all);
+                int64_t upto = n;  // inclusive sum over the threads
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t u = __shfl_up_sync(0xffffffffu, upto, d);
+                    if (lane >= d) upto += u;
+                }
+                __syncthreads();
+                if (lane == 31) s_sum[warp] = upto;
+                __syncthreads();
+                int64_t all = 0;
+#pragma unroll 1
+                for (int w = 0; w < kThreads / 32; ++w) {
+                    if (w < warp) upto += s_sum[w];
+                    all += s_sum[w];
+                }
+                if (i0 < 0) {
+                    tiles = (int)all;
+                    s_first[tid] = (int)(upto - n);
+                    s_count[tid] = s.count;
+                    s_length[tid] = s.length;
+                    __syncthreads();
+                    continue;
+                }
+                upto += before;
                 before += all;
-                if (pass == 1 && n > 0 && run.begin >= sum - n && run.begin < sum) {
+                if (round == 0 && a.c.batch <= kThreads && tiles <= kThreads) {
+                    share_out(before);
+                    round = 1;
+                }
+                if (round == 1 && n > 0 && run.begin >= upto - n && run.begin < upto) {
                     s_found[0] = b0 + lo;
-                    s_found[1] = i - s_first[lo];
-                    s_found[2] = run.begin - (sum - n);
+                    s_found[1] = tile;
+                    s_found[2] = (int)(run.begin - (upto - n));
                 }
             }
             __syncthreads();
-            if (pass == 1 && before > run.begin) break;
+            if (round == 1 && before > run.begin) break;
         }
-        if (pass == 0) {
-            total = before;
-            run.shares.base = total / gridDim.x;
-            run.shares.more = total % gridDim.x;
-            run.begin = run.shares.start(blockIdx.x);
-            run.end = run.shares.start(blockIdx.x + 1);
-            if (run.begin >= run.end) return false;
-        }
+        if (round == 0) share_out(before);
+        if (run.begin >= run.end) return false;
     }
-    at.b = (int)s_found[0];
-    at.tile = (int)s_found[1];
+    at.b = s_found[0];
+    at.tile = s_found[1];
     load_sequence(x, at.b, at.s);
     set_tile(a, at);
-    at.g = (int)(s_found[2] / (at.end - at.block));
-    at.from = at.block + (int)(s_found[2] % (at.end - at.block));
+    at.g = s_found[2] / (at.end - at.block);
+    at.from = at.block + s_found[2] % (at.end - at.block);
     at.to = (int)min((int64_t)at.end, at.from + (run.end - run.begin));
     return true;
 }
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kBarsAt);
     const AttentionArgs& a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ratio = a.heads / a.c.kv_heads;
+    const int ratio = a.ratio;
 
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Entry& e = bars->work[k % kEntries];
                 e.b = seg.b;
                 e.g = seg.g;
-                e.row = (int64_t)seg.tile * kTile;
+                e.row = seg.tile * kTile;
                 e.first = seg.s.first;
                 e.count = seg.s.count;
                 e.length = seg.s.length;
@@ -498,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 e.end[0] = max(e.begin[0], seg.end_of(0));
                 e.end[1] = max(e.begin[1], seg.end_of(1));
                 const int64_t item = unit - (seg.from - seg.block);
-                e.c0 = (int)run.shares.owner(item);
-                e.c1 = (int)run.shares.owner(item + (seg.end - seg.block) - 1);
+                e.c0 = run.shares.owner(item, blockIdx.x);
+                e.c1 = run.shares.owner(item + (seg.end - seg.block) - 1, blockIdx.x);
                 e.last = left == n;
                 ptx::mbar_arrive(&bars->work_full[k % kEntries]);
             }
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (piece < pieces)
                         tma_load_4d(ring + st * L::kStageBytes + slab * L::kSlabBytes + piece * x.box * 128,
-                                    kv ? &map_v : &map_k, &bars->full[st], slab * 64, p % a.c.page_size, g,
+                                    kv ? &map_v : &map_k, &bars->full[st], slab * 64, a.c.by_page.remainder(p), g,
                                     (int)page);
                     ++issued;
                 }
@@ -738,12 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
             for (int i = 0; i < 32 / kRowsPer; ++i) {
                 const int r = (warp & 3) * 32 + i * kRowsPer + lane / kPieces;
-                const int64_t at = e.row + w * kHalf + r;
-                const int64_t token = at / ratio;
+                const int at = e.row + w * kHalf + r;
+                const int token = a.by_ratio.quotient(at);
                 const bool real = token < e.count;
-                const uint16_t* src = a.q + (real ? (e.first + token) * a.q_row_stride +
-                                                        (e.g * ratio + at % ratio) * a.q_head_stride + piece * 8
-                                                  : 0);
+                const uint16_t* src =
+                    a.q + (real ? (e.first + token) * a.q_row_stride +
+                                      (int64_t)(e.g * ratio + at - token * ratio) * a.q_head_stride + piece * 8
+                                : 0);
                 ptx::cp_async_16(q_smem + (piece >> 3) * L::kSlabBytes + r * 128 + (((piece & 7) ^ (r & 7)) << 4), src,
                                  real ? 16u : 0u);
             }
@@ -764,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int begin = e.begin[w], end = e.end[w];
             int low, high;
             {
-                const int64_t token = (e.row + w * kHalf + row) / ratio;
-                const int place = e.length - e.count + (int)token;
+                const int token = a.by_ratio.quotient(e.row + w * kHalf + row);
+                const int place = e.length - e.count + token;
                 low = a.window > 0 ? max(0, place - a.window + 1) : 0;
                 high = token >= e.count ? 0 : a.causal ? min(e.length, place + 1) : e.length;
             }
@@ -862,10 +869,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after();
             }
             const float l = sum.x + sum.y;
-            const int64_t at = e.row + w * kHalf + row;
-            const int64_t token = at / ratio;
+            const int at = e.row + w * kHalf + row;
+            const int token = a.by_ratio.quotient(at);
             const bool real = token < e.count;
-            const int64_t out_row = (e.first + token) * a.heads + e.g * ratio + at % ratio;
+            const int64_t out_row = (int64_t)(e.first + token) * a.heads + e.g * ratio + at - token * ratio;
             const int c0 = e.c0, c1 = e.c1;
             auto write32 = [&](int d, const float (&v)[32], float scale) {
                 uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + d);
@@ -921,8 +928,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __threadfence();
                     const float2* st = x.stats + w * kHalf + row;
                     float top = -INFINITY, total = 0.0f;
-                    for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(st + (2 * c + (c == c0)) * kTile).x);
-                    for (int64_t c = c0; c <= c1; ++c) {
+                    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(st + (2 * c + (c == c0)) * kTile).x);
+                    for (int c = c0; c <= c1; ++c) {
                         const float2 v = __ldcg(st + (2 * c + (c == c0)) * kTile);
                         total += v.x == -INFINITY ? 0.0f : v.y * fast_exp2(v.x - top);
                     }
@@ -932,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                        for (int64_t c = c0; c <= c1; ++c) {
+                        for (int c = c0; c <= c1; ++c) {
                             const int64_t part = 2 * c + (c == c0);
                             const float mc = __ldcg(st + part * kTile).x;
                             const float f = mc == -INFINITY ? 0.0f : fast_exp2(mc - top);

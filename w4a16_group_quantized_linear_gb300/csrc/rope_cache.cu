@@ -210,12 +210,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int b = sequence_of(a.c, t, first, count);
     // place in the sequence; negative where the sequence is shorter than its new tokens
     int place = -1;
-    if (b >= 0) place = cache_length(a.c, b) - count + (int)(t - first);
+    if (b >= 0) place = cache_length(a.c, __ldg(a.c.kv_lens + b)) - count + (int)(t - first);
     float c[8], s[8];
     const bool rotate = p.pair >= 0 && angles(a.r, a.c.T, t, place, p.pair, a.c.err, c, s);
     int64_t page = -1;
     if (place >= 0) page = page_of(a.c, b, place);
-    const int64_t slot = page * a.c.page_stride + (place < 0 ? 0 : place % a.c.page_size) * a.c.slot_stride;
+    const int64_t slot = page * a.c.page_stride + (place < 0 ? 0 : a.c.by_page.remainder(place)) * a.c.slot_stride;
 #pragma unroll
     for (int k = 0; k < HPT; ++k) {
         const int h = group + k * groups;
