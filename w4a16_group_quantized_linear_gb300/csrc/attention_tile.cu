@@ -57,7 +57,8 @@ constexpr int kThreads = 384;
 // Registers: a launch of 384 threads has 168 each; the two softmax warpgroups
 // hold a row of 128 scores a thread and take 208, the third keeps 88 (2 * 208 + 88 = 3 * 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
+constexpr int kLoadK = 8, kMmaWarp = 9, kPlanWarp = 10, kLoadV = 11;
+constexpr int kBarBytes = 1792;  // struct Bars
 constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutCol = 256;
@@ -85,7 +86,7 @@ struct Layout {
     static constexpr int kStages = (224 * 1024 - 2 * kStageBytes) / kStageBytes;
     static constexpr int kRingAt = 2 * kStageBytes;
     static constexpr int kBarsAt = kRingAt + kStages * kStageBytes;
-    static constexpr int kSmem = kBarsAt + 1024 + 1024;  // barriers, and the 1024-byte alignment
+    static constexpr int kSmem = kBarsAt + kBarBytes + 1024;  // barriers, and the 1024-byte alignment
 };
 
 constexpr int kMaxStages = 12;
@@ -95,7 +96,9 @@ struct Entry {
     int b, g, first, count, length;
     int low;                   // first place that any row of the tile sees
     int from, to;              // blocks
-    int begin[2], end[2];      // of them, those that the halves see
+    int ordinal;               // how many blocks of the run come before them
+    int begin[2], end[2];      // of them, those of the halves: every one from begin to end, or every other
+    int paired;                // the halves have the same rows and take turns with the blocks
     int c0, c1;                // the thread blocks that share the tile
     int last;
     int row;                   // first row of the tile
@@ -103,22 +106,25 @@ struct Entry {
 
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];  // ring
-    uint64_t v_clean[kMaxStages];  // the slots past the last place of the v block in a stage are zero
+    uint64_t landed;      // a v block that holds a sequence's last place, before it is cleaned
     uint64_t q_full[2];   // a half's queries are in shared memory
     uint64_t s_full[2];   // a half's scores are in TMEM (and its o is up to date)
     uint64_t p_part[2];   // the first 64 columns of a half's p are in TMEM
     uint64_t p_full[2];   // and all of it
     uint64_t o_done[2];   // a half's o is complete for the tile
+    uint64_t pair_in;     // the first half of a paired tile has left its o and statistics
+    uint64_t pair_out;    // and the second has taken them
     uint64_t part_in[2];  // a half's threads have written their part
     uint64_t part_out[2]; // whether it was the last of its tile is known
     uint64_t work_full[kEntries], work_empty[kEntries];
     uint64_t mma_done;
     Entry work[kEntries];
+    float2 pair_stats[kHalf];
     uint32_t tmem;
     int abort;
     int last[2];
 };
-static_assert(sizeof(Bars) <= 1024, "barriers");
+static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 
 struct TileArgs {
     AttentionArgs a;
@@ -170,8 +176,10 @@ struct Segment {
     Range half0, half1;   // all that the halves see
     int low, block, end;  // of the whole tile; end > block even if nothing is seen
     int from, to;         // the stretch
-    __device__ __forceinline__ int begin_of(int w) const { return max(w ? half1.block : half0.block, from); }
-    __device__ __forceinline__ int end_of(int w) const { return min(w ? half1.end : half0.end, to); }
+    // with no second half of rows, and blocks enough, both halves work on the first
+    __device__ __forceinline__ bool paired(int ratio) const {
+        return s.count * ratio <= tile * kTile + kHalf && end - block > 1;
+    }
 };
 
 __device__ __forceinline__ void set_tile(const AttentionArgs& a, Segment& s) {
@@ -430,8 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < L::kStages; ++i) {
                 ptx::mbar_init(&bars->full[i], 1);
-                ptx::mbar_init(&bars->empty[i], 1);
-                ptx::mbar_init(&bars->v_clean[i], 1);
+                ptx::mbar_init(&bars->empty[i], 2);  // a commit for each half
             }
             for (int w = 0; w < 2; ++w) {
                 ptx::mbar_init(&bars->q_full[w], kHalf);
@@ -444,8 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int i = 0; i < kEntries; ++i) {
                 ptx::mbar_init(&bars->work_full[i], 1);
-                ptx::mbar_init(&bars->work_empty[i], 10);  // load, MMA and softmax warps
+                ptx::mbar_init(&bars->work_empty[i], 12);  // loads, MMAs of the two halves, softmax warps
             }
+            ptx::mbar_init(&bars->landed, 1);
+            ptx::mbar_init(&bars->pair_in, kHalf);
+            ptx::mbar_init(&bars->pair_out, kHalf);
             ptx::mbar_init(&bars->mma_done, 1);
             bars->abort = 0;
             ptx::fence_mbar_init();
@@ -475,9 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
     };
 
-    if (warp >= kLoadWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    }
+    if (warp >= kLoadK) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kPlanWarp) {
         // -------------------------------------------------------------- plan
         int64_t left = run.end - run.begin, unit = run.begin;
@@ -499,10 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 e.low = seg.low;
                 e.from = seg.from;
                 e.to = seg.to;
-                e.begin[0] = seg.begin_of(0);
-                e.begin[1] = seg.begin_of(1);
-                e.end[0] = max(e.begin[0], seg.end_of(0));
-                e.end[1] = max(e.begin[1], seg.end_of(1));
+                e.ordinal = (int)(unit - run.begin);
+                e.paired = seg.paired(ratio);
+                e.begin[0] = max(seg.half0.block, seg.from);
+                e.begin[1] = e.paired ? seg.from + 1 : max(seg.half1.block, seg.from);
+                e.end[0] = min(seg.half0.end, seg.to);
+                e.end[1] = e.paired ? e.end[0] : min(seg.half1.end, seg.to);
                 const int64_t item = unit - (seg.from - seg.block);
                 e.c0 = run.shares.owner(item, blockIdx.x);
                 e.c1 = run.shares.owner(item + (seg.end - seg.block) - 1, blockIdx.x);
@@ -515,67 +525,86 @@ __global__ void __launch_bounds__(kThreads, 1)
             next_segment(x, left, seg);
         }
         if (!ok && lane == 0) fail(x, bars);
-    } else if (warp == kLoadWarp) {
+    } else if (warp == kLoadK || warp == kLoadV) {
         // ------------------------------------------------------------- loads
+        // k blocks are the ring's even entries, v blocks the odd ones
+        const bool values = warp == kLoadV;
+        const CUtensorMap* map = values ? &map_v : &map_k;
         const int pieces = kBlock / x.box;
         const int piece = lane / L::kSlabs, slab = lane % L::kSlabs;
-        int issued = 0;
-        // v block `dirty` (its number in the ring's order; -1: none): slots past
-        // the last place are zeroed once it is there, as 0 times what they hold might not be 0
+        int n = 0, issued = -1;
+        // The v block of a sequence's last place lands on a barrier of its own; then
+        // its slots past that place are zeroed (0 times what they hold might not be 0),
+        // and only then is it handed on. Other copies go out meanwhile, but nothing
+        // is waited for before that.
         int dirty = -1, dirty_row = 0, dirty_rows = 0;
+        uint32_t landed_parity = 0;
         auto clean = [&] {
-            const int st = dirty % L::kStages;
-            ok = ok && wait_bar(&bars->full[st], (dirty / L::kStages) & 1, abort, wait_limit());
+            ok = ok && wait_bar(&bars->landed, landed_parity, abort, wait_limit());
             ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
-                for (int c = lane; c < dirty_rows * (D / 8); c += 32) {
-                    const int row = dirty_row + c / (D / 8), part = c % (D / 8);
-                    *reinterpret_cast<uint4*>(ring + st * L::kStageBytes + (part >> 3) * L::kSlabBytes + row * 128 +
-                                              (part & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                ptx::fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->v_clean[st]);
+            if (!ok) return;
+            landed_parity ^= 1u;
+            const int st = dirty % L::kStages;
+            for (int c = lane; c < dirty_rows * (D / 8); c += 32) {
+                const int row = dirty_row + c / (D / 8), part = c % (D / 8);
+                *reinterpret_cast<uint4*>(ring + st * L::kStageBytes + (part >> 3) * L::kSlabBytes + row * 128 +
+                                          (part & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
+            ptx::fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->full[st]);
             dirty = -1;
         };
-        for (int k = 0; entry(k); ++k) {
+        auto wait_clean = [&](uint64_t* bar, uint32_t parity) {
+            if (__all_sync(0xffffffffu, ok && ptx::mbar_try_wait(bar, parity))) return true;
+            if (dirty >= 0) clean();
+            ok = ok && wait_bar(bar, parity, abort, wait_limit());
+            ok = __all_sync(0xffffffffu, ok);
+            return ok;
+        };
+        for (int k = 0; wait_clean(&bars->work_full[k % kEntries], (k / kEntries) & 1); ++k) {
             const Entry& e = bars->work[k % kEntries];
             const int to = e.to, length = e.length, low = e.low, b = e.b, g = e.g;
-            for (int j = e.from; ok && j < to; ++j) {
+            const bool last = e.last;
+            // this lane's page piece of block j; outside the cache: zeros
+            auto page_at = [&](int j) {
                 const int p = j * kBlock + piece * x.box;
-                int64_t page = a.c.pages;  // outside the cache: zeros
-                if (piece < pieces && p < length && p + x.box > low) {
-                    page = page_of(a.c, b, p);
-                    if (page < 0) page = a.c.pages;
-                }
+                int64_t page = -1;
+                if (piece < pieces && j < to && p < length && p + x.box > low) page = page_of(a.c, b, p);
+                return (int)(page < 0 ? a.c.pages : page);
+            };
+            int page = page_at(e.from);
+            for (int j = e.from; ok && j < to; ++j) {
+                const int next_page = page_at(j + 1);
+                // Both of a block's stages are waited for in the ring's order, the other
+                // warp's too: a barrier's parity tells only its next phase from the one before.
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int st = issued % L::kStages, round = issued / L::kStages;
-                    if (dirty >= 0 && round > 0 &&
-                        !__all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->empty[st], (round - 1) & 1)))
-                        clean();
-                    ok = ok && may_issue(issued) &&
-                         (round == 0 || wait_bar(&bars->empty[st], (round - 1) & 1, abort, wait_limit()));
-                    ok = __all_sync(0xffffffffu, ok);
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int st = n % L::kStages, round = n / L::kStages;
+                    if (round > 0 && !wait_clean(&bars->empty[st], (round - 1) & 1)) break;
+                    if (kv != (values ? 1 : 0)) continue;
+                    ok = may_issue(n);
                     if (!ok) break;
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->full[st], L::kStageBytes);
+                    const int rows = values ? tail_rows(length - j * kBlock, x.box) : 0;
+                    if (rows > 0 && dirty >= 0) {
+                        clean();
+                        if (!ok) break;
+                    }
+                    uint64_t* bar = rows > 0 ? &bars->landed : &bars->full[st];
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
                     __syncwarp();
                     if (piece < pieces)
-                        tma_load_4d(ring + st * L::kStageBytes + slab * L::kSlabBytes + piece * x.box * 128,
-                                    kv ? &map_v : &map_k, &bars->full[st], slab * 64, a.c.by_page.remainder(p), g,
-                                    (int)page);
-                    ++issued;
+                        tma_load_4d(ring + st * L::kStageBytes + slab * L::kSlabBytes + piece * x.box * 128, map, bar,
+                                    slab * 64, a.c.by_page.remainder(j * kBlock + piece * x.box), g, page);
+                    issued = n;
+                    if (rows > 0) {
+                        dirty = n;
+                        dirty_row = length - j * kBlock;
+                        dirty_rows = rows;
+                    }
                 }
-                const int past = length - j * kBlock, rows = tail_rows(past, x.box);
-                if (ok && rows > 0) {
-                    if (dirty >= 0) clean();
-                    dirty = issued - 1;
-                    dirty_row = past;
-                    dirty_rows = rows;
-                }
+                page = next_page;
             }
-            const bool last = e.last;
             done_with(k);
             if (!ok || last) break;
         }
@@ -583,8 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) {
             fail(x, bars);
             volatile int never = 0;  // our own copies land before the thread block ends
-            for (int i = max(0, issued - L::kStages); i < issued; ++i)
-                wait_bar(&bars->full[i % L::kStages], (i / L::kStages) & 1, &never, kDrainLimitNs);
+            if (dirty >= 0) wait_bar(&bars->landed, landed_parity, &never, kDrainLimitNs);
+            for (int i = issued; i >= 0 && i > issued - L::kStages; i -= 2)
+                if (i != dirty)
+                    wait_bar(&bars->full[i % L::kStages], (i / L::kStages) & 1, &never, kDrainLimitNs);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -628,99 +659,92 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (last) ptx::mma_commit(&bars->o_done[w]);
                 return true;
             };
-            // what a block needs of its entry
-            struct View {
-                int to, length, begin0, end0, begin1, end1, last;
-            };
-            auto view = [&](int k) {
-                const Entry& e = bars->work[k % kEntries];
-                return View{e.to, e.length, e.begin[0], e.end[0], e.begin[1], e.end[1], e.last};
-            };
-            auto advance = [](uint32_t& st, uint32_t& parity) {
-                if (++st == L::kStages) {
-                    st = 0;
-                    parity ^= 1u;
-                }
-            };
-            int k = 0;                                // entry of the block whose p v comes next
-            int j = 0, i = 0;                         // that block, and the one whose scores come next
-            uint32_t vst = 0, vparity = 0, kst = 0, kparity = 0;  // their ring stages
-            uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0, clean_parities = 0;
-            bool turn = false, more = true;           // the two are of different entries; there is a second one
-            View cur{}, nxt{};
-            auto plan = [&] {
-                vst = kst;
-                vparity = kparity;
-                advance(vst, vparity);
-                kst = vst;
-                kparity = vparity;
-                advance(kst, kparity);
-                i = j + 1;
-                turn = i == cur.to;
-                more = !turn || !cur.last;
-                if (turn && more && wait(&bars->work_full[(k + 1) % kEntries], ((k + 1) / kEntries) & 1)) {
-                    nxt = view(k + 1);
-                    i = bars->work[(k + 1) % kEntries].from;
-                }
-            };
-            if (wait(&bars->work_full[0], 0)) {  // the first block's scores
-                cur = nxt = view(0);
-                j = bars->work[0].from;
-                wait(&bars->full[0], 0);
-                if (ok && j >= cur.begin0 && j < cur.end0 && wait(&bars->q_full[0], 0)) {
-                    scores(0, 0);
-                    q_parity0 = 1;
-                }
-                if (ok && j >= cur.begin1 && j < cur.end1 && wait(&bars->q_full[1], 0)) {
-                    scores(1, 0);
-                    q_parity1 = 1;
-                }
-                ptx::mma_commit(&bars->empty[0]);
-                plan();
-            }
-            while (ok) {
-                if (!wait(&bars->full[vst], vparity)) break;
-                if (tail_rows(cur.length - j * kBlock, x.box) > 0) {
-                    if (!wait(&bars->v_clean[vst], clean_parities >> vst & 1u)) break;
-                    clean_parities ^= 1u << vst;
-                }
-                if (j >= cur.begin0 && j < cur.end0) {
-                    if (!output(0, vst, p_parity0, j == cur.begin0, j == cur.end0 - 1)) break;
-                    p_parity0 ^= 1u;
-                }
-                if (more) {
-                    if (!wait(&bars->full[kst], kparity)) break;
-                    if (i >= nxt.begin0 && i < nxt.end0) {
-                        if (i == nxt.begin0) {
-                            if (!wait(&bars->q_full[0], q_parity0)) break;
-                            q_parity0 ^= 1u;
+            // The two halves are two streams of blocks: each has its next scores formed as
+            // soon as its last p is used up. The one that is further behind goes first, and neither
+            // passes the other by more than two blocks, so that what one waits for never
+            // depends on what the other has yet to do. Every block of the run is waited
+            // for and given back once by each, in order, whether the half sees it or not.
+            struct Stream {
+                int k = -1, j = 0, to = 0;          // entry, block, and the end of the entry's blocks
+                int begin = 0, end = 0, step = 1;   // the half's blocks of the entry
+                int shift = 0;                      // from block to place in the run
+                bool last = false, more = true;
+                bool formed = false;                // the block's scores are on their way
+                uint32_t q_parity = 0, p_parity = 0;
+                __device__ __forceinline__ int at() const { return j + shift; }
+            } s0, s1;
+            auto release = [&](int n) { ptx::mma_commit(&bars->empty[n % L::kStages]); };
+            auto here = [&](int n) { return ptx::mbar_try_wait(&bars->full[n % L::kStages], (n / L::kStages) & 1); };
+            // towards the half's next block, as far as that goes without waiting
+            auto advance = [&](int w, Stream& s, const Stream& other) {
+                bool moved = false;
+                while (s.more && !s.formed) {
+                    if (s.j == s.to) {
+                        if (s.last) {
+                            ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
+                            s.more = false;
+                            return true;
                         }
-                        scores(0, kst);
+                        const int k = s.k + 1;
+                        if (!ptx::mbar_try_wait(&bars->work_full[k % kEntries], (k / kEntries) & 1)) return moved;
+                        if (k > 0) ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
+                        const Entry& e = bars->work[k % kEntries];
+                        s.k = k;
+                        s.j = e.from;
+                        s.to = e.to;
+                        s.begin = e.begin[w];
+                        s.end = e.end[w];
+                        s.step = e.paired ? 2 : 1;
+                        s.shift = e.ordinal - e.from;
+                        s.last = e.last;
+                        moved = true;
                     }
+                    const int n = 2 * s.at();
+                    if ((other.more && s.at() > other.at() + 2) || !here(n)) return moved;
+                    if (s.j >= s.begin && s.j < s.end && ((s.j - s.begin) & (s.step - 1)) == 0) {
+                        if (s.j == s.begin) {
+                            if (!ptx::mbar_try_wait(&bars->q_full[w], s.q_parity)) return moved;
+                            s.q_parity ^= 1u;
+                        }
+                        ptx::tc_fence_after();
+                        scores(w, n % L::kStages);
+                        release(n);
+                        s.formed = true;
+                        return true;
+                    }
+                    if (!here(n + 1)) return moved;
+                    release(n);
+                    release(n + 1);
+                    ++s.j;
+                    moved = true;
                 }
-                if (j >= cur.begin1 && j < cur.end1) {
-                    if (!output(1, vst, p_parity1, j == cur.begin1, j == cur.end1 - 1)) break;
-                    p_parity1 ^= 1u;
+                return moved;
+            };
+            auto add_values = [&](int w, Stream& s) {
+                const int n = 2 * s.at() + 1;
+                if (!here(n) || !output(w, n % L::kStages, s.p_parity, s.j == s.begin, s.j + s.step >= s.end))
+                    return false;
+                s.p_parity ^= 1u;
+                release(n);
+                ++s.j;
+                s.formed = false;
+                return true;
+            };
+            uint64_t since = 0;
+            int idle = 0;
+            while (ok && (s0.more || s1.more)) {
+                bool moved = s0.formed && (!s1.formed || s0.at() <= s1.at()) && add_values(0, s0);
+                if (!moved && s1.formed) moved = add_values(1, s1);
+                moved |= advance(0, s0, s1);
+                moved |= advance(1, s1, s0);
+                if (moved) {
+                    idle = 0;
+                    since = 0;
+                } else if ((++idle & 31) == 0) {  // bounded, like every wait
+                    const uint64_t now = ptx::globaltimer_ns();
+                    if (since == 0) since = now;
+                    if (*abort || now - since > wait_limit()) ok = false;
                 }
-                ptx::mma_commit(&bars->empty[vst]);
-                if (!more) break;
-                // the round after this one, while the products above are queued
-                const bool second = i >= nxt.begin1 && i < nxt.end1;
-                if (second && i == nxt.begin1) {
-                    if (!wait(&bars->q_full[1], q_parity1)) break;
-                    q_parity1 ^= 1u;
-                }
-                const uint32_t st = kst;
-                if (turn) {
-                    ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
-                    ++k;
-                    cur = nxt;
-                }
-                j = i;
-                plan();
-                if (!ok) break;
-                if (second) scores(1, st);
-                ptx::mma_commit(&bars->empty[st]);
             }
             if (!ok) fail(x, bars);
             ptx::mma_commit(&bars->mma_done);
@@ -728,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_bar(&bars->mma_done, 0, &never, kDrainLimitNs);
         }
         __syncwarp();
-    } else if (warp < kLoadWarp) {
+    } else {
         // ----------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int w = warp >> 2;
@@ -736,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_addr = lane_base + w * kBlock, o_addr = lane_base + kOutCol + w * D;
         const uint32_t q_smem = ptx::smem_u32(smem) + w * L::kStageBytes;
-        int ns = 0, no = 0, nj = 0;
+        int ns = 0, no = 0, nj = 0, npair = 0;
         // this half's queries of an entry, 16 bytes a lane; rows past the sequence's are zeros
         auto load_q = [&](const Entry& e) {
             constexpr int kPieces = D / 8, kRowsPer = 32 / kPieces;
@@ -744,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
             for (int i = 0; i < 32 / kRowsPer; ++i) {
                 const int r = (warp & 3) * 32 + i * kRowsPer + lane / kPieces;
-                const int at = e.row + w * kHalf + r;
+                const int at = e.row + (e.paired ? 0 : w * kHalf) + r;
                 const int token = a.by_ratio.quotient(at);
                 const bool real = token < e.count;
                 const uint16_t* src =
@@ -768,10 +792,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Entry& e = bars->work[k % kEntries];
             const Entry& next = bars->work[(k + 1) % kEntries];
             const bool last = e.last;
-            const int begin = e.begin[w], end = e.end[w];
+            const int begin = e.begin[w], end = e.end[w], step = e.paired ? 2 : 1;
+            const int first_row = e.row + (e.paired ? 0 : w * kHalf);
             int low, high;
             {
-                const int token = a.by_ratio.quotient(e.row + w * kHalf + row);
+                const int token = a.by_ratio.quotient(first_row + row);
                 const int place = e.length - e.count + token;
                 low = a.window > 0 ? max(0, place - a.window + 1) : 0;
                 high = token >= e.count ? 0 : a.causal ? min(e.length, place + 1) : e.length;
@@ -779,13 +804,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool load_next = false;
             float m = -INFINITY;
             float2 sum = make_float2(0.0f, 0.0f);
-            for (int j = begin; j < end; ++j) {
+            for (int j = begin; j < end; j += step) {
                 if (!wait_bar(&bars->s_full[w], ns & 1, abort, wait_limit())) ok = false;
                 ++ns;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                if (j == end - 1 && !last) {  // the last scores are formed: q may go
+                if (j + step >= end && !last) {  // the last scores are formed: q may go
                     if (!entry(k + 1)) break;
                     load_next = next.end[w] > next.begin[w];
                     if (load_next) load_q(next);
@@ -854,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            if (begin == end && !last) {
+            if (begin >= end && !last) {
                 if (!entry(k + 1)) break;
                 load_next = next.end[w] > next.begin[w];
                 if (load_next) load_q(next);
@@ -868,8 +893,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ptx::tc_fence_after();
             }
-            const float l = sum.x + sum.y;
-            const int at = e.row + w * kHalf + row;
+            float l = sum.x + sum.y;
+            // A paired tile: the second half adds the first one's o, straight from its TMEM columns.
+            float scale = 1.0f, scale0 = 0.0f;
+            if (e.paired) {
+                if (w == 0) {
+                    bars->pair_stats[row] = make_float2(m, l);
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&bars->pair_in);
+                }
+                if (!wait_bar(w == 0 ? &bars->pair_out : &bars->pair_in, npair & 1, abort, wait_limit())) ok = false;
+                ++npair;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (w == 0) {
+                    done_with(k);
+                    if (last) break;
+                    continue;
+                }
+                const float2 other = bars->pair_stats[row];
+                const float top = fmaxf(m, other.x);
+                scale = m == -INFINITY ? 0.0f : fast_exp2(m - top);
+                scale0 = other.x == -INFINITY ? 0.0f : fast_exp2(other.x - top);
+                m = top;
+                l = l * scale + other.y * scale0;
+            }
+            const int at = first_row + row;
             const int token = a.by_ratio.quotient(at);
             const bool real = token < e.count;
             const int64_t out_row = (int64_t)(e.first + token) * a.heads + e.g * ratio + at - token * ratio;
@@ -897,7 +947,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_ld_wait();
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = end > begin ? __uint_as_float(r[i]) : 0.0f;
+                for (int i = 0; i < 32; ++i) v[i] = end > begin ? __uint_as_float(r[i]) * scale : 0.0f;
+                if (e.paired) {
+                    ptx::tmem_ld_32x32b_x32(o_addr - D + d, r);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[i]) * scale0;
+                }
                 if (c0 == c1) {
                     if (real) write32(d, v, inv);
                 } else {
@@ -907,16 +963,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ptx::tc_fence_before();  // o may be overwritten once the next p is announced
+            if (e.paired) ptx::mbar_arrive(&bars->pair_out);
             if (c0 == c1) {
                 if (real) write_lse(m, l);
             } else {
                 __stcg(x.stats + slot * kTile + w * kHalf + row, make_float2(m, l));
                 __threadfence();
                 ptx::mbar_arrive(&bars->part_in[w]);
+                int* counter = x.counters + 2 * c0 + w;
                 if (row == 0 && wait_bar(&bars->part_in[w], nj & 1, abort, wait_limit())) {
-                    const int done = ptx::atom_add_acq_rel_gpu(x.counters + 2 * c0 + w, 1);
+                    const int done = ptx::atom_add_acq_rel_gpu(counter, 1);
                     bars->last[w] = done == c1 - c0;
-                    if (bars->last[w]) x.counters[2 * c0 + w] = 0;
+                    if (bars->last[w]) *counter = 0;
                     ptx::mbar_arrive(&bars->part_out[w]);
                 }
                 __syncwarp();
@@ -926,11 +984,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (bars->last[w]) {
                     __threadfence();
-                    const float2* st = x.stats + w * kHalf + row;
+                    const int parts = c1 - c0 + 1;  // of thread blocks c0 to c1: the first one's last tile, the others' first
+                    auto slot_of = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0)); };
+                    auto stats = [&](int i) { return __ldcg(x.stats + slot_of(i) * kTile + w * kHalf + row); };
                     float top = -INFINITY, total = 0.0f;
-                    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(st + (2 * c + (c == c0)) * kTile).x);
-                    for (int c = c0; c <= c1; ++c) {
-                        const float2 v = __ldcg(st + (2 * c + (c == c0)) * kTile);
+#pragma unroll 4
+                    for (int i = 0; i < parts; ++i) top = fmaxf(top, stats(i).x);
+#pragma unroll 4
+                    for (int i = 0; i < parts; ++i) {
+                        const float2 v = stats(i);
                         total += v.x == -INFINITY ? 0.0f : v.y * fast_exp2(v.x - top);
                     }
                     const float inv_total = total > 0.0f || total != total ? 1.0f / total : 0.0f;
@@ -939,13 +1001,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                        for (int c = c0; c <= c1; ++c) {
-                            const int64_t part = 2 * c + (c == c0);
-                            const float mc = __ldcg(st + part * kTile).x;
+#pragma unroll 2
+                        for (int i = 0; i < parts; ++i) {
+                            const float mc = stats(i).x;
                             const float f = mc == -INFINITY ? 0.0f : fast_exp2(mc - top);
-                            const float* src = x.parts + (part * D + d) * kTile + w * kHalf + row;
+                            const float* src = x.parts + (slot_of(i) * D + d) * kTile + w * kHalf + row;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += f * __ldcg(src + i * kTile);
+                            for (int c = 0; c < 32; ++c) v[c] += f * __ldcg(src + c * kTile);
                         }
                         if (real) write32(d, v, inv_total);
                     }
