@@ -5,8 +5,8 @@
 // out = softmax(c q k^T) v in one pass: with m the running maximum of a row's
 // scores s and p_j = 2^(s_j - m), both l = sum p_j and o = sum p_j v_j are
 // multiplied by 2^(m - m') when the maximum moves to m'. The maximum only
-// moves when a score passes it by more than 8, so p stays below 2^8, far
-// inside fp16's range, and the multiplication is rare; out = o / l is the same for any m.
+// moves when a score passes it by E::kSlack, which keeps p inside the element
+// type and makes the multiplication rare; out = o / l is the same for any m.
 //
 // What bounds it is reading the cache once: 2 D 16-bit elements of k and v per place and
 // cached head, against 4 D operations for each row. So the work is spread over
@@ -37,7 +37,6 @@ constexpr int kBlock = kWarps * kStep;  // places per block of the work list
 constexpr int kBlocksPerSm = 2;
 constexpr int kLeast = 1;               // blocks of a run, if the list has fewer than every SM could take
 constexpr int kRingBytes = 24 * 1024;   // per warp
-constexpr float kSlack = 8.0f;          // how far a score may pass the running maximum (log2)
 
 template <int D>
 struct Layout {
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                 float v = (s[0][n][i] + s[1][n][i]) * a.scale_log2;
                 if (p < low[n][i & 1] || p >= high[n][i & 1]) v = -INFINITY;
                 s[0][n][i] = v;
-                rise = rise || v > m[n][i & 1] + kSlack;
+                rise = rise || v > m[n][i & 1] + E::kSlack;
             }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll

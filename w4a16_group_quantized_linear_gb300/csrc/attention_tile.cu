@@ -5,8 +5,9 @@
 //
 // One pass over the places with the running maximum m and sum l of the
 // softmax: p = 2^(c s - m), l += sum p, o = o 2^(m - m') + p v whenever m moves
-// to m', which it only does when a score passes it by more than 8 (so p stays
-// below 2^8 and the read-scale-write of o is rare; out = o / l whatever m is).
+// to m', which it only does when a score passes it by E::kSlack (which keeps p
+// inside the element type and makes the read-scale-write of o rare; out = o / l
+// whatever m is).
 //
 // 4 D operations per (row, place) bound it: per block of 128 places and
 // half tile of 128 rows two 128 x 128 x D products, 512 cycles each at D = 128,
@@ -62,7 +63,6 @@ constexpr int kBarBytes = 1792;  // struct Bars
 constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutCol = 256;
-constexpr float kSlack = 8.0f;   // how far a score may pass the running maximum (log2)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 
@@ -566,21 +566,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Entry& e = bars->work[k % kEntries];
             const int to = e.to, length = e.length, low = e.low, b = e.b, g = e.g;
             const bool last = e.last;
-            // this lane's page piece of block j; outside the cache: zeros
-            auto page_at = [&](int j) {
-                const int p = j * kBlock + piece * x.box;
+            // the pages of 32 pieces, a lane each, read a group ahead; outside the cache: zeros
+            auto pages_from = [&](int first) {
+                const int p = (first + lane) * x.box;
                 int64_t page = -1;
-                if (piece < pieces && j < to && p < length && p + x.box > low) page = page_of(a.c, b, p);
+                if (p < length && p + x.box > low && p < to * kBlock) page = page_of(a.c, b, p);
                 return (int)(page < 0 ? a.c.pages : page);
             };
-            int page = page_at(e.from);
+            int group = e.from * pieces;  // its first piece
+            int pages = pages_from(group), more_pages = pages_from(group + 32);
             for (int j = e.from; ok && j < to; ++j) {
-                const int next_page = page_at(j + 1);
+                if (j * pieces >= group + 32) {
+                    group += 32;
+                    pages = more_pages;
+                    more_pages = pages_from(group + 32);
+                }
+                const int page = __shfl_sync(0xffffffffu, pages, j * pieces - group + (piece & (pieces - 1)));
                 // Both of a block's stages are waited for in the ring's order, the other
                 // warp's too: a barrier's parity tells only its next phase from the one before.
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++n) {
                     const int st = n % L::kStages, round = n / L::kStages;
+                    if (dirty >= 0 && __all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->landed, landed_parity))) clean();
                     if (round > 0 && !wait_clean(&bars->empty[st], (round - 1) & 1)) break;
                     if (kv != (values ? 1 : 0)) continue;
                     ok = may_issue(n);
@@ -603,7 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dirty_rows = rows;
                     }
                 }
-                page = next_page;
             }
             done_with(k);
             if (!ok || last) break;
@@ -822,10 +828,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int lo = low - j * kBlock, hi = high - j * kBlock;
                 if (__any_sync(0xffffffffu, lo > 0 || hi < kBlock)) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        if (!__any_sync(0xffffffffu, lo > c * 32 || hi < c * 32 + 32)) continue;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (c * 32 + i < lo || c * 32 + i >= hi) s[c][i] = 0xFF800000u;  // -infinity
+                    }
                 }
                 float top = __uint_as_float(s[0][0]), top2 = __uint_as_float(s[0][1]);
 #pragma unroll
@@ -836,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top2 = max3(top2, __uint_as_float(s[c][i + 2]), __uint_as_float(s[c][i + 3]));
                     }
                 top = fmaxf(top, top2) * a.scale_log2;
-                if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                if (__any_sync(0xffffffffu, top > m + E::kSlack)) {
                     top = fmaxf(top, m);
                     const float keep = m == -INFINITY ? 0.0f : fast_exp2(m - top);
                     m = top;
