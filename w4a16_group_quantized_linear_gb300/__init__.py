@@ -19,6 +19,7 @@ Build it with ``python -m w4a16_group_quantized_linear_gb300.build`` (or
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -424,6 +425,11 @@ def moe_combine(y_sorted: torch.Tensor, row_of: torch.Tensor, topk_weights: torc
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace_bytes(index: int, T: int, B: int, H: int, G: int, D: int, max_q_len: int) -> int:
+    return int(lib().w4a16_paged_attention_workspace_bytes(T, B, H, G, D, max_q_len))
+
+
 def rope_table(rows: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """The angles of :func:`rope` and :func:`kv_append`: fp32 [rows, rotary_dim],
     cos(p * base^(-2i / rotary_dim)) for pair i in the first half of row p and
@@ -626,7 +632,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
     st = _raw_stream(index)
     h = _lib or lib()
-    need = h.w4a16_paged_attention_workspace_bytes(T, B, H, G, D, max_q_len)
+    need = _attention_workspace_bytes(index, T, B, H, G, D, max_q_len)
     ws = _ws.get((index, st, "attention"))
     if need and (ws is None or ws.numel() < need):
         ws = _workspace(q.device, ctypes.c_void_p(st), need, "attention")

@@ -95,13 +95,22 @@ __device__ __forceinline__ int sequence_of(const CacheArgs& c, int64_t t, int& f
         count = __ldg(c.q_offsets + b + 1) - first;
         if (first == t && count == 1) return b;
     }
-    int lo = 0, hi = c.batch - 1;  // the last b with q_offsets[b] <= t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(c.q_offsets + mid) <= t) lo = mid;
-        else hi = mid - 1;
+    // the last b with q_offsets[b] <= t, for the warp's first token: 32 candidates at a time
+    const int lane = threadIdx.x & 31;
+    const unsigned active = __activemask();
+    const int64_t t0 = __shfl_sync(active, t, __ffs(active) - 1);
+    int lo = 0, width = c.batch;  // it is in [lo, lo + width)
+    while (width > 1) {
+        const int step = (width + 31) / 32;
+        const int at = lo + lane * step;
+        const bool le = at < lo + width && __ldg(c.q_offsets + at) <= t0;
+        const unsigned hits = __ballot_sync(active, le);
+        const int last = hits ? 31 - __clz(hits) : 0;
+        width = min(step, width - last * step);
+        lo += last * step;
     }
     b = lo;
+    while (b + 1 < c.batch && __ldg(c.q_offsets + b + 1) <= t) ++b;  // this thread's, a token or two on
     first = __ldg(c.q_offsets + b);
     const int next = __ldg(c.q_offsets + b + 1);
     count = next - first;

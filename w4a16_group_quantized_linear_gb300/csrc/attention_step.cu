@@ -35,7 +35,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;               // places per warp step
 constexpr int kBlock = kWarps * kStep;  // places per block of the work list
 constexpr int kBlocksPerSm = 2;
-constexpr int kLeast = 1;               // blocks of a run, if the list has fewer than every SM could take
 constexpr int kRingBytes = 24 * 1024;   // per warp
 
 template <int D>
@@ -125,11 +124,10 @@ __device__ __forceinline__ void load_sequence(const AttentionArgs& a, int b, int
 
 // This thread block's run of `total` units.
 __device__ __forceinline__ void share_out(int64_t total, Shares& shares, int64_t& begin, int64_t& end) {
-    const int runs = (int)min((int64_t)gridDim.x, (total + kLeast - 1) / kLeast);
-    shares.base = runs ? total / runs : 0;
-    shares.more = runs ? (int)(total - shares.base * runs) : 0;
-    begin = blockIdx.x < runs ? shares.start(blockIdx.x) : total;
-    end = blockIdx.x < runs ? shares.start(blockIdx.x + 1) : total;
+    shares.base = total / gridDim.x;
+    shares.more = (int)(total - shares.base * gridDim.x);
+    begin = shares.start(blockIdx.x);
+    end = shares.start(blockIdx.x + 1);
 }
 
 // A position in the work list, as a warp walks it.
@@ -459,26 +457,47 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         __syncthreads();
         if (!s_last) return;
         __threadfence();
-        for (int i = tid; i < rows * L::kChunks; i += kThreads) {
-            const int r = i / L::kChunks, d = i % L::kChunks * 8;
+        // a thread per 8 elements of a row; the parts' statistics by way of shared memory, 64 parts at a time
+        float2* stats = reinterpret_cast<float2*>(join);  // [64][rows]
+        static_assert(64 * kRows * sizeof(float2) <= L::kJoinBytes, "statistics of 64 parts");
+        for (int i0 = 0; i0 < rows * L::kChunks; i0 += kThreads) {
+            const int i = i0 + tid;
+            const bool mine = i < rows * L::kChunks;
+            const int r = mine ? i / L::kChunks : 0, d = i % L::kChunks * 8;
             float top = -INFINITY, sum = 0.0f, acc[8];
-#pragma unroll 8
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(arg.stats + (2 * c + (c == c0)) * kRows + r).x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+            for (int p0 = c0; p0 <= c1; p0 += 64) {
+                const int n = min(64, c1 + 1 - p0);
+                auto slot_of = [&](int k) { return (int64_t)(2 * (p0 + k) + (p0 + k == c0)); };
+                __syncthreads();
+                for (int k = tid; k < n * rows; k += kThreads) {
+                    const int part = k / rows, row = k - part * rows;
+                    stats[part * kRows + row] = __ldcg(arg.stats + slot_of(part) * kRows + row);
+                }
+                __syncthreads();
+                if (!mine) continue;
+                float higher = top;
+                for (int k = 0; k < n; ++k) higher = fmaxf(higher, stats[k * kRows + r].x);
+                const float keep = top == -INFINITY ? 0.0f : fast_exp2(top - higher);
+                top = higher;
+                sum *= keep;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] *= keep;
 #pragma unroll 8
-            for (int c = c0; c <= c1; ++c) {
-                const int64_t part = (2 * c + (c == c0)) * kRows + r;
-                const float2 st = __ldcg(arg.stats + part);
-                const float4* src = reinterpret_cast<const float4*>(arg.parts + part * D + d);
-                const float4 x = __ldcg(src), y = __ldcg(src + 1);
-                const float f = st.x == -INFINITY ? 0.0f : fast_exp2(st.x - top);
-                sum += st.y * f;
-                acc[0] += x.x * f; acc[1] += x.y * f; acc[2] += x.z * f; acc[3] += x.w * f;
-                acc[4] += y.x * f; acc[5] += y.y * f; acc[6] += y.z * f; acc[7] += y.w * f;
+                for (int k = 0; k < n; ++k) {
+                    const float4* src = reinterpret_cast<const float4*>(arg.parts + (slot_of(k) * kRows + r) * D + d);
+                    const float4 x = __ldcg(src), y = __ldcg(src + 1);
+                    const float2 st = stats[k * kRows + r];
+                    const float f = st.x == -INFINITY ? 0.0f : fast_exp2(st.x - top);
+                    sum += st.y * f;
+                    acc[0] += x.x * f; acc[1] += x.y * f; acc[2] += x.z * f; acc[3] += x.w * f;
+                    acc[4] += y.x * f; acc[5] += y.y * f; acc[6] += y.z * f; acc[7] += y.w * f;
+                }
             }
-            write_row(r, d, acc, top, sum);
+            if (mine) write_row(r, d, acc, top, sum);
         }
+        __syncthreads();  // the shared arrays are free again
     };
 
     // -------------------------------------------------------------- the run --

@@ -437,12 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ratio = a.ratio;
 
-    ptx::grid_dependency_wait();
-    ptx::launch_dependents();
-    if (blockIdx.x == 0) check_offsets(a.c);
-    Run run;
-    Segment seg;
-    if (!find_run(x, reinterpret_cast<int*>(ring), run, seg)) return;  // the same for all threads
+    // what does not depend on the kernel before this one
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < L::kStages; ++i) {
@@ -476,13 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_relinquish();
         if (lane == 0) W4A16_COUNT_TMEM(tmem_allocs);
     }
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    if (blockIdx.x == 0) check_offsets(a.c);
+    Run run;
+    Segment seg;
+    bool ok = find_run(x, reinterpret_cast<int*>(ring), run, seg);  // false, for all threads: nothing to do
     ptx::fence_proxy_async_shared();  // the scratch above was the ring's memory
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem;
     volatile int* abort = &bars->abort;
-    bool ok = true;
+    const bool idle = !ok;
     // entry k of the work, for this warp to read; false if it gave up
     auto entry = [&](int k) {
         if (ok && !wait_bar(&bars->work_full[k % kEntries], (k / kEntries) & 1, abort, wait_limit())) ok = false;
@@ -494,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
     };
 
-    if (warp == kPlanWarp) {
+    if (idle) {
+        // straight to the end
+    } else if (warp == kPlanWarp) {
         // -------------------------------------------------------------- plan
         int64_t left = run.end - run.begin, unit = run.begin;
         for (int k = 0; ok; ++k) {
