@@ -44,7 +44,7 @@ w4a16_status check_cache(const w4a16_paged_cache* c, int64_t T) {
         c->page_table_stride < 0)
         return W4A16_ERR_INVALID_ARG;
     if (T == 0) return W4A16_OK;
-    if (c->batch == 0 || !c->k || !c->v || !c->page_table || !c->q_offsets || !c->kv_lens)
+    if (c->batch == 0 || c->pages == 0 || !c->k || !c->v || !c->page_table || !c->q_offsets || !c->kv_lens)
         return W4A16_ERR_INVALID_ARG;
     if (!aligned16(c->k) || !aligned16(c->v)) return W4A16_ERR_MISALIGNED;
     return W4A16_OK;
