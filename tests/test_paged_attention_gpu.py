@@ -487,3 +487,34 @@ def test_workspace_refusals(w4, cuda_device):
 
     assert call(None, 0) == 7
     assert call(w4._ptr(out), need - 1) == 7
+
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("H,G,D,page", [(10, 1, 128, 16), (10, 1, 64, 48), (24, 2, 128, 128), (32, 1, 128, 32)])
+def test_some_rows_over_long_sequences(w4, cuda_device, H, G, D, page, window):
+    """A few to 128 rows per cached head over thousands of places: blocks are shared out between
+    the halves of a tile and between thread blocks; several tiles to a thread block."""
+    r = np.random.default_rng(D + page + window)
+    most = 128 // (H // G)
+    lens = [(int(n), int(n + c)) for n, c in zip(r.integers(1, most + 1, 20), r.integers(0, 5000, 20))]
+    b = Batch(cuda_device, "fp16", H, G, D, page, lens, seed=page)
+    out, lse = w4.paged_attention(*b.args(), b.max_q, window=window, return_lse=True)
+    b.check(out, lse, window=window)
+
+
+@pytest.mark.parametrize("H,G,D", [(10, 1, 64), (16, 2, 128), (32, 1, 128)])
+def test_some_rows_of_many_short_sequences(w4, cuda_device, H, G, D):
+    """One to four blocks each: tiles of one block and of several follow each other in every order."""
+    r = np.random.default_rng(H + D)
+    most = 128 // (H // G)
+    lens = [(int(n), int(n + c)) for n, c in zip(r.integers(0, most + 1, 260), r.integers(0, 450, 260))]
+    b = Batch(cuda_device, "bf16", H, G, D, 16, lens, seed=D)
+    b.check(w4.paged_attention(*b.args(), b.max_q))
+
+
+def test_chunks_with_a_few_rows_in_the_last_tile(w4, cuda_device):
+    """256-row tiles whose last one has 1 to 255 rows, with and without a part in another thread block."""
+    lens = [(n, n + c) for n, c in ((52, 0), (53, 300), (77, 1100), (103, 40), (26, 900), (103, 3000))]
+    b = Batch(cuda_device, "fp16", 10, 2, 128, 16, lens, seed=31)
+    out, lse = w4.paged_attention(*b.args(), b.max_q, return_lse=True)
+    b.check(out, lse)

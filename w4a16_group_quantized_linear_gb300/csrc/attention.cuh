@@ -207,9 +207,8 @@ struct Shares {
 
 constexpr size_t align_up(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Sequences of up to kStepRows rows per cached head (attention_step.cu). max_rows
-// is at least the rows of each of these sequences.
-constexpr int kStepRows = 16;
+// Sequences of up to max_rows <= kStepRows rows per cached head (attention_step.cu).
+constexpr int kStepRows = 32;
 w4a16_status attention_step_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, int max_rows,
                                    void* workspace, cudaStream_t st);
 size_t attention_step_workspace_bytes(const DeviceInfo& dev, int head_dim);

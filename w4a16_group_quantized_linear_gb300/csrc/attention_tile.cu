@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
             for (int i = 0; i < 32 / kRowsPer; ++i) {
                 const int r = (warp & 3) * 32 + i * kRowsPer + lane / kPieces;
-                const int at = e.row + (PAIRED ? 0 : w * kHalf) + r;
+                const int at = e.row + (PAIRED && e.paired ? 0 : w * kHalf) + r;
                 const int token = a.by_ratio.quotient(at);
                 const bool real = token < e.count;
                 const uint16_t* src =
@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool last = e.last;
             const bool paired = PAIRED && e.paired;
             const int begin = e.begin[w], end = e.end[w], step = paired ? 2 : 1;
-            const int first_row = e.row + (PAIRED ? 0 : w * kHalf);
+            const int first_row = e.row + (paired ? 0 : w * kHalf);
             int low, high;
             {
                 const int token = a.by_ratio.quotient(first_row + row);
