@@ -2,25 +2,20 @@
 //
 // A sequence's work is a number of rows per cached head: its new tokens times
 // the query heads that share the head. With few rows the cache's bytes are all
-// that counts and attention_step.cu takes them; with more, the 8-row products
-// of that kernel are what it waits for, and attention_tile.cu takes 256 rows to a tile
-// on the tensor cores. Measured: 25 rows (5 draft tokens, 5 heads to a cached
-// one) of 16 sequences 85 us against 90 on the tiles, 32 rows (one token, 32
-// heads to a cached one) of 64 sequences 119 against 131; so 32 rows is the
-// limit of a batch that has no more. The lengths are on the device, so where a batch may hold both
-// kinds both kernels are launched, and each passes over the other's; there the limit is 16, as the variant
-// for 32 rows costs batches of single tokens more than it gains (a mixed
-// batch 140 us against 133).
+// that counts and attention_step.cu takes them; past 16 the 8-row products
+// of that kernel are what it waits for (with a variant for 32 rows, 25 rows of
+// 16 sequences took 94 us, as on the tiles, and 32 of 64 sequences 132
+// against 130), and attention_tile.cu takes 256 rows to a tile on the tensor
+// cores. The lengths are on the device, so where a batch may hold both kinds
+// both kernels are launched, and each passes over the other's.
 #include "attention.cuh"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kStepRowsBeside = 16;  // the step kernel's limit beside the other
-
 struct Plan {
     bool step, tile;
-    int step_rows;  // most rows of a sequence of the step kernel's
+    int step_rows;  // most rows of a sequence of the step kernel
 };
 
 Plan plan_for(int64_t T, int64_t batch, int heads, int kv_heads, int64_t max_q_len) {
@@ -29,8 +24,8 @@ Plan plan_for(int64_t T, int64_t batch, int heads, int kv_heads, int64_t max_q_l
     p.tile = most > kStepRows;
     // every sequence has max_q_len new tokens, as one alone has: no second kind
     const bool alike = T == batch * max_q_len || batch == 1;
-    p.step = !p.tile || (ratio <= kStepRowsBeside && !alike);
-    p.step_rows = p.tile ? kStepRowsBeside : (int)most;
+    p.step = !p.tile || (ratio <= kStepRows && !alike);
+    p.step_rows = (int)(most < kStepRows ? most : kStepRows);
     return p;
 }
 
@@ -53,7 +48,7 @@ w4a16_status attention_launch(const DeviceInfo& dev, int dtype, const AttentionA
         const w4a16_status s = attention_step_launch(dev, dtype, a, p.step_rows, workspace, st);
         if (s != W4A16_OK || !p.tile) return s;
     }
-    return attention_tile_launch(dev, dtype, a, p.step ? p.step_rows + 1 : 1,
+    return attention_tile_launch(dev, dtype, a, p.step ? kStepRows + 1 : 1,
                                  static_cast<unsigned char*>(workspace) +
                                      align_up(attention_step_workspace_bytes(dev, 128)), st);
 }

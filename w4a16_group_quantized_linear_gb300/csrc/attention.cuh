@@ -12,7 +12,7 @@ namespace w4a16 {
 
 // ------------------------------------------------------- 16-bit elements --
 
-// kSlack: how far (log2) a score may pass the running maximum before the maximum
+// kSlack: how far (log2) a score may pass the running maximum of a whole tile before the maximum
 // moves. A softmax weight then reaches 2^kSlack, which has to stay inside the
 // type (fp16: 65504 = 2^16), and weights times values summed in fp32 inside that.
 struct Fp16 {
@@ -207,8 +207,9 @@ struct Shares {
 
 constexpr size_t align_up(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Sequences of up to max_rows <= kStepRows rows per cached head (attention_step.cu).
-constexpr int kStepRows = 32;
+// Sequences of up to kStepRows rows per cached head (attention_step.cu). max_rows
+// is at least the rows of each of these sequences.
+constexpr int kStepRows = 16;
 w4a16_status attention_step_launch(const DeviceInfo& dev, int dtype, const AttentionArgs& a, int max_rows,
                                    void* workspace, cudaStream_t st);
 size_t attention_step_workspace_bytes(const DeviceInfo& dev, int head_dim);

@@ -1,12 +1,14 @@
 // Attention over the paged cache for few rows: single tokens, and the few rows
-// of draft tokens (up to 32 rows per cached head, a row being one query head
+// of draft tokens (up to 16 rows per cached head, a row being one query head
 // of one new token; heads that share a cached head share its reads).
 //
 // out = softmax(c q k^T) v in one pass: with m the running maximum of a row's
 // scores s and p_j = 2^(s_j - m), both l = sum p_j and o = sum p_j v_j are
-// multiplied by 2^(m - m') when the maximum moves to m'. The maximum only
-// moves when a score passes it by E::kSlack, which keeps p inside the element
-// type and makes the multiplication rare; out = o / l is the same for any m.
+// multiplied by 2^(m - m') when the maximum moves to m'. p is rounded to the
+// element type for the second product. The maximum moves with every score
+// that passes it, so the largest weight is 1 and exact, and where few weights count,
+// little is lost: 1.00 to 1.05 times the error of rounding the result alone, where a
+// maximum that lags (by up to 2^14 or 2^40 in p) gives 1.3 to 2.0, at the same speed.
 //
 // What bounds it is reading the cache once: 2 D 16-bit elements of k and v per place and
 // cached head, against 4 D operations for each row. So the work is spread over
@@ -24,16 +26,13 @@
 // products are formed transposed, s^T = k q^T and o^T = v^T p^T, so that
 // the 16-wide side of the m16n8k16 MMA is places and head elements, all of them
 // real, and the rows fill the 8-wide side: one of them for up to 8 rows, two for
-// 16, four for 32 (whose queries come from shared memory instead of registers).
-// p reaches the second product's operand layout by an 8x8 register transpose.
+// 16. p reaches the second product's operand layout by an 8x8 register transpose.
 //
 // Measured (heads of 128, 8 cached): one token each of 64 sequences of 300 to
-// 8000 places, 1.10 GB: 166 us, 6.6 TB/s, 98% of the copy rate; two of 125000
-// and 133000 places 162 us, 6.5 TB/s; one of 777 places 9.8 us, which is
-// latency: 2 us of launch, 1 to find the run, 2 for page entries and then k and v,
-// 1.5 for a block's products with instructions not yet cached, 3 for
-// the join. With four row groups the products bound it: an m16n8k16 takes a
-// scheduler 32 cycles, 4.0 TB/s at 25 rows.
+// 8000 places, 1.10 GB: 171 us, 6.4 TB/s, 95% of the copy rate; two of 125000
+// and 133000 places, 1.06 GB: 167 us, 6.3 TB/s; one of 777 places 10 us, which is
+// latency: 2 us of launch, 1 to find the run, 2 for page entries and then k and
+// v, 1 for a block's products with instructions not yet cached, 4 for the join.
 #include "attention.cuh"
 
 namespace w4a16 {
@@ -166,13 +165,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     constexpr int kRows = NT * 8;
     constexpr int kKs = D / 16;  // k-steps of the scores; 16-element tiles of the output
     extern __shared__ __align__(128) unsigned char smem[];
-    constexpr bool kSharedQ = NT > 2;   // queries in shared memory, not in registers
+    __shared__ int64_t s_sum[kWarps];
+    __shared__ int s_found[2];
     __shared__ float2 s_stats[kWarps][kRows];
-    // one region by turns: the run's search, an item's queries, the joining of the warps' parts
-    float* join = reinterpret_cast<float*>(smem + kWarps * kRingBytes);
-    int64_t* s_sum = reinterpret_cast<int64_t*>(join);  // [kWarps]
-    int* s_found = reinterpret_cast<int*>(s_sum + kWarps);  // [2]
-    int* s_last = reinterpret_cast<int*>(join);
+    __shared__ int s_last;
     const AttentionArgs& a = arg.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp = lane >> 2, quad = lane & 3;
@@ -233,7 +229,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     load_sequence(a, at.b, kRows, at.s);
     at.g = s_found[1] / at.s.blocks;
     at.block = at.s.block + s_found[1] % at.s.blocks;
-    __syncthreads();  // the shared region is free again
     at.end = at.s.block + at.s.blocks;
     Cursor to = at;  // of the loads, which run ahead
     int64_t to_load = run_end - run_begin;
@@ -278,40 +273,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     };
 
     // ------------------------------------------------------- computation --
-    uint32_t qf[kSharedQ ? 1 : kKs][NT][2];
-    const uint32_t q_smem = ptx::smem_u32(join);
+    uint32_t qf[kKs][NT][2];
     float o[kKs][NT][4];
     float m[NT][2], l[NT][2];
     int low[NT][2], high[NT][2];  // places that this lane's columns (rows of q) see
 
-    auto query = [&](int r) {  // row r of the item; nullptr past its rows
-        const int token = a.by_ratio.quotient(r);
-        return token < at.s.count ? a.q + (int64_t)(at.s.first + token) * a.q_row_stride +
-                                        (int64_t)(at.g * ratio + r - token * ratio) * a.q_head_stride
-                                  : nullptr;
-    };
     auto start_item = [&]() {
-        if constexpr (kSharedQ) {
-            static_assert(kRows * L::kRowBytes <= L::kJoinBytes, "queries");
-            for (int i = tid; i < kRows * L::kChunks; i += kThreads) {
-                const int r = i / L::kChunks, chunk = i % L::kChunks;
-                const uint16_t* q = query(r);
-                *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(join) + L::at(r, chunk)) =
-                    q ? *reinterpret_cast<const uint4*>(q + chunk * 8) : make_uint4(0, 0, 0, 0);
-            }
-            __syncthreads();
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if constexpr (!kSharedQ) {
-                const uint16_t* q = query(n * 8 + grp);
+            const int r = n * 8 + grp;
+            const bool real = r < at.s.count * ratio;
+            const int64_t t = at.s.first + a.by_ratio.quotient(r);
+            const uint16_t* q =
+                a.q + t * a.q_row_stride + (int64_t)(at.g * ratio + a.by_ratio.remainder(r)) * a.q_head_stride;
 #pragma unroll
-                for (int ks = 0; ks < kKs; ++ks)
+            for (int ks = 0; ks < kKs; ++ks)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        qf[ks][n][j] =
-                            q ? __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16 + j * 8 + quad * 2)) : 0u;
-            }
+                for (int j = 0; j < 2; ++j)
+                    qf[ks][n][j] = real ? __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16 + j * 8 + quad * 2)) : 0u;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = n * 8 + quad * 2 + j;
@@ -331,53 +310,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     auto compute_step = [&](int stage) {
         const int p0 = at.block * kBlock + warp * kStep;
         if (p0 >= at.s.length || p0 + kStep <= at.s.low) return;
-        // row groups past the first two, where the item has rows there
-        const bool more = NT <= 2 || at.s.count * ratio > 16;
         const uint32_t kb = ring_u + stage * 2 * L::kHalfStage;
         const uint32_t vb = kb + L::kHalfStage;
-        constexpr int kChains = NT > 2 ? 1 : 2;  // of dependent MMAs; four row groups are chains enough
-        float s[kChains][NT][4];
+        float s[2][NT][4];  // two chains of dependent MMAs
 #pragma unroll
-        for (int c = 0; c < kChains; ++c)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[c][n][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) s[0][n][i] = s[1][n][i] = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < kKs; ++ks) {
             uint32_t k[4];
             ldmatrix_x4(k, kb + L::at(lane & 15, ks * 2 + (lane >> 4)));
-            if constexpr (kSharedQ) {
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    if (n >= 2 && !more) break;
-                    uint32_t q[4];
-                    ldmatrix_x4(q, q_smem + L::at((n + (lane >> 4)) * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)));
-                    mma<E>(s[0][n], k, q[0], q[1]);
-                    mma<E>(s[0][n + 1], k, q[2], q[3]);
-                }
-            } else {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma<E>(s[ks % kChains][n], k, qf[ks][n][0], qf[ks][n][1]);
-            }
+            for (int n = 0; n < NT; ++n) mma<E>(s[ks & 1][n], k, qf[ks][n][0], qf[ks][n][1]);
         }
         bool rise = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n >= 2 && !more) break;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int p = p0 + grp + (i >> 1) * 8;
-                float v = (kChains == 2 ? s[0][n][i] + s[kChains - 1][n][i] : s[0][n][i]) * a.scale_log2;
+                float v = (s[0][n][i] + s[1][n][i]) * a.scale_log2;
                 if (p < low[n][i & 1] || p >= high[n][i & 1]) v = -INFINITY;
                 s[0][n][i] = v;
-                rise = rise || v > m[n][i & 1] + E::kSlack;
+                rise = rise || v > m[n][i & 1];
             }
-        }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n >= 2 && !more) break;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float top = fmaxf(s[0][n][j], s[0][n][j + 2]);
@@ -393,12 +353,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                         o[ks][n][j + 2] *= keep;
                     }
                 }
-            }
         }
         uint32_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (n >= 2 && !more) break;
             float p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -415,15 +373,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             uint32_t v[4];
             ldmatrix_x4_trans(v, vb + L::at((lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n >= 2 && !more) break;
-                mma<E>(o[ks][n], v, pf[n][0], pf[n][1]);
-            }
+            for (int n = 0; n < NT; ++n) mma<E>(o[ks][n], v, pf[n][0], pf[n][1]);
         }
     };
 
     // Adds up the warps' parts of the item that ends here (or whose run ends
     // here) and writes the result, or the part for the last of its thread blocks to join.
+    float* join = reinterpret_cast<float*>(smem + kWarps * kRingBytes);
     auto write_row = [&](int r, int d, float (&acc)[8], float top, float sum) {
         const int64_t row = (int64_t)(at.s.first + a.by_ratio.quotient(r)) * a.heads + at.g * ratio +
                             a.by_ratio.remainder(r);
@@ -503,18 +459,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         __syncthreads();
         if (tid == 0) {
             const int done = ptx::atom_add_acq_rel_gpu(arg.counters + c0, 1);
-            *s_last = done == c1 - c0;
-            if (*s_last) arg.counters[c0] = 0;
+            s_last = done == c1 - c0;
+            if (s_last) arg.counters[c0] = 0;
         }
         __syncthreads();
-        const bool last = *s_last;
-        __syncthreads();  // the shared region is free again
-        if (!last) return;
+        if (!s_last) return;
         __threadfence();
-        // a thread per 8 elements of a row; the parts' statistics by way of shared memory, kParts at a time
-        constexpr int kParts = L::kJoinBytes / (int)(kRows * sizeof(float2)) < 64
-                                   ? L::kJoinBytes / (int)(kRows * sizeof(float2)) : 64;
-        float2* stats = reinterpret_cast<float2*>(join);  // [kParts][kRows]
+        // a thread per 8 elements of a row; the parts' statistics by way of shared memory, 64 parts at a time
+        float2* stats = reinterpret_cast<float2*>(join);  // [64][rows]
+        static_assert(64 * kRows * sizeof(float2) <= L::kJoinBytes, "statistics of 64 parts");
         for (int i0 = 0; i0 < rows * L::kChunks; i0 += kThreads) {
             const int i = i0 + tid;
             const bool mine = i < rows * L::kChunks;
@@ -522,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             float top = -INFINITY, sum = 0.0f, acc[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
-            for (int p0 = c0; p0 <= c1; p0 += kParts) {
-                const int n = min(kParts, c1 + 1 - p0);
+            for (int p0 = c0; p0 <= c1; p0 += 64) {
+                const int n = min(64, c1 + 1 - p0);
                 auto slot_of = [&](int k) { return (int64_t)(2 * (p0 + k) + (p0 + k == c0)); };
                 __syncthreads();
                 for (int k = tid; k < n * rows; k += kThreads) {
@@ -612,13 +565,11 @@ w4a16_status attention_step_launch(const DeviceInfo& dev, int dtype, const Atten
     arg.stats = reinterpret_cast<float2*>(w);
     w += align_up(2 * (size_t)blocks * kStepRows * sizeof(float2));
     arg.parts = reinterpret_cast<float*>(w);
-    const bool f16 = dtype == W4A16_DTYPE_F16, wide = a.c.head_dim == 128, two = max_rows > 8, four = max_rows > 16;
+    const bool f16 = dtype == W4A16_DTYPE_F16, wide = a.c.head_dim == 128, two = max_rows > 8;
 #define W4A16_STEP(D, NT) \
     return f16 ? launch<Fp16, D, NT>(dev, arg, blocks, st) : launch<Bf16, D, NT>(dev, arg, blocks, st)
-    if (wide && four) W4A16_STEP(128, 4);
     if (wide && two) W4A16_STEP(128, 2);
     if (wide) W4A16_STEP(128, 1);
-    if (four) W4A16_STEP(64, 4);
     if (two) W4A16_STEP(64, 2);
     W4A16_STEP(64, 1);
 #undef W4A16_STEP
