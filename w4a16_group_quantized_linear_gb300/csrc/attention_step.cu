@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             }
             const int page = __shfl_sync(0xffffffffu, my_page, to.block - pages_from);
             const int p0 = to.block * kBlock + warp * kStep;
-            const int64_t base = (int64_t)page * a.c.page_stride + (int64_t)a.c.by_page.remainder(p0) * a.c.slot_stride +
+            const int64_t base = (int64_t)page * a.c.page_stride +
+                                 (int64_t)a.c.by_page.remainder(p0) * a.c.slot_stride +
                                  (int64_t)to.g * a.c.head_stride;
             const uint32_t dst = ring_u + stage * 2 * L::kHalfStage;
             constexpr int kRowsPer = 32 / L::kChunks;  // rows per instruction

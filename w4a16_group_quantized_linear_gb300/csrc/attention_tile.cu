@@ -74,7 +74,9 @@ constexpr uint64_t kDrainLimitNs = 1000000000ull;
 __device__ TestHooks g_hooks = {kWaitLimitNs, -1};
 __device__ TestCounters g_counters = {0ull, 0ull};
 __device__ __forceinline__ uint64_t wait_limit() { return g_hooks.wait_limit_ns; }
-__device__ __forceinline__ bool may_issue(int issued) { return g_hooks.issue_limit < 0 || issued < g_hooks.issue_limit; }
+__device__ __forceinline__ bool may_issue(int issued) {
+    return g_hooks.issue_limit < 0 || issued < g_hooks.issue_limit;
+}
 #define W4A16_COUNT_TMEM(field) atomicAdd(&g_counters.field, 1ull)
 #else
 __device__ __forceinline__ constexpr uint64_t wait_limit() { return kWaitLimitNs; }
@@ -286,10 +288,12 @@ __device__ __forceinline__ bool elect_one() {
 // the registers cannot be read before it.
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
                  :
                  : "memory");
 }
@@ -335,7 +339,7 @@ struct Run {
 __device__ __forceinline__ bool find_run(const TileArgs& x, int* scratch, Run& run, Segment& at) {
     __shared__ int64_t s_sum[kThreads / 32];
     __shared__ int s_found[3];
-    int* s_first = scratch;  // first tile of each sequence of this round
+    int* s_first = scratch;  // first tile of each of these sequences
     int* s_count = scratch + kThreads;
     int* s_length = s_count + kThreads;
     const AttentionArgs& a = x.a;
@@ -605,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++n) {
                     const int st = n % L::kStages, round = n / L::kStages;
-                    if (dirty >= 0 && __all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->landed, landed_parity))) clean();
+                    if (dirty >= 0 && __all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->landed, landed_parity)))
+                        clean();
                     if (round > 0 && !wait_clean(&bars->empty[st], (round - 1) & 1)) break;
                     if (kv != (values ? 1 : 0)) continue;
                     ok = may_issue(n);
@@ -645,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------------- MMA
         // One thread. The tensor core's queue holds about 200 cycles of products, so what
-        // this thread does between two of them is kept below that: everything about the block
-        // after next is worked out in the middle of a round, not at its turn.
+        // this thread does between two of them is kept below that: what comes next is
+        // worked out while products are queued, not at its turn.
         constexpr uint32_t kIdescS = idesc<E>(kBlock, false), kIdescO = idesc<E>(D, true);
         if (elect_one()) {
             const uint32_t ring_u = ptx::smem_u32(ring);
@@ -683,207 +688,210 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (last) ptx::mma_commit(&bars->o_done[w]);
                 return true;
             };
-          if constexpr (!PAIRED) {
-            // what a block needs of its entry
-            struct View {
-                int to, begin0, end0, begin1, end1, last;
-            };
-            auto view = [&](int k) {
-                const Entry& e = bars->work[k % kEntries];
-                return View{e.to, e.begin[0], e.end[0], e.begin[1], e.end[1], e.last};
-            };
-            auto advance = [](uint32_t& st, uint32_t& parity) {
-                if (++st == L::kStages) {
-                    st = 0;
-                    parity ^= 1u;
-                }
-            };
-            int k = 0;                                // entry of the block whose p v comes next
-            int j = 0, i = 0;                         // that block, and the one whose scores come next
-            uint32_t vst = 0, vparity = 0, kst = 0, kparity = 0;  // their ring stages
-            uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0;
-            bool turn = false, more = true;           // the two are of different entries; there is a second one
-            View cur{}, nxt{};
-            auto plan = [&] {
-                vst = kst;
-                vparity = kparity;
-                advance(vst, vparity);
-                kst = vst;
-                kparity = vparity;
-                advance(kst, kparity);
-                i = j + 1;
-                turn = i == cur.to;
-                more = !turn || !cur.last;
-                if (turn && more && wait(&bars->work_full[(k + 1) % kEntries], ((k + 1) / kEntries) & 1)) {
-                    nxt = view(k + 1);
-                    i = bars->work[(k + 1) % kEntries].from;
-                }
-            };
-            if (wait(&bars->work_full[0], 0)) {  // the first block's scores
-                cur = nxt = view(0);
-                j = bars->work[0].from;
-                wait(&bars->full[0], 0);
-                if (ok && j >= cur.begin0 && j < cur.end0 && wait(&bars->q_full[0], 0)) {
-                    scores(0, 0);
-                    q_parity0 = 1;
-                }
-                if (ok && j >= cur.begin1 && j < cur.end1 && wait(&bars->q_full[1], 0)) {
-                    scores(1, 0);
-                    q_parity1 = 1;
-                }
-                ptx::mma_commit(&bars->empty[0]);
-                plan();
-            }
-            while (ok) {
-                if (!wait(&bars->full[vst], vparity)) break;
-                if (j >= cur.begin0 && j < cur.end0) {
-                    if (!output(0, vst, p_parity0, j == cur.begin0, j == cur.end0 - 1)) break;
-                    p_parity0 ^= 1u;
-                }
-                if (more) {
-                    if (!wait(&bars->full[kst], kparity)) break;
-                    if (i >= nxt.begin0 && i < nxt.end0) {
-                        if (i == nxt.begin0) {
-                            if (!wait(&bars->q_full[0], q_parity0)) break;
-                            q_parity0 ^= 1u;
-                        }
-                        scores(0, kst);
+            if constexpr (!PAIRED) {
+                // Block by block, one half and then the other.
+                // what a block needs of its entry
+                struct View {
+                    int to, begin0, end0, begin1, end1, last;
+                };
+                auto view = [&](int k) {
+                    const Entry& e = bars->work[k % kEntries];
+                    return View{e.to, e.begin[0], e.end[0], e.begin[1], e.end[1], e.last};
+                };
+                auto advance = [](uint32_t& st, uint32_t& parity) {
+                    if (++st == L::kStages) {
+                        st = 0;
+                        parity ^= 1u;
                     }
+                };
+                int k = 0;                                // entry of the block whose p v comes next
+                int j = 0, i = 0;                         // that block, and the one whose scores come next
+                uint32_t vst = 0, vparity = 0, kst = 0, kparity = 0;  // their ring stages
+                uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0;
+                bool turn = false, more = true;           // the two are of different entries; there is a second one
+                View cur{}, nxt{};
+                auto plan = [&] {
+                    vst = kst;
+                    vparity = kparity;
+                    advance(vst, vparity);
+                    kst = vst;
+                    kparity = vparity;
+                    advance(kst, kparity);
+                    i = j + 1;
+                    turn = i == cur.to;
+                    more = !turn || !cur.last;
+                    if (turn && more && wait(&bars->work_full[(k + 1) % kEntries], ((k + 1) / kEntries) & 1)) {
+                        nxt = view(k + 1);
+                        i = bars->work[(k + 1) % kEntries].from;
+                    }
+                };
+                if (wait(&bars->work_full[0], 0)) {  // the first block's scores
+                    cur = nxt = view(0);
+                    j = bars->work[0].from;
+                    wait(&bars->full[0], 0);
+                    if (ok && j >= cur.begin0 && j < cur.end0 && wait(&bars->q_full[0], 0)) {
+                        scores(0, 0);
+                        q_parity0 = 1;
+                    }
+                    if (ok && j >= cur.begin1 && j < cur.end1 && wait(&bars->q_full[1], 0)) {
+                        scores(1, 0);
+                        q_parity1 = 1;
+                    }
+                    ptx::mma_commit(&bars->empty[0]);
+                    plan();
                 }
-                if (j >= cur.begin1 && j < cur.end1) {
-                    if (!output(1, vst, p_parity1, j == cur.begin1, j == cur.end1 - 1)) break;
-                    p_parity1 ^= 1u;
+                while (ok) {
+                    if (!wait(&bars->full[vst], vparity)) break;
+                    if (j >= cur.begin0 && j < cur.end0) {
+                        if (!output(0, vst, p_parity0, j == cur.begin0, j == cur.end0 - 1)) break;
+                        p_parity0 ^= 1u;
+                    }
+                    if (more) {
+                        if (!wait(&bars->full[kst], kparity)) break;
+                        if (i >= nxt.begin0 && i < nxt.end0) {
+                            if (i == nxt.begin0) {
+                                if (!wait(&bars->q_full[0], q_parity0)) break;
+                                q_parity0 ^= 1u;
+                            }
+                            scores(0, kst);
+                        }
+                    }
+                    if (j >= cur.begin1 && j < cur.end1) {
+                        if (!output(1, vst, p_parity1, j == cur.begin1, j == cur.end1 - 1)) break;
+                        p_parity1 ^= 1u;
+                    }
+                    ptx::mma_commit(&bars->empty[vst]);
+                    if (!more) break;
+                    // the round after this one, while the products above are queued
+                    const bool second = i >= nxt.begin1 && i < nxt.end1;
+                    if (second && i == nxt.begin1) {
+                        if (!wait(&bars->q_full[1], q_parity1)) break;
+                        q_parity1 ^= 1u;
+                    }
+                    const uint32_t st = kst;
+                    if (turn) {
+                        ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
+                        ++k;
+                        cur = nxt;
+                    }
+                    j = i;
+                    plan();
+                    if (!ok) break;
+                    if (second) scores(1, st);
+                    ptx::mma_commit(&bars->empty[st]);
                 }
-                ptx::mma_commit(&bars->empty[vst]);
-                if (!more) break;
-                // the round after this one, while the products above are queued
-                const bool second = i >= nxt.begin1 && i < nxt.end1;
-                if (second && i == nxt.begin1) {
-                    if (!wait(&bars->q_full[1], q_parity1)) break;
-                    q_parity1 ^= 1u;
-                }
-                const uint32_t st = kst;
-                if (turn) {
-                    ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
-                    ++k;
-                    cur = nxt;
-                }
-                j = i;
-                plan();
-                if (!ok) break;
-                if (second) scores(1, st);
-                ptx::mma_commit(&bars->empty[st]);
-            }
-          } else {
-            // The two halves are two streams of blocks: each has its next scores formed as
-            // soon as its last p is used up. The one that is further behind goes first, and neither
-            // passes the other by more than two blocks, so that what one waits for never
-            // depends on what the other has yet to do. Every block of the run is waited
-            // for by each, in order, whether the half sees it or not.
-            struct Stream {
-                int k = -1, j = 0, to = 0;          // entry, block, and the end of the entry's blocks
-                int begin = 0, end = 0, step = 1;   // the half's blocks of the entry
-                int shift = 0;                      // from block to place in the run
-                bool last = false, more = true;
-                bool formed = false;                // the block's scores are on their way
-                uint32_t q_parity = 0, p_parity = 0;
-                __device__ __forceinline__ int at() const { return j + shift; }
-            } s0, s1;
-            // gives a ring entry back, if the other stream is through with it too (else it will)
-            auto release = [&](int n, const Stream& other) {
-                if (other.at() > n >> 1 || (other.at() == n >> 1 && other.formed && !(n & 1)))
-                    ptx::mma_commit(&bars->empty[n % L::kStages]);
-            };
-            auto here = [&](int n) { return ptx::mbar_try_wait(&bars->full[n % L::kStages], (n / L::kStages) & 1); };
-            // towards the half's next block, as far as that goes without waiting
-            auto advance = [&](int w, Stream& s, const Stream& other) {
-                bool moved = false;
-                while (s.more && !s.formed) {
-                    if (s.j == s.to) {
-                        if (s.last) {
-                            ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
-                            s.more = false;
+            } else {
+                // The two halves are two streams of blocks: each has its next scores formed as
+                // soon as its last p is used up. The one that is further behind goes first, and neither
+                // passes the other by more than two blocks, so that what one waits for never
+                // depends on what the other has yet to do. Every block of the run is waited
+                // for by each, in order, whether the half sees it or not.
+                struct Stream {
+                    int k = -1, j = 0, to = 0;          // entry, block, and the end of the entry's blocks
+                    int begin = 0, end = 0, step = 1;   // the half's blocks of the entry
+                    int shift = 0;                      // from block to place in the run
+                    bool last = false, more = true;
+                    bool formed = false;                // the block's scores are on their way
+                    uint32_t q_parity = 0, p_parity = 0;
+                    __device__ __forceinline__ int at() const { return j + shift; }
+                } s0, s1;
+                // gives a ring entry back, if the other stream is through with it too (else it will)
+                auto release = [&](int n, const Stream& other) {
+                    if (other.at() > n >> 1 || (other.at() == n >> 1 && other.formed && !(n & 1)))
+                        ptx::mma_commit(&bars->empty[n % L::kStages]);
+                };
+                auto here = [&](int n) {  // entry n of the ring has landed
+                    return ptx::mbar_try_wait(&bars->full[n % L::kStages], (n / L::kStages) & 1);
+                };
+                // towards the half's next block, as far as that goes without waiting
+                auto advance = [&](int w, Stream& s, const Stream& other) {
+                    bool moved = false;
+                    while (s.more && !s.formed) {
+                        if (s.j == s.to) {
+                            if (s.last) {
+                                ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
+                                s.more = false;
+                                return true;
+                            }
+                            const int k = s.k + 1;
+                            if (!ptx::mbar_try_wait(&bars->work_full[k % kEntries], (k / kEntries) & 1)) return moved;
+                            if (k > 0) ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
+                            const Entry& e = bars->work[k % kEntries];
+                            s.k = k;
+                            s.j = e.from;
+                            s.to = e.to;
+                            s.begin = e.begin[w];
+                            s.end = e.end[w];
+                            s.step = e.paired ? 2 : 1;
+                            s.shift = e.ordinal - e.from;
+                            s.last = e.last;
+                            moved = true;
+                        }
+                        const int n = 2 * s.at();
+                        if ((other.more && s.at() > other.at() + 2) || !here(n)) return moved;
+                        if (s.j >= s.begin && s.j < s.end && ((s.j - s.begin) & (s.step - 1)) == 0) {
+                            if (s.j == s.begin) {
+                                if (!ptx::mbar_try_wait(&bars->q_full[w], s.q_parity)) return moved;
+                                s.q_parity ^= 1u;
+                            }
+                            ptx::tc_fence_after();
+                            scores(w, n % L::kStages);
+                            release(n, other);
+                            s.formed = true;
                             return true;
                         }
-                        const int k = s.k + 1;
-                        if (!ptx::mbar_try_wait(&bars->work_full[k % kEntries], (k / kEntries) & 1)) return moved;
-                        if (k > 0) ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
-                        const Entry& e = bars->work[k % kEntries];
-                        s.k = k;
-                        s.j = e.from;
-                        s.to = e.to;
-                        s.begin = e.begin[w];
-                        s.end = e.end[w];
-                        s.step = e.paired ? 2 : 1;
-                        s.shift = e.ordinal - e.from;
-                        s.last = e.last;
+                        if (!here(n + 1)) return moved;
+                        release(n, other);
+                        release(n + 1, other);
+                        ++s.j;
                         moved = true;
                     }
-                    const int n = 2 * s.at();
-                    if ((other.more && s.at() > other.at() + 2) || !here(n)) return moved;
-                    if (s.j >= s.begin && s.j < s.end && ((s.j - s.begin) & (s.step - 1)) == 0) {
-                        if (s.j == s.begin) {
-                            if (!ptx::mbar_try_wait(&bars->q_full[w], s.q_parity)) return moved;
-                            s.q_parity ^= 1u;
-                        }
-                        ptx::tc_fence_after();
-                        scores(w, n % L::kStages);
-                        release(n, other);
-                        s.formed = true;
-                        return true;
-                    }
-                    if (!here(n + 1)) return moved;
+                    return moved;
+                };
+                auto add_values = [&](int w, Stream& s, const Stream& other) {
+                    const int n = 2 * s.at() + 1;
+                    if (!here(n)) return false;
+                    // Where the half goes on in the same tile and the blocks up to its next one are
+                    // here, that is found out before the wait for p, and the next scores follow
+                    // the products at once.
+                    const int ahead = n - 1 + 2 * s.step;  // the next block's k
+                    bool on = s.j + s.step < s.end && (!other.more || s.at() + s.step <= other.at() + 2) && here(ahead);
+                    if (s.step == 2) on = on && here(n + 1) && here(n + 2);
+                    const int st = ahead % L::kStages;
+                    if (!output(w, n % L::kStages, s.p_parity, s.j == s.begin, s.j + s.step >= s.end)) return false;
+                    s.p_parity ^= 1u;
                     release(n, other);
-                    release(n + 1, other);
-                    ++s.j;
-                    moved = true;
-                }
-                return moved;
-            };
-            auto add_values = [&](int w, Stream& s, const Stream& other) {
-                const int n = 2 * s.at() + 1;
-                if (!here(n)) return false;
-                // Where the half goes on in the same tile and the blocks up to its next one are
-                // here, that is found out before the wait for p, and the next scores follow
-                // the products at once.
-                const int ahead = n - 1 + 2 * s.step;  // the next block's k
-                bool on = s.j + s.step < s.end && (!other.more || s.at() + s.step <= other.at() + 2) && here(ahead);
-                if (s.step == 2) on = on && here(n + 1) && here(n + 2);
-                const int st = ahead % L::kStages;
-                if (!output(w, n % L::kStages, s.p_parity, s.j == s.begin, s.j + s.step >= s.end)) return false;
-                s.p_parity ^= 1u;
-                release(n, other);
-                if (on) scores(w, st);
-                if (on) {
-                    if (s.step == 2) {
-                        release(n + 1, other);
-                        release(n + 2, other);
+                    if (on) scores(w, st);
+                    if (on) {
+                        if (s.step == 2) {
+                            release(n + 1, other);
+                            release(n + 2, other);
+                        }
+                        release(ahead, other);
+                        s.j += s.step;
+                    } else {
+                        ++s.j;
+                        s.formed = false;
                     }
-                    release(ahead, other);
-                    s.j += s.step;
-                } else {
-                    ++s.j;
-                    s.formed = false;
-                }
-                return true;
-            };
-            uint64_t since = 0;
-            int idle = 0;
-            while (ok && (s0.more || s1.more)) {
-                bool moved = s0.formed && (!s1.formed || s0.at() <= s1.at()) && add_values(0, s0, s1);
-                if (!moved && s1.formed) moved = add_values(1, s1, s0);
-                moved |= advance(0, s0, s1);
-                moved |= advance(1, s1, s0);
-                if (moved) {
-                    idle = 0;
-                    since = 0;
-                } else if ((++idle & 31) == 0) {  // bounded, like every wait
-                    const uint64_t now = ptx::globaltimer_ns();
-                    if (since == 0) since = now;
-                    if (*abort || now - since > wait_limit()) ok = false;
+                    return true;
+                };
+                uint64_t since = 0;
+                int idle = 0;
+                while (ok && (s0.more || s1.more)) {
+                    bool moved = s0.formed && (!s1.formed || s0.at() <= s1.at()) && add_values(0, s0, s1);
+                    if (!moved && s1.formed) moved = add_values(1, s1, s0);
+                    moved |= advance(0, s0, s1);
+                    moved |= advance(1, s1, s0);
+                    if (moved) {
+                        idle = 0;
+                        since = 0;
+                    } else if ((++idle & 31) == 0) {  // bounded, like every wait
+                        const uint64_t now = ptx::globaltimer_ns();
+                        if (since == 0) since = now;
+                        if (*abort || now - since > wait_limit()) ok = false;
+                    }
                 }
             }
-          }
             if (!ok) fail(x, bars);
             ptx::mma_commit(&bars->mma_done);
             volatile int never = 0;
@@ -1158,7 +1166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (bars->last[w]) {
                     __threadfence();
-                    const int parts = c1 - c0 + 1;  // of thread blocks c0 to c1: the first one's last tile, the others' first
+                    // of thread blocks c0 to c1: the first one's last tile, the others' first
+                    const int parts = c1 - c0 + 1;
                     auto slot_of = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0)); };
                     auto stats = [&](int i) { return __ldcg(x.stats + slot_of(i) * kTile + w * kHalf + row); };
                     float top = -INFINITY, total = 0.0f;
@@ -1251,17 +1260,18 @@ w4a16_status launch(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
     w4a16_status s = make_map(x.a.c, x.a.c.k, f16, x.box, &mk);
     if (s == W4A16_OK) s = make_map(x.a.c, x.a.c.v, f16, x.box, &mv);
     if (s != W4A16_OK) return s;
-    return launch_overlapped("paged_attention", tile_kernel<E, D, PAIRED>, dim3((unsigned)dev.sms), kThreads, L::kSmem, st, mk,
-                             mv, x);
+    return launch_overlapped("paged_attention", tile_kernel<E, D, PAIRED>, dim3((unsigned)dev.sms), kThreads, L::kSmem,
+                             st, mk, mv, x);
 }
 
 template <class E, int D>
 w4a16_status launch_rows(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
     // Sequences that all fit half a tile (drafts being verified, short chunks)
-    // share out their blocks between the halves: 5 rows x 5 heads over 2000 to
-    // 9000 places, 16 sequences, 88 us against 109 with one half idle. For tiles of both halves
-    // the issuing loop that knows of no pairs is the faster one (2048 tokens over
-    // 30048 places 807 against 868 us).
+    // share out their blocks between the halves: 5 tokens x 5 heads over 2000 to
+    // 9000 places, 16 sequences, 89 us against 109 with one half idle (94 with the
+    // maximum that moves at once). For tiles of both halves the issuing loop that
+    // knows of no pairs is the faster one (2048 tokens over 30048 places 807
+    // against 868 us).
     return x.a.max_q_len * x.a.ratio <= kHalf ? launch<E, D, true>(dev, x, st) : launch<E, D, false>(dev, x, st);
 }
 
