@@ -783,9 +783,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // The two halves are two streams of blocks: each has its next scores formed as
                 // soon as its last p is used up. The one that is further behind goes first, and neither
-                // passes the other by more than two blocks, so that what one waits for never
-                // depends on what the other has yet to do. Every block of the run is waited
+                // passes the other by more than two blocks. Every block of the run is waited
                 // for by each, in order, whether the half sees it or not.
+                //
+                // A half's p may depend on what the other has yet to do: at the end of a paired
+                // tile each waits for the other's o (pair_in, pair_out) before its next p, and
+                // the stream ahead may be in the tile after that. So nothing is waited for here
+                // that is not on its way whatever this thread does: the first part of p is polled
+                // for like all else (its second part follows from the same pass). The stream
+                // behind can always go on, and that is enough: all of the other's products of the tiles
+                // before it are issued, so its half gets past them, fetches its queries and
+                // announces p; and its blocks are loaded, as the ring holds the two blocks that the
+                // other may be ahead.
                 struct Stream {
                     int k = -1, j = 0, to = 0;          // entry, block, and the end of the entry's blocks
                     int begin = 0, end = 0, step = 1;   // the half's blocks of the entry
@@ -858,6 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool on = s.j + s.step < s.end && (!other.more || s.at() + s.step <= other.at() + 2) && here(ahead);
                     if (s.step == 2) on = on && here(n + 1) && here(n + 2);
                     const int st = ahead % L::kStages;
+                    if (!ptx::mbar_try_wait(&bars->p_part[w], s.p_parity)) return false;
                     if (!output(w, n % L::kStages, s.p_parity, s.j == s.begin, s.j + s.step >= s.end)) return false;
                     s.p_parity ^= 1u;
                     release(n, other);
