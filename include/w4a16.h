@@ -477,6 +477,13 @@ W4A16_API size_t w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t 
  * reported a device error. */
 W4A16_API w4a16_status w4a16_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
 
+/* The capture that `stream` is part of (cudaStreamBeginCapture), a number that no other
+ * capture of the process has; 0 where it is not being captured. A graph keeps the
+ * addresses of the workspaces that its calls were given: they must live as long as it
+ * does, and calls that may run at the same time (on two streams, or in two
+ * graphs replayed on two streams) need workspaces of their own. */
+W4A16_API w4a16_status w4a16_stream_capture_id(void* stream, uint64_t* id);
+
 /* Synchronizes `stream`, then reads and clears the current device's sticky
  * error word: W4A16_OK, W4A16_ERR_TIMEOUT (a bounded wait in the GEMV or the
  * GEMM gave up), W4A16_ERR_BAD_OFFSETS (w4a16_grouped_linear, or the query

@@ -13,6 +13,14 @@ This module is a thin ctypes binding over the C ABI of ``libw4a16.so``
 allocates outputs with PyTorch and passes raw device pointers and the current
 CUDA stream. Every step of the computation runs in the library's CUDA
 kernels; there is no fallback. If the library is missing, every call raises.
+
+Calls that split work across thread blocks join it in a workspace that this
+module keeps for each stream. A CUDA graph goes on using the workspace of the
+stream that it was captured on, whatever is called on that stream afterwards; graphs
+captured on one stream must therefore be replayed one after another, and not at
+the same time as other calls on that stream. A graph captured on a stream on
+which nothing was called before has a workspace of its own.
+
 Build it with ``python -m w4a16_group_quantized_linear_gb300.build`` (or
 ``__graft_entry__.build()``).
 """
@@ -82,6 +90,7 @@ EXPORTS = {
     "w4a16_paged_attention_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32, _I64]),
     "w4a16_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
     "w4a16_workspace_init": (_I32, [_P, _SZ, _P]),
+    "w4a16_stream_capture_id": (_I32, [_P, _P]),
     "w4a16_device_status": (_I32, [_P]),
     "w4a16_status_string": (ctypes.c_char_p, [_I32]),
     "w4a16_version": (_I32, []),
@@ -171,8 +180,24 @@ def _out(out, shape, device: torch.device, K: int):
     return out
 
 
-# one zero-initialised workspace per (device, stream, kind of call), grown on demand
+# One zero-initialised workspace per (device, stream, kind of call), grown on
+# demand. A buffer that a larger one takes the place of is kept: a captured
+# graph may hold its address. Each is at least twice the one before it, so
+# all that are kept are together no larger than the newest.
 _ws: dict = {}
+_replaced: list = []
+# The same for calls under capture on a stream that has no workspace of its own
+# yet: (capture id, buffer). Such a buffer is the graph's (its memory comes
+# from the graph's pool, its zero-fill is one of the graph's nodes), so no
+# call outside that capture may use it.
+_captured: dict = {}
+
+
+def _capture_id(stream) -> int:
+    """Of the capture that `stream` is part of; 0: none."""
+    n = ctypes.c_uint64(0)
+    _check(lib().w4a16_stream_capture_id(stream, ctypes.byref(n)), "w4a16_stream_capture_id")
+    return n.value
 
 
 def _workspace(dev: torch.device, stream, nbytes: int, kind: str = "linear"):
@@ -180,11 +205,23 @@ def _workspace(dev: torch.device, stream, nbytes: int, kind: str = "linear"):
         return None
     key = (dev.index, stream.value or 0, kind)
     buf = _ws.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
-        _check(lib().w4a16_workspace_init(_ptr(buf), buf.numel(), stream), "w4a16_workspace_init")
-        _ws[key] = buf
-    return buf
+    if buf is not None and buf.numel() >= nbytes:
+        return buf
+    capture = _capture_id(stream)
+    if capture:
+        of, own = _captured.get(key, (0, None))
+        if of == capture and own.numel() >= nbytes:
+            return own
+    new = torch.empty(max(nbytes, 1 << 20, 0 if capture or buf is None else 2 * buf.numel()), dtype=torch.uint8,
+                      device=dev)
+    _check(lib().w4a16_workspace_init(_ptr(new), new.numel(), stream), "w4a16_workspace_init")
+    if capture:
+        _captured[key] = (capture, new)
+        return new
+    if buf is not None:
+        _replaced.append(buf)
+    _ws[key] = new
+    return new
 
 
 def workspace_bytes(M: int, N: int, K: int, group: int, E: int = 1) -> int:

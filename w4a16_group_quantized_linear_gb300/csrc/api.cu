@@ -212,6 +212,17 @@ w4a16_status w4a16_workspace_init(void* workspace, size_t workspace_bytes, void*
     return cuda_status(cudaMemsetAsync(workspace, 0, workspace_bytes, (cudaStream_t)stream));
 }
 
+w4a16_status w4a16_stream_capture_id(void* stream, uint64_t* id) {
+    if (!id) return W4A16_ERR_INVALID_ARG;
+    *id = 0;
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    unsigned long long n = 0;
+    const w4a16_status s = cuda_status(cudaStreamGetCaptureInfo((cudaStream_t)stream, &capturing, &n),
+                                       "w4a16_stream_capture_id");
+    if (s == W4A16_OK && capturing == cudaStreamCaptureStatusActive) *id = n;
+    return s;
+}
+
 w4a16_status w4a16_linear(const uint16_t* x, const uint8_t* qweight, const uint16_t* scales, uint16_t* y,
                           int64_t M, int64_t N, int64_t K, int32_t group, void* workspace, size_t workspace_bytes,
                           void* stream) {
