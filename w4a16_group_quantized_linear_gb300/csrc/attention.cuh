@@ -184,6 +184,13 @@ struct AttentionArgs {
     int64_t max_q_len;
 };
 
+// The first place that a row at `place` sees. A row of a sequence that is shorter than its new tokens has a
+// negative place, and the window may be anything up to 2^31 - 1: nothing here passes 32 bits.
+__device__ __forceinline__ int first_seen(const AttentionArgs& a, int place) {
+    const int back = a.window - 1;
+    return a.window > 0 ? max(place, back) - back : 0;
+}
+
 // 2^x of the special-function unit (2 ulp), results below the normal range to zero.
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

@@ -125,7 +125,7 @@ __device__ __forceinline__ void load_sequence(const AttentionArgs& a, int b, int
     s.blocks = 0;
     if (first < 0 || next > a.c.T || s.count <= 0 || s.count > a.max_q_len || s.count * a.ratio > max_rows) return;
     s.length = cache_length(a.c, length);
-    s.low = a.window > 0 ? max(0, s.length - s.count - a.window + 1) : 0;
+    s.low = first_seen(a, s.length - s.count);
     s.block = s.low / kBlock;
     s.blocks = max(1, (s.length + kBlock - 1) / kBlock - s.block);
 }
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             for (int j = 0; j < 2; ++j) {
                 const int row = n * 8 + quad * 2 + j;
                 const int place = at.s.length - at.s.count + a.by_ratio.quotient(row);
-                low[n][j] = a.window > 0 ? max(0, place - a.window + 1) : 0;
+                low[n][j] = first_seen(a, place);
                 high[n][j] = row < at.s.count * ratio ? (a.causal ? min(at.s.length, place + 1) : at.s.length) : 0;
                 m[n][j] = -INFINITY;
                 l[n][j] = 0.0f;

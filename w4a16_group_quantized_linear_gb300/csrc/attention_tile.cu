@@ -169,7 +169,7 @@ __device__ __forceinline__ Range range_of(const AttentionArgs& a, int count, int
     const int first = length - count + a.by_ratio.quotient(r0), last = length - count + a.by_ratio.quotient(r1 - 1);
     const int high = a.causal ? min(length, last + 1) : length;
     if (high <= 0) return r;
-    r.low = a.window > 0 ? max(0, first - a.window + 1) : 0;
+    r.low = first_seen(a, first);
     r.block = r.low / kBlock;
     r.end = (high + kBlock - 1) / kBlock;
     return r;
@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             {
                 const int token = a.by_ratio.quotient(first_row + row);
                 const int place = e.length - e.count + token;
-                low = a.window > 0 ? max(0, place - a.window + 1) : 0;
+                low = first_seen(a, place);
                 high = token >= e.count ? 0 : a.causal ? min(e.length, place + 1) : e.length;
             }
             bool load_next = false;
