@@ -30,3 +30,29 @@ def test_window_as_large_as_it_can_be(w4, cuda_device, lens, window):
     b = Batch(cuda_device, "fp16", 10, 2, 128, 16, lens, seed=5)
     out, lse = w4.paged_attention(*b.args(), b.max_q, window=window, return_lse=True)
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("positions", [False, True])
+@pytest.mark.parametrize("q_len", [1, 5, 60])
+@pytest.mark.parametrize("length", [-3, 7 * 16 + 1, 7 * 16 + 60, 1 << 29])
+def test_append_stores_nothing_for_a_length_out_of_range(w4, cuda_device, length, q_len, positions):
+    """Its page table has room for 7 pages of 16; the other sequences' rows are stored."""
+    import torch
+
+    b = Batch(cuda_device, "fp16", 4, 2, 64, 16, [(2, 30), (q_len, 96), (3, 40)], seed=q_len, poison=3.0)
+    b.page_table[1] = b.page_table[1].clamp(min=0)   # every entry names a page
+    bad = torch.tensor([30, length, 40], dtype=torch.int32, device=cuda_device)
+    T = b.offsets[-1]
+    kn, vn = (torch.randn(T, 2, 64, device=cuda_device).half() for _ in range(2))
+    want_k, want_v = b.k.clone(), b.v.clone()
+    for s in (0, 2):
+        for t in range(b.offsets[s], b.offsets[s + 1]):
+            p = b.kv[s] - (b.offsets[s + 1] - t)
+            want_k[b.table[s][p // 16], p % 16], want_v[b.table[s][p // 16], p % 16] = kn[t], vn[t]
+    rotary = {}
+    if positions:   # position 0 turns by nothing
+        rotary = dict(table=w4.rope_table(8, 64, device=cuda_device),
+                      positions=torch.zeros(T, dtype=torch.int32, device=cuda_device))
+    w4.kv_append(kn, vn, b.k, b.v, b.page_table, b.q_offsets, bad, **rotary)
+    assert w4.device_status(raise_on_error=False) == 9
+    assert torch.equal(b.k, want_k) and torch.equal(b.v, want_v)

@@ -208,9 +208,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
     int first, count;
     const int b = sequence_of(a.c, t, first, count);
-    // place in the sequence; negative where the sequence is shorter than its new tokens
+    // place in the sequence; negative where the sequence is shorter than its new tokens, and where its length
+    // is out of range (reported): held to the range, that one would name places that are taken
     int place = -1;
-    if (b >= 0) place = cache_length(a.c, __ldg(a.c.kv_lens + b)) - count + (int)(t - first);
+    if (b >= 0) {
+        const int length = __ldg(a.c.kv_lens + b);
+        if (cache_length(a.c, length) == length) place = length - count + (int)(t - first);
+    }
     float c[8], s[8];
     const bool rotate = p.pair >= 0 && angles(a.r, a.c.T, t, place, p.pair, a.c.err, c, s);
     int64_t page = -1;
