@@ -441,10 +441,10 @@ W4A16_API w4a16_status w4a16_kv_append(const w4a16_paged_cache* cache, int64_t T
  * kv_lens[b], with W4A16_CAUSAL up to its own place p, and with window > 0
  * (which needs W4A16_CAUSAL) above p - window. A row that sees nothing gets
  * out = 0. lse (fp32 [T, heads], or NULL) is the natural logarithm of the
- * softmax's sum, -infinity for such a row. Pages that hold only places no row of a
- * sequence sees, and slots past its last place, are never multiplied in, whatever
- * they hold. Places that some rows of a sequence see and others do not must
- * hold finite values.
+ * softmax's sum, -infinity for such a row. What lies before the first place that
+ * any row of a sequence sees, and past its last place, is never multiplied in,
+ * whatever it holds, and pages that hold nothing else are not read. Places that some
+ * rows of a sequence see and others do not must hold finite values.
  *
  * q is [T, heads, head_dim] with the given strides, out contiguous.
  * max_q_len is at least the number of new tokens of every sequence (more:

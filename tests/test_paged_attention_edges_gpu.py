@@ -56,3 +56,35 @@ def test_append_stores_nothing_for_a_length_out_of_range(w4, cuda_device, length
     w4.kv_append(kn, vn, b.k, b.v, b.page_table, b.q_offsets, bad, **rotary)
     assert w4.device_status(raise_on_error=False) == 9
     assert torch.equal(b.k, want_k) and torch.equal(b.v, want_v)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("window", [1, 30, 200])
+@pytest.mark.parametrize("lens", [[(1, 300), (3, 200)], [(20, 400), (7, 300), (20, 100)], [(130, 500), (1, 90), (70, 1000)]])
+def test_places_before_every_window_may_hold_anything(w4, cuda_device, lens, window, page):
+    """Also in a page that holds places that rows see: infinities and NaN there reach no result."""
+    for value in (float("nan"), float("inf")):
+        b = Batch(cuda_device, "fp16", 10, 2, 128, page, lens, seed=page)
+        for s, m in enumerate(b.kv):
+            n = b.offsets[s + 1] - b.offsets[s]
+            for p in range(max(0, m - n - window + 1)):
+                b.k[b.table[s][p // page], p % page] = value
+                b.v[b.table[s][p // page], p % page] = value
+        out, lse = w4.paged_attention(*b.args(), b.max_q, window=window, return_lse=True)
+        b.check(out, lse, window=window)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("window", [1, 30, 200])
+@pytest.mark.parametrize("lens", [[(1, 300), (3, 200)], [(20, 400), (7, 300), (20, 100)], [(130, 500), (1, 90), (70, 1000)]])
+def test_places_before_every_window_may_hold_anything(w4, cuda_device, lens, window, page):
+    """Also in a page that holds places that rows see: infinities and NaN there reach no result."""
+    for value in (float("nan"), float("inf")):
+        b = Batch(cuda_device, "fp16", 10, 2, 128, page, lens, seed=page)
+        for s, m in enumerate(b.kv):
+            n = b.offsets[s + 1] - b.offsets[s]
+            for p in range(max(0, m - n - window + 1)):
+                b.k[b.table[s][p // page], p % page] = value
+                b.v[b.table[s][p // page], p % page] = value
+        out, lse = w4.paged_attention(*b.args(), b.max_q, window=window, return_lse=True)
+        b.check(out, lse, window=window)

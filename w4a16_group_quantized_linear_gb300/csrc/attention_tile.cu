@@ -32,8 +32,8 @@
 //   warp 8          TMA: k and v blocks into a ring of shared memory, one box per page piece and
 //                   64 elements. Pages that hold nothing to see are not read:
 //                   a box outside the cache reads as zeros. Slots past a
-//                   sequence's last place are zeroed in the v block (0 times
-//                   whatever they hold might not be 0).
+//                   sequence's last place and before a window's first are zeroed in the
+//                   v block (0 times whatever they hold might not be 0).
 //   warp 9          MMA issue: p v of block j, then q k of block j + 1, for one half
 //                   and then the other.
 //   warp 10         lays out the work: each tile's rows, blocks and sharers, a few tiles
@@ -112,7 +112,7 @@ struct Entry {
 
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];  // ring
-    uint64_t landed;      // a v block that holds a sequence's last place, before it is cleaned
+    uint64_t landed;      // a v block that holds a sequence's last place or a window's first, before it is cleaned
     uint64_t q_full[2];   // a half's queries are in shared memory
     uint64_t s_full[2];   // a half's scores are in TMEM (and its o is up to date)
     uint64_t p_part[2];   // the first 64 columns of a half's p are in TMEM
@@ -256,6 +256,12 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 // Slots of a block's last page piece that are past the sequence's `past` places in the block.
 __device__ __forceinline__ int tail_rows(int past, int box) {
     return past > 0 && past < kBlock ? (box - (past & (box - 1))) & (box - 1) : 0;  // box: a power of two
+}
+
+// Slots of a block's first page piece to be read that are before the first place that a row of the
+// tile sees, which is `before` places into the block.
+__device__ __forceinline__ int head_rows(int before, int box) {
+    return before > 0 && before < kBlock ? before & (box - 1) : 0;
 }
 
 // v block as the B operand of p v: 64-element slabs of 128-byte rows, a row per
@@ -555,11 +561,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pieces = kBlock / x.box;
         const int piece = lane / L::kSlabs, slab = lane % L::kSlabs;
         int n = 0, issued = -1;
-        // The v block of a sequence's last place lands on a barrier of its own; then
-        // its slots past that place are zeroed (0 times what they hold might not be 0),
-        // and only then is it handed on. Other copies go out meanwhile, but nothing
-        // is waited for before that.
-        int dirty = -1, dirty_row = 0, dirty_rows = 0;
+        // The v block of a sequence's last place, or of a window's first, lands on a barrier
+        // of its own; then its slots past the one and before the other are zeroed (0 times what
+        // they hold might not be 0), and only then is it handed on. Other copies go out meanwhile,
+        // but nothing is waited for before that.
+        int dirty = -1, dirty_head = 0, dirty_heads = 0, dirty_row = 0, dirty_rows = 0;
         uint32_t landed_parity = 0;
         auto clean = [&] {
             ok = ok && wait_bar(&bars->landed, landed_parity, abort, wait_limit());
@@ -567,8 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) return;
             landed_parity ^= 1u;
             const int st = dirty % L::kStages;
-            for (int c = lane; c < dirty_rows * (D / 8); c += 32) {
-                const int row = dirty_row + c / (D / 8), part = c % (D / 8);
+            for (int c = lane; c < (dirty_heads + dirty_rows) * (D / 8); c += 32) {
+                const int i = c / (D / 8), part = c % (D / 8);
+                const int row = i < dirty_heads ? dirty_head + i : dirty_row + i - dirty_heads;
                 *reinterpret_cast<uint4*>(ring + st * L::kStageBytes + (part >> 3) * L::kSlabBytes + row * 128 +
                                           (part & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
@@ -616,19 +623,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = may_issue(n);
                     if (!ok) break;
                     const int rows = values ? tail_rows(length - j * kBlock, x.box) : 0;
-                    if (rows > 0 && dirty >= 0) {
+                    const int heads = values ? head_rows(low - j * kBlock, x.box) : 0;
+                    const bool unclean = rows + heads > 0;
+                    if (unclean && dirty >= 0) {
                         clean();
                         if (!ok) break;
                     }
-                    uint64_t* bar = rows > 0 ? &bars->landed : &bars->full[st];
+                    uint64_t* bar = unclean ? &bars->landed : &bars->full[st];
                     if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
                     __syncwarp();
                     if (piece < pieces)
                         tma_load_4d(ring + st * L::kStageBytes + slab * L::kSlabBytes + piece * x.box * 128, map, bar,
                                     slab * 64, a.c.by_page.remainder(j * kBlock + piece * x.box), g, page);
                     issued = n;
-                    if (rows > 0) {
+                    if (unclean) {
                         dirty = n;
+                        dirty_head = low - j * kBlock - heads;
+                        dirty_heads = heads;
                         dirty_row = length - j * kBlock;
                         dirty_rows = rows;
                     }
