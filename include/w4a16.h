@@ -384,8 +384,8 @@ typedef struct {
  * out[t, h] = x[t, h] turned by token t's positions. x and out are
  * [T, heads, head_dim] with the given strides; out may be x (the same strides),
  * and may not overlap it otherwise. head_dim is a multiple of 16, at most 1024.
- * A position outside the table is reported (W4A16_ERR_BAD_CACHE) and its pairs
- * are copied unturned.
+ * A position outside the table is reported (W4A16_ERR_BAD_CACHE) and the pairs of
+ * its axis turn by nothing (finite ones are copied); those of other axes turn.
  */
 W4A16_API w4a16_status w4a16_rope(int32_t dtype, const uint16_t* x, int64_t x_row_stride, int64_t x_head_stride,
                                   uint16_t* out, int64_t out_row_stride, int64_t out_head_stride, int64_t T,

@@ -88,3 +88,43 @@ def test_places_before_every_window_may_hold_anything(w4, cuda_device, lens, win
                 b.v[b.table[s][p // page], p % page] = value
         out, lse = w4.paged_attention(*b.args(), b.max_q, window=window, return_lse=True)
         b.check(out, lse, window=window)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pattern", ["cycle", "blocks"])
+@pytest.mark.parametrize("R", [32, 64])
+def test_a_position_outside_the_table_leaves_only_its_own_pairs(w4, cuda_device, R, pattern, interleaved):
+    """With several axes, pairs of the other axes are turned all the same; in the append too, where
+    keys under the caller's positions are checked along with the queries."""
+    import torch
+
+    r = np.random.default_rng(R)
+    b = Batch(cuda_device, "fp16", 4, 2, 64, 16, [(1, 20), (6, 31)], seed=R, poison=2.0)
+    T, half = b.offsets[-1], R // 2
+    axes = [i % 3 if pattern == "cycle" else i * 3 // half for i in range(half)]
+    pos = r.integers(0, 50, (3, T)).astype(np.int32)
+    pos[1, 2], pos[2, 4], pos[:, 5] = 50, -1, 1 << 30
+    wrong = (pos < 0) | (pos >= 50)
+    table = w4.rope_table(50, R, device=cuda_device)
+    where = dict(table=table, positions=torch.from_numpy(pos).to(cuda_device), pair_axes=axes, interleaved=interleaved)
+
+    def check(y, x):
+        ref, mag = oa.rope(_np(x), _np(table), np.where(wrong, 0, pos), axes, interleaved)
+        for i in range(half):
+            e = [2 * i, 2 * i + 1] if interleaved else [i, i + half]
+            for t in np.flatnonzero(wrong[axes[i]]):
+                ref[t][:, e], mag[t][:, e] = _np(x)[t][:, e], 0
+                assert np.array_equal(_np(y)[t][:, e], ref[t][:, e])
+        assert (np.abs(_np(y) - ref) <= oa.rope_tolerance(ref, mag, "fp16")).all()
+
+    check(w4.rope(b.q, where["positions"], table, pair_axes=axes, interleaved=interleaved), b.q)
+    assert w4.device_status(raise_on_error=False) == 9
+    kn = torch.randn(T, 2, 64, device=cuda_device).half()
+    q = w4.kv_append(kn, kn, b.k, b.v, b.page_table, b.q_offsets, b.kv_lens, q=b.q, **where)
+    assert w4.device_status(raise_on_error=False) == 9
+    seq, place = oa.places(b.offsets, b.kv)
+    pages = torch.tensor([b.table[s][p // 16] for s, p in zip(seq, place)], device=cuda_device)
+    slots = torch.from_numpy(place % 16).to(cuda_device)
+    check(q, b.q)
+    check(b.k[pages, slots], kn)
+    assert torch.equal(b.v[pages, slots], kn)

@@ -56,7 +56,8 @@ __device__ __forceinline__ Pieces pieces_of(const RotaryArgs& r, int chunk) {
 
 // Cosines and sines of 8 pairs of token t. `place` is the position used when
 // the caller gave none. Returns false (nothing to turn) where there is no such
-// position; one that the caller gave outside the table is reported.
+// position. One outside the table is reported, and the pairs of its axis turn by
+// nothing: false, or a cosine of 1 among pairs of other axes.
 __device__ __forceinline__ bool angles(const RotaryArgs& r, int64_t T, int64_t t, int place, int pair,
                                        unsigned int* err, float (&c)[8], float (&s)[8]) {
     const int half = r.dim / 2;
@@ -78,7 +79,7 @@ __device__ __forceinline__ bool angles(const RotaryArgs& r, int64_t T, int64_t t
     for (int i = 0; i < 8; ++i) ok = ok && pos[i] >= 0 && pos[i] < r.rows;
     if (!ok) {
         raise_device_error(err, W4A16_ERR_BAD_CACHE);
-        return false;
+        if (same || r.rows == 0) return false;
     }
     if (same) {
         const float4* row = reinterpret_cast<const float4*>(r.table + (int64_t)pos[0] * r.dim + pair);
@@ -89,11 +90,24 @@ __device__ __forceinline__ bool angles(const RotaryArgs& r, int64_t T, int64_t t
         s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;
         s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
     } else {
+        // from the last row for a position outside (as from a negative one), and put right below: a
+        // test at each load costs the append of 3 axes 7%
+        const uint32_t last = (uint32_t)min(r.rows - 1, (int64_t)0x7fffffff);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float* row = r.table + (int64_t)pos[i] * r.dim + pair + i;
+            const float* row = r.table + (int64_t)min((uint32_t)pos[i], last) * r.dim + pair + i;
             c[i] = __ldg(row);
             s[i] = __ldg(row + half);
+        }
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int p = __ldg(r.positions + r.pair_axis[pair + i] * T + t);
+                if (p < 0 || p >= r.rows) {
+                    c[i] = 1.0f;
+                    s[i] = 0.0f;
+                }
+            }
         }
     }
     return true;
@@ -180,8 +194,9 @@ struct AppendArgs {
 };
 
 // The heads of a token in one row: queries, then keys, then values.
+// (Five thread blocks an SM with one head a thread: left to itself the compiler takes registers for the rare path.)
 template <class E, int HPT>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, HPT == 1 ? 5 : 3) append_kernel(const __grid_constant__ AppendArgs a) {
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     if (blockIdx.x == 0) check_offsets(a.c);
