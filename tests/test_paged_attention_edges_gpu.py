@@ -128,3 +128,23 @@ def test_a_position_outside_the_table_leaves_only_its_own_pairs(w4, cuda_device,
     check(q, b.q)
     check(b.k[pages, slots], kn)
     assert torch.equal(b.v[pages, slots], kn)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 5), (1, 40)], [(1, 9000), (2, 7)], [(20, 1500), (5, 20)],
+                                  [(20, 6000), (5, 20)], [(130, 700), (70, 90)], [(300, 9000)]])
+def test_a_query_that_is_not_a_number(w4, cuda_device, lens, D):
+    """Its row's result and logarithm are NaN, and no other row changes."""
+    import torch
+
+    b = Batch(cuda_device, "fp16", 10, 2, D, 16, lens, seed=D)
+    good, good_lse = w4.paged_attention(*b.args(), b.max_q, return_lse=True)
+    rows = [(0, 3), (b.offsets[-1] - 1, 9)]
+    other = torch.ones(b.offsets[-1], 10, dtype=torch.bool, device=cuda_device)
+    for t, h in rows:
+        b.q[t, h, 5] = float("nan")
+        other[t, h] = False
+    out, lse = w4.paged_attention(*b.args(), b.max_q, return_lse=True)
+    for t, h in rows:
+        assert out[t, h].isnan().all() and lse[t, h].isnan()
+    assert torch.equal(out[other], good[other]) and torch.equal(lse[other], good_lse[other])

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 st = s_stats[w][r];
-                    sum += st.x == -INFINITY ? 0.0f : st.y * fast_exp2(st.x - top);
+                    sum += st.y * (st.x == -INFINITY ? 0.0f : fast_exp2(st.x - top));  // a sum of NaN stays one
                     const float4* src = reinterpret_cast<const float4*>(join + L::join_at(w, col, d));
                     const float4 x = src[0], y = src[1];
                     acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;

@@ -1197,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
                     for (int i = 0; i < parts; ++i) {
                         const float2 v = stats(i);
-                        total += v.x == -INFINITY ? 0.0f : v.y * fast_exp2(v.x - top);
+                        total += v.y * (v.x == -INFINITY ? 0.0f : fast_exp2(v.x - top));  // a sum of NaN stays one
                     }
                     const float inv_total = total > 0.0f || total != total ? 1.0f / total : 0.0f;
 #pragma unroll 1
