@@ -450,7 +450,8 @@ W4A16_API w4a16_status w4a16_kv_append(const w4a16_paged_cache* cache, int64_t T
  * max_q_len is at least the number of new tokens of every sequence (more:
  * W4A16_ERR_BAD_OFFSETS, and that sequence's rows are not written).
  * Scores, softmax and sums are in fp32; the softmax weights are rounded to
- * the element type for the products with v; out is rounded once. Sequences
+ * the element type for the products with v; out is rounded once. Values above
+ * 2^113 divided by the places that a row sees (bf16) can overflow the fp32 sums. Sequences
  * with few rows are split over their length and joined through `workspace`,
  * in a fixed order: results are deterministic.
  * workspace: device buffer of at least

@@ -148,3 +148,19 @@ def test_a_query_that_is_not_a_number(w4, cuda_device, lens, D):
     for t, h in rows:
         assert out[t, h].isnan().all() and lse[t, h].isnan()
     assert torch.equal(out[other], good[other]) and torch.equal(lse[other], good_lse[other])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_bf16_values_under_rising_scores(w4, cuda_device, D):
+    """Values of 10^32: the sums before their division stay finite although the running maximum lags."""
+    import torch
+
+    b = Batch(cuda_device, "bf16", 10, 2, D, 16, [(64, 256)] * 60, seed=D)   # two blocks and more for each SM
+    for s, m in enumerate(b.kv):
+        for p in range(0, m, 16):
+            # 1/4 more in the exponent of two with each place
+            b.k[b.table[s][p // 16]] = (0.25 * 0.6931 * D ** -0.5 * torch.arange(p, p + 16.0)).to(b.k)[:, None, None]
+    b.q.copy_(torch.ones_like(b.q))
+    b.v.mul_(1e32)
+    out, lse = w4.paged_attention(*b.args(), b.max_q, return_lse=True)
+    b.check(out, lse)

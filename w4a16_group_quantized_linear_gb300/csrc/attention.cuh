@@ -12,12 +12,8 @@ namespace w4a16 {
 
 // ------------------------------------------------------- 16-bit elements --
 
-// kSlack: how far (log2) a score may pass the running maximum of a whole tile before the maximum
-// moves. A softmax weight then reaches 2^kSlack, which has to stay inside the
-// type (fp16: 65504 = 2^16), and weights times values summed in fp32 inside that.
 struct Fp16 {
     static constexpr int kDtype = W4A16_DTYPE_F16;
-    static constexpr float kSlack = 14.0f;
     __device__ static __forceinline__ float2 unpack(uint32_t v) {
         return __half22float2(*reinterpret_cast<const __half2*>(&v));
     }
@@ -29,7 +25,6 @@ struct Fp16 {
 
 struct Bf16 {
     static constexpr int kDtype = W4A16_DTYPE_BF16;
-    static constexpr float kSlack = 40.0f;
     __device__ static __forceinline__ float2 unpack(uint32_t v) {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
     }

@@ -5,7 +5,7 @@
 //
 // One pass over the places with the running maximum m and sum l of the
 // softmax: p = 2^(c s - m), l += sum p, o = o 2^(m - m') + p v whenever m moves
-// to m', which in whole tiles it only does when a score passes it by E::kSlack
+// to m', which in whole tiles it only does when a score passes it by kMaxSlack
 // (which keeps p inside the element type and makes the read-scale-write of o
 // rare; out = o / l whatever m is).
 //
@@ -65,6 +65,10 @@ constexpr int kThreads = 384;
 constexpr int kLoadK = 8, kMmaWarp = 9, kPlanWarp = 10, kLoadV = 11;
 constexpr int kBarBytes = 1792;  // struct Bars
 constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
+// How far (log2) a score may pass the running maximum of a whole tile before the maximum moves. A
+// weight reaches 2^14, inside fp16's 2^16, and o, not divided by l yet, that many times the values'
+// sum: with bf16's range it has to stay small. (2^40 was no faster, and lost values past 2^87.)
+constexpr float kMaxSlack = 14.0f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutCol = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -927,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // that of rounding the result alone, where they are up to 1.7 times). For whole tiles
         // it would cost 11% (2048 tokens over 30048 places 881 against 798 us) for errors of
         // 1.1 instead of 1.4 times.
-        constexpr float kSlack = PAIRED ? 0.0f : E::kSlack;
+        constexpr float kSlack = PAIRED ? 0.0f : kMaxSlack;
         const int w = warp >> 2;
         const int row = tid & (kHalf - 1);
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
