@@ -164,3 +164,34 @@ def test_large_bf16_values_under_rising_scores(w4, cuda_device, D):
     b.v.mul_(1e32)
     out, lse = w4.paged_attention(*b.args(), b.max_q, return_lse=True)
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("lens", [[(1, 9000), (1, 300)], [(300, 4000)]])
+def test_calls_after_a_wait_that_gave_up(w4, cuda_device, monkeypatch, lens):
+    """Reading the timeout makes the kept workspaces ready again (test-hooks build: a 1 ms limit and a
+    loader that stops after up to three blocks)."""
+    import ctypes
+
+    from w4a16_group_quantized_linear_gb300 import build
+
+    lib = ctypes.CDLL(build.build(variant="testhooks"))
+    for name, (res, args) in w4.EXPORTS.items():
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
+    lib.w4a16_test_set_hooks.restype = ctypes.c_int32
+    lib.w4a16_test_set_hooks.argtypes = [ctypes.c_uint64, ctypes.c_int32]
+    monkeypatch.setattr(w4, "_lib", lib)
+    monkeypatch.setattr(w4, "_ws", {})
+    stopped = Batch(cuda_device, "fp16", 10, 2, 128, 16, [(300, 4000)], seed=1)
+    b = Batch(cuda_device, "fp16", 10, 2, 128, 16, lens, seed=2)
+    try:
+        for limit in (0, 1, 2, 3):
+            assert lib.w4a16_test_set_hooks(1_000_000, limit) == 0
+            w4.paged_attention(*stopped.args(), stopped.max_q)
+            assert w4.device_status(raise_on_error=False) == 5
+    finally:
+        assert lib.w4a16_test_set_hooks(2_000_000_000, -1) == 0
+    for _ in range(2):
+        b.check(w4.paged_attention(*b.args(), b.max_q))
+        stopped.check(w4.paged_attention(*stopped.args(), stopped.max_q))
+    assert w4.device_status(raise_on_error=False) == 0

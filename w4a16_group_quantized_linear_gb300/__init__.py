@@ -46,6 +46,8 @@ STATUS = {0: "W4A16_OK", 1: "W4A16_ERR_INVALID_ARG", 2: "W4A16_ERR_UNSUPPORTED",
           4: "W4A16_ERR_CUDA", 5: "W4A16_ERR_TIMEOUT", 6: "W4A16_ERR_BAD_OFFSETS", 7: "W4A16_ERR_WORKSPACE",
           8: "W4A16_ERR_BAD_ROUTING", 9: "W4A16_ERR_BAD_CACHE"}
 
+TIMEOUT = 5  # of STATUS: a bounded wait on the device gave up
+
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 
 
@@ -683,9 +685,18 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
 
 def device_status(raise_on_error: bool = True) -> int:
-    """Synchronizes the current stream and reads/clears the device error word."""
-    st = _stream(torch.device("cuda", torch.cuda.current_device()))
+    """Synchronizes the current stream and reads/clears the device error word.
+    After a timeout the workspaces kept here are made ready again (the whole
+    device is synchronized): the call that gave up left its counters set."""
+    index = torch.cuda.current_device()
+    st = _stream(torch.device("cuda", index))
     status = int(lib().w4a16_device_status(st))
+    if status == TIMEOUT:
+        torch.cuda.synchronize(index)
+        for buf in [*_ws.values(), *_replaced, *(own for _, own in _captured.values())]:
+            if buf.get_device() == index:
+                _check(lib().w4a16_workspace_init(_ptr(buf), buf.numel(), st), "w4a16_workspace_init")
+        torch.cuda.synchronize(index)
     if raise_on_error:
         _check(status, "device")
     return status
