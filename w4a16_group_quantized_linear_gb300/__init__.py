@@ -147,7 +147,16 @@ def _check(status: int, where: str):
         raise W4A16Error(status, where)
 
 
+def _on_current_device(index):
+    """The library launches on the current device, and sizes workspaces for it."""
+    current = torch._C._cuda_getDevice()
+    if index is not None and index != current:
+        raise ValueError(f"the tensors are on cuda:{index} and the current device is cuda:{current}: make the call "
+                         "under torch.cuda.device(tensor.device)")
+
+
 def _stream(dev: torch.device):
+    _on_current_device(dev.index)
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
@@ -486,6 +495,7 @@ _ROTARY = struct.Struct("PqiiPiP")          # _Rotary
 
 
 def _raw_stream(index: int) -> int:
+    _on_current_device(index)
     return torch._C._cuda_getCurrentRawStream(index)
 
 
