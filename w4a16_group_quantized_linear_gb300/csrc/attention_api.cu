@@ -141,8 +141,9 @@ w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int64_t T, co
                                    void* workspace, size_t workspace_bytes, void* stream) {
     w4a16_status s = check_cache(cache, T);
     if (s != W4A16_OK) return s;
+    const float scale_log2 = scale * 1.4426950408889634f;
     if (heads < 1 || heads % cache->kv_heads != 0 || max_q_len < 0 || (flags & ~W4A16_CAUSAL) || window < 0 ||
-        (window > 0 && !(flags & W4A16_CAUSAL)) || !std::isfinite(scale) || !(scale > 0.0f) ||
+        (window > 0 && !(flags & W4A16_CAUSAL)) || !std::isfinite(scale_log2) || !(scale > 0.0f) ||
         bad_stride(q_row_stride) || bad_stride(q_head_stride))
         return W4A16_ERR_INVALID_ARG;
     if (T == 0) return W4A16_OK;
@@ -164,7 +165,7 @@ w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int64_t T, co
     a.by_ratio = fast_div(a.ratio);
     a.causal = (flags & W4A16_CAUSAL) ? 1 : 0;
     a.window = window;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     a.max_q_len = max_q_len < T ? max_q_len : T;
     return attention_launch(*dev, cache->dtype, a, workspace, workspace_bytes, (cudaStream_t)stream);
 }
