@@ -488,10 +488,15 @@ def rope_table(rows: int, rotary_dim: int, base: float = 10000.0, device="cuda")
     return torch.cat((angle.cos(), angle.sin()), dim=1).float()
 
 
+def _packer(c_type) -> struct.Struct:
+    """Packs the fields of a ctypes structure, in native alignment: several times faster than making one."""
+    code = {_P: "P", ctypes.c_char_p: "P", _I64: "q", _I32: "i"}
+    return struct.Struct("".join(code[t] for _, t in c_type._fields_))
+
+
 # The calls below are made once per layer and token, so their checks ask each
 # tensor for little: its device index (-1 off the GPU), type, shape and strides.
-_CACHE = struct.Struct("PPqqqqPqiiPPiiii")  # _PagedCache
-_ROTARY = struct.Struct("PqiiPiP")          # _Rotary
+_CACHE, _ROTARY = _packer(_PagedCache), _packer(_Rotary)
 
 
 def _raw_stream(index: int) -> int:
