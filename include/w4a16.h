@@ -448,7 +448,11 @@ W4A16_API w4a16_status w4a16_kv_append(const w4a16_paged_cache* cache, int64_t T
  *
  * q is [T, heads, head_dim] with the given strides, out contiguous.
  * max_q_len is at least the number of new tokens of every sequence (more:
- * W4A16_ERR_BAD_OFFSETS, and that sequence's rows are not written).
+ * W4A16_ERR_BAD_OFFSETS, and that sequence's rows are not written). It chooses the
+ * kernels, and with them the time and the rounding: where max_q_len * heads /
+ * kv_heads is at most 128 the largest softmax weight of a row is 1, exactly; above, a
+ * row that attends in whole tiles has weights up to 2^14 and results off by about 1.4
+ * times the rounding of out instead of 1.1. So it should be no larger than it has to be.
  * Scores, softmax and sums are in fp32; the softmax weights are rounded to
  * the element type for the products with v; out is rounded once. Values above
  * 2^113 divided by the places that a row sees (bf16) can overflow the fp32 sums. Sequences

@@ -671,8 +671,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     heads in groups of heads / kv_heads sharing a cached head. A row sees its sequence's
     places up to its own (all of them with ``causal=False``), the last ``window``
     of them where that is not 0. ``max_q_len`` is at least the longest sequence's number
-    of new tokens (it chooses the kernels; the lengths themselves stay on the
-    device). ``scale`` defaults to head_dim^-1/2. A row that sees nothing gets 0.
+    of new tokens (it chooses the kernels, so one that is larger than need be costs time and
+    some accuracy; the lengths themselves stay on the device). ``scale`` defaults to head_dim^-1/2. A row that sees nothing gets 0.
 
     Returns out [T, heads, head_dim], or (out, lse) with ``return_lse``: lse
     fp32 [T, heads] is the natural logarithm of the softmax's sum."""

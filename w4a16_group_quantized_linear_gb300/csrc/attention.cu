@@ -4,7 +4,7 @@
 // the query heads that share the head. With few rows the cache's bytes are all
 // that counts and attention_step.cu takes them; past 16 the 8-row products
 // of that kernel are what it waits for (with a variant for 32 rows, 25 rows of
-// 16 sequences took 94 us, as on the tiles, and 32 of 64 sequences 132
+// 16 sequences took 94 us, where the tiles take 87, and 32 of 64 sequences 132
 // against 130), and attention_tile.cu takes 256 rows to a tile on the tensor
 // cores. The lengths are on the device, so where a batch may hold both kinds
 // both kernels are launched, and each passes over the other's.

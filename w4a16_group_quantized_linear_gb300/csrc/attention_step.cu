@@ -7,7 +7,7 @@
 // multiplied by 2^(m - m') when the maximum moves to m'. p is rounded to the
 // element type for the second product. The maximum moves with every score
 // that passes it, so the largest weight is 1 and exact, and where few weights count,
-// little is lost: 1.00 to 1.05 times the error of rounding the result alone, where a
+// little is lost: 1.00 to 1.07 times the error of rounding the result alone, where a
 // maximum that lags (by up to 2^14 or 2^40 in p) gives 1.3 to 2.0, at the same speed.
 //
 // What bounds it is reading the cache once: 2 D 16-bit elements of k and v per place and

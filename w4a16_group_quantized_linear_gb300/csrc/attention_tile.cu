@@ -15,12 +15,13 @@
 // one half's scores go through the softmax, the tensor core forms the other's
 // products, and each k and v block that is read serves 256 rows.
 //
-// Measured: 2048 tokens over 30048 places, 40 heads of 128 on 8: 798 us, 1526
-// TFLOP/s, 79% of the cuBLAS bf16 burst (2900 cycles for a block of both halves,
-// 2048 of them products; for seconds on end the power limit takes the clock to
-// 1.6 GHz and it is 930 us). Heads of 64 have half the products to the same
+// Measured: 2048 tokens over 30048 places, 40 heads of 128 on 8: 786 to 805 us in short
+// runs, 1510 to 1550 TFLOP/s, 79 to 81% of the cuBLAS bf16 burst (2900 cycles for a block of
+// both halves, 2048 of them products); for seconds on end the power limit takes the clock to
+// 1.6 GHz and it is 900 to 930 us. Heads of 64 have half the products to the same
 // softmax: 633 us, 961 TFLOP/s. 14 sequences, 8 of single tokens, 6 of 287 to
-// 1427 with a window of 1024, 32 heads of 64 on 4: 134 us with the step kernel's 10.
+// 1427 with a window of 1024, 32 heads of 64 on 4: 135 to 165 us from process to
+// process, with the step kernel's 10. 5 tokens of 16 sequences over 2000 to 9000 places: 87 us.
 //
 //   warps 0-3, 4-7  softmax of the two halves: thread = row = TMEM lane. Reads
 //                   its 128 scores (tcgen05.ld), writes p as 16-bit pairs over
@@ -29,16 +30,17 @@
 //                   queries (rows of different tokens and heads: cp.async into the
 //                   swizzled layout) while the last block of the tile before
 //                   it is in work, and writes the result.
-//   warp 8          TMA: k and v blocks into a ring of shared memory, one box per page piece and
-//                   64 elements. Pages that hold nothing to see are not read:
-//                   a box outside the cache reads as zeros. Slots past a
-//                   sequence's last place and before a window's first are zeroed in the
-//                   v block (0 times whatever they hold might not be 0).
+//   warps 8, 11     TMA: k blocks (8) and v blocks (11) into one ring of shared memory, the
+//                   ring's even and odd entries, one box per page piece and 64
+//                   elements. Pages that hold nothing to see are not read (a box outside
+//                   the cache reads as zeros). Slots past a sequence's last place and
+//                   before a window's first are zeroed in the v block (0 times whatever
+//                   they hold might not be 0). Each warp waits for all entries in order: a
+//                   barrier's parity tells only its next phase from the one before.
 //   warp 9          MMA issue: p v of block j, then q k of block j + 1, for one half
 //                   and then the other.
 //   warp 10         lays out the work: each tile's rows, blocks and sharers, a few tiles
-//                   ahead, so that the others keep none of it in registers (warp 11 only
-//                   fills the warpgroup).
+//                   ahead, so that the others keep none of it in registers.
 //
 // TMEM: scores (and p) of the halves in columns [0, 128) and [128, 256), o in
 // [256, 256 + D) and [256 + D, 256 + 2 D).
@@ -927,9 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ----------------------------------------------------------- softmax
         // How far a score may pass the maximum before it moves. Not at all where there are few rows,
         // whose time is the cache's: the largest weight is then 1 and exact, and the error of
-        // rounding p next to nothing (94 against 91 us at 25 rows; errors 1.0 to 1.1 times
+        // rounding p next to nothing (87 against 85 us at 25 rows; errors 1.0 to 1.1 times
         // that of rounding the result alone, where they are up to 1.7 times). For whole tiles
-        // it would cost 11% (2048 tokens over 30048 places 881 against 798 us) for errors of
+        // it would cost 11% (2048 tokens over 30048 places 870 against 786 us) for errors of
         // 1.1 instead of 1.4 times.
         constexpr float kSlack = PAIRED ? 0.0f : kMaxSlack;
         const int w = warp >> 2;
@@ -1293,10 +1295,10 @@ template <class E, int D>
 w4a16_status launch_rows(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
     // Sequences that all fit half a tile (drafts being verified, short chunks)
     // share out their blocks between the halves: 5 tokens x 5 heads over 2000 to
-    // 9000 places, 16 sequences, 89 us against 109 with one half idle (94 with the
-    // maximum that moves at once). For tiles of both halves the issuing loop that
+    // 9000 places, 16 sequences, 87 us against 103 with one half idle (and the
+    // maximum that lags). For tiles of both halves the issuing loop that
     // knows of no pairs is the faster one (2048 tokens over 30048 places 807
-    // against 868 us).
+    // against 868 us when both were built with that maximum).
     return x.a.max_q_len * x.a.ratio <= kHalf ? launch<E, D, true>(dev, x, st) : launch<E, D, false>(dev, x, st);
 }
 
