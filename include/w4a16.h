@@ -392,6 +392,17 @@ W4A16_API w4a16_status w4a16_rope(int32_t dtype, const uint16_t* x, int64_t x_ro
                                   int32_t heads, int32_t head_dim, const w4a16_rotary* rotary, void* stream);
 
 /*
+ * The same with each head divided by its root mean square first:
+ * out[t, h] = turn(x[t, h] / sqrt(mean_d(x[t, h, d]^2) + eps) * weight), in fp32,
+ * rounded once. weight is fp32 [head_dim] on the device, 16-byte aligned; eps >= 0
+ * (with 0 a head of zeros gives NaN); head_dim is at most 512.
+ */
+W4A16_API w4a16_status w4a16_rope_norm(int32_t dtype, const uint16_t* x, int64_t x_row_stride, int64_t x_head_stride,
+                                       uint16_t* out, int64_t out_row_stride, int64_t out_head_stride, int64_t T,
+                                       int32_t heads, int32_t head_dim, const float* weight, float eps,
+                                       const w4a16_rotary* rotary, void* stream);
+
+/*
  * A cache of `pages` pages of `page_size` tokens, and the batch of sequences
  * that a call appends or attends with. Element d of head g of a page's slot is
  * at page * page_stride + slot * slot_stride + g * head_stride + d in both k
@@ -432,6 +443,60 @@ W4A16_API w4a16_status w4a16_kv_append(const w4a16_paged_cache* cache, int64_t T
                                        int64_t q_row_stride, int64_t q_head_stride, int32_t heads, uint16_t* q_out,
                                        const w4a16_rotary* rotary, void* stream);
 
+/*
+ * The cache in 8 bits. Each row x of head_dim elements is held as one byte an
+ * element and one scale: s = max(max_d |x[d]|, 2^-100) / most and q = x / s to the nearest
+ * (ties either way), an integer in [-127, 127] (W4A16_CACHE_INT8, most = 127, two's
+ * complement) or an e4m3 number (W4A16_CACHE_E4M3, most = 448); it stands for
+ * q s. A row that holds an infinity or a NaN gets the scale NaN.
+ *
+ * The calls that take scales read the rest from the w4a16_paged_cache: k and v then point
+ * to bytes, strides are in bytes and multiples of 16, and dtype is the element
+ * type of the call's 16-bit tensors. The scale of head g's row in a page's slot is at
+ * page * page_stride + g * head_stride + slot in k (keys) and v (values).
+ */
+#define W4A16_CACHE_INT8 1
+#define W4A16_CACHE_E4M3 2
+
+typedef struct {
+    int32_t format;                    /* W4A16_CACHE_* */
+    float* k;                          /* device, fp32, 16-byte aligned */
+    float* v;
+    int64_t page_stride, head_stride;  /* in elements, multiples of 4 */
+} w4a16_cache_scales;
+
+/* Weights of the query and the key heads' norms (device, fp32 [head_dim], 16-byte
+ * aligned; NULL: those heads are left as they are), as in w4a16_rope_norm. */
+typedef struct {
+    const float* q;
+    const float* k;
+    float eps;
+} w4a16_head_norms;
+
+/*
+ * w4a16_kv_append into an 8-bit cache (scales; NULL: the 16-bit one), with the
+ * heads of q and k divided by their root mean squares and weighted before they are turned
+ * (norms; NULL: as they are). What is computed is rounded once, to q_out's type, the
+ * cache's, or the 8 bits. Rows that are not stored leave their scales as they were.
+ */
+W4A16_API w4a16_status w4a16_kv_append_ex(const w4a16_paged_cache* cache, const w4a16_cache_scales* scales, int64_t T,
+                                          const uint16_t* k, int64_t k_row_stride, int64_t k_head_stride,
+                                          const uint16_t* v, int64_t v_row_stride, int64_t v_head_stride,
+                                          const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
+                                          int32_t heads, uint16_t* q_out, const w4a16_head_norms* norms,
+                                          const w4a16_rotary* rotary, void* stream);
+
+/*
+ * The inverse of the append: k and v ([T, kv_heads, head_dim], contiguous, of the
+ * cache's dtype) are the cached rows at each row's place, q s rounded once (scales
+ * NULL: the 16-bit cache's, as they are). To read places [first, end) of a sequence, pass kv_lens =
+ * end and end - first rows. Zeros for a place that is negative, or whose page or length is out of
+ * range (W4A16_ERR_BAD_CACHE); a row that no sequence holds (W4A16_ERR_BAD_OFFSETS) is
+ * not written. k and v must not overlap the cache.
+ */
+W4A16_API w4a16_status w4a16_kv_read(const w4a16_paged_cache* cache, const w4a16_cache_scales* scales, int64_t T,
+                                     uint16_t* k, uint16_t* v, void* stream);
+
 /* Each row sees only the places up to its own (else: all of its sequence). */
 #define W4A16_CAUSAL 1u
 
@@ -469,6 +534,19 @@ W4A16_API w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int
                                              uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                                              void* stream);
 
+/*
+ * w4a16_paged_attention over an 8-bit cache (scales; NULL: the 16-bit one), with the
+ * same workspace. The products are formed with q as it is held, exact in either
+ * element type; a key's scale multiplies its fp32 scores, a value's its softmax weights. Of a
+ * place that no row of a sequence sees the scales are not multiplied in either; a place with the scale
+ * NaN makes the rows that see it NaN.
+ */
+W4A16_API w4a16_status w4a16_paged_attention_ex(const w4a16_paged_cache* cache, const w4a16_cache_scales* scales,
+                                                int64_t T, const uint16_t* q, int64_t q_row_stride,
+                                                int64_t q_head_stride, int32_t heads, int64_t max_q_len,
+                                                uint32_t flags, int32_t window, float scale, uint16_t* out,
+                                                float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Bytes of workspace w4a16_paged_attention needs on the current device; 0 if none. */
 W4A16_API size_t w4a16_paged_attention_workspace_bytes(int64_t T, int32_t batch, int32_t heads, int32_t kv_heads,
                                                        int32_t head_dim, int64_t max_q_len);
@@ -492,10 +570,10 @@ W4A16_API w4a16_status w4a16_stream_capture_id(void* stream, uint64_t* id);
 /* Synchronizes `stream`, then reads and clears the current device's sticky
  * error word: W4A16_OK, W4A16_ERR_TIMEOUT (a bounded wait in the GEMV or the
  * GEMM gave up), W4A16_ERR_BAD_OFFSETS (w4a16_grouped_linear, or the query
- * offsets of w4a16_kv_append and w4a16_paged_attention),
+ * offsets of w4a16_kv_append, w4a16_kv_read and w4a16_paged_attention),
  * W4A16_ERR_BAD_ROUTING (w4a16_moe_dispatch, w4a16_moe_combine) or
- * W4A16_ERR_BAD_CACHE (w4a16_rope, w4a16_kv_append, w4a16_paged_attention). The word
- * keeps the first error raised since it was last cleared. */
+ * W4A16_ERR_BAD_CACHE (w4a16_rope, w4a16_kv_append, w4a16_kv_read, w4a16_paged_attention).
+ * The word keeps the first error raised since it was last cleared. */
 W4A16_API w4a16_status w4a16_device_status(void* stream);
 
 /* Static, human-readable name of a status code. */

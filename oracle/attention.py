@@ -1,4 +1,5 @@
-"""Rotary positions, the paged cache and attention over it, in 64 bits.
+"""Rotary positions, head norms, the paged cache in 16 and 8 bits and attention
+over it, in 64 bits.
 
 Plain numpy from the definitions, one token and one head at a time, sharing no
 code with the kernels. Inputs are the stored 16-bit values as float64 (or the
@@ -20,6 +21,25 @@ Bounds. With u the half-spacing of the element type (2^-11 fp16, 2^-8 bf16):
   bounds what the rounding of small weights (relative to a largest one of at
   least 1) and of the result loses below fp16's normal range;
 * the logarithm of the sum: |lse - ref| <= e + 2^-22 |ref|.
+
+* a head's norm x / sqrt(mean x^2 + eps) w: the mean takes at most 22 fp32 roundings
+  (16 elements in a row, 5 sums over threads, the division), eps one; the
+  reciprocal root halves them and adds 2 ulp; two products follow. In all n = 20
+  2^-24 of the value, on top of what turns it:
+      |y - ref| <= u |ref| + n |ref| + (2^-22 + n) (|a c| + |b s|) + tiny
+* a row in 8 bits: x / s is off by two roundings of 2^-24 before it goes to the
+  nearest integer (at most 127 of them: 2^-16 of a step) or the nearest e4m3
+  number (half a step is 2^-4 of the value, or 2^-10 of s below its normal range):
+      |q s - ref| <= (1/2 + 2^-15) s + d,  or  max(2^-4 |ref|, 2^-10 s) (1 + 2^-10) + d
+  where d is how far the row itself may be off, and |s - ref| <= (d + 2^-22 max|x|) / most;
+* attention over 8-bit rows: the integers are exact in the products and the
+  weights p_j s_j (s_j the value's scale) are rounded to the type, so the bounds
+  are those of the 16-bit cache, but for small weights, which are relative to
+  a largest weight times scale: fp16's tiny (1 + max_j s_j sum_j |q_jd|), as the
+  products run in fp16 whatever the type. Where keys and values are brought to
+  16 bits as q s first (whole tiles), w = 2^-11 of fp16, a score is off by w S more, a
+  weight by twice that (it and the sum), and a value by w:
+      |y - ref| <= ... + 2 w (1 + S) A,   |lse - ref| <= ... + w S
 """
 from __future__ import annotations
 
@@ -129,3 +149,81 @@ def attention_tolerance(out, parts, dtype):
 def lse_tolerance(lse, D, parts):
     with np.errstate(invalid="ignore"):
         return np.where(np.isfinite(lse), _slack(D, parts) + 2.0 ** -22 * np.abs(lse), 0.0)
+
+
+NORM = 20 * 2.0 ** -24
+
+MOST = {"int8": 127.0, "e4m3": 448.0}
+LEAST = 2.0 ** -100  # what a row's largest element is taken for if it is less
+
+
+def head_norm(x, weight, eps):
+    """x [..., D] / sqrt(mean(x^2) + eps) * weight."""
+    x = np.asarray(x, np.float64)
+    return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+
+
+def norm_rope_tolerance(y, mag, dtype):
+    return (UNIT[dtype] + NORM) * np.abs(y) + (2.0 ** -22 + NORM) * mag + TINY[dtype]
+
+
+def e4m3(x):
+    """The nearest e4m3 number (ties to even), held to 448."""
+    x = np.asarray(x, np.float64)
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -6))) - 3)
+    return np.clip(np.rint(x / step) * step, -448.0, 448.0)
+
+
+def hold(x, form):
+    """Rows x [..., D] in 8 bits: (q, scale [...])."""
+    x = np.asarray(x, np.float64)
+    scale = np.maximum(np.abs(x).max(-1), LEAST) / MOST[form]
+    y = x / scale[..., None]
+    return np.rint(y) if form == "int8" else e4m3(y), scale
+
+
+def held_tolerance(x, form, off=0.0):
+    """How far q s may be from the row x [..., D], and s from its scale; off: what the row itself may be off."""
+    top = np.maximum(np.abs(x).max(-1), LEAST)
+    worst = np.max(np.broadcast_to(off, x.shape), -1)
+    scale = (top + worst) / MOST[form] * (1 + 2.0 ** -22)
+    s = scale[..., None]
+    step = (0.5 + 2.0 ** -15) * s if form == "int8" else \
+        np.maximum(2.0 ** -4 * (np.abs(x) + off), 2.0 ** -10 * s) * (1 + 2.0 ** -10)
+    return step + off, (worst + 2.0 ** -22 * top) / MOST[form]
+
+
+def attention8(q, k, v, k_scale, v_scale, page_table, q_offsets, kv_lens, **kw):
+    """attention() over the rows that an 8-bit cache holds: k, v [pages, size, G, D] the values as held,
+    k_scale, v_scale [pages, G, size]. parts["V"] is what bounds the small weights there."""
+    def rows(x, s):
+        return np.asarray(x, np.float64) * np.swapaxes(np.asarray(s, np.float64), 1, 2)[..., None]
+
+    out, lse, parts = attention(q, rows(k, k_scale), rows(v, v_scale), page_table, q_offsets, kv_lens, **kw)
+    T, H, D = out.shape
+    G, size = k.shape[2], k.shape[1]
+    causal, window = kw.get("causal", True), kw.get("window", 0)
+    V = np.zeros_like(parts["V"])
+    for t, (b, p) in enumerate(zip(*places(q_offsets, kv_lens))):
+        end = min(kv_lens[b], p + 1) if causal else kv_lens[b]
+        at = range(max(0, p - window + 1) if window else 0, end)
+        if not len(at):
+            continue
+        pages, slots = [page_table[b][j // size] for j in at], [j % size for j in at]
+        for g in range(G):
+            most = np.asarray(v_scale, np.float64)[pages, g, slots].max()
+            V[t, g * (H // G):(g + 1) * (H // G)] = most * np.abs(np.asarray(v, np.float64)[pages, slots, g]).sum(0)
+    parts["V"] = V
+    return out, lse, parts
+
+
+def attention8_tolerance(out, parts, dtype, rounded=False):
+    """rounded: keys and values are brought to 16 bits as q s first."""
+    u, e = UNIT[dtype], _slack(out.shape[2], parts)[..., None]
+    k = UNIT["fp16"] * (1 + parts["S"][..., None]) if rounded else 0.0
+    return u * np.abs(out) + (u + e + 2 * k) * parts["A"] + TINY["fp16"] * (1 + parts["V"])
+
+
+def lse8_tolerance(lse, D, parts, rounded=False):
+    k = UNIT["fp16"] * parts["S"] if rounded else 0.0
+    return lse_tolerance(lse, D, parts) + np.where(np.isfinite(lse), k, 0.0)

@@ -5,8 +5,9 @@ one fp16 scale per group of 32/64/128 input features and fp16 activations
 (LLM170 page, introduction: "W4A16 (int4 sym g128, f16 activations)").
 
 Around the layer: the routed experts' dispatch, GGUF block formats, and the
-attention that sits between a decoder's projections (rotary positions, a paged
-key/value cache and attention over it, fp16 or bf16).
+attention that sits between a decoder's projections (norms of the query and key
+heads, rotary positions, a paged key/value cache in 16 or 8 bits and attention
+over it, fp16 or bf16).
 
 This module is a thin ctypes binding over the C ABI of ``libw4a16.so``
 (declared in ``include/w4a16.h``): it checks tensor dtypes and shapes,
@@ -36,7 +37,7 @@ import torch
 
 __all__ = ["pack", "unpack", "linear", "linear_gated", "grouped_linear", "grouped_linear_gather", "moe_route",
            "moe_dispatch", "moe_combine", "blocks_row_bytes", "blocks_linear", "blocks_dequant", "BLOCK_FORMATS",
-           "rope_table", "rope", "kv_append", "paged_attention",
+           "rope_table", "rope", "kv_append", "kv_read", "paged_attention",
            "workspace_bytes", "device_status", "STATIC_WEIGHTS",
            "W4A16Error", "lib", "LIB_PATH", "EXPORTS", "STATUS"]
 
@@ -65,6 +66,16 @@ class _PagedCache(ctypes.Structure):
                 ("head_dim", _I32), ("dtype", _I32)]
 
 
+class _CacheScales(ctypes.Structure):
+    """w4a16_cache_scales"""
+    _fields_ = [("format", _I32), ("k", _P), ("v", _P), ("page_stride", _I64), ("head_stride", _I64)]
+
+
+class _HeadNorms(ctypes.Structure):
+    """w4a16_head_norms"""
+    _fields_ = [("q", _P), ("k", _P), ("eps", ctypes.c_float)]
+
+
 # name -> (restype, argtypes); mirrors include/w4a16.h
 EXPORTS = {
     "w4a16_pack": (_I32, [_P, _I64, _I64, _I32, _P, _P, _P]),
@@ -86,6 +97,12 @@ EXPORTS = {
     "w4a16_blocks_linear": (_I32, [_I32, _P, _P, _P, _I64, _I64, _I64, _P]),
     "w4a16_blocks_dequant": (_I32, [_I32, _P, _I64, _I64, _P, _P]),
     "w4a16_rope": (_I32, [_I32, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, _P]),
+    "w4a16_rope_norm": (_I32, [_I32, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, ctypes.c_float, _P, _P]),
+    "w4a16_kv_append_ex": (_I32, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P,
+                                  _P]),
+    "w4a16_kv_read": (_I32, [_P, _P, _I64, _P, _P, _P]),
+    "w4a16_paged_attention_ex": (_I32, [_P, _P, _I64, _P, _I64, _I64, _I32, _I64, ctypes.c_uint32, _I32,
+                                        ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "w4a16_kv_append": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P]),
     "w4a16_paged_attention": (_I32, [_P, _I64, _P, _I64, _I64, _I32, _I64, ctypes.c_uint32, _I32, ctypes.c_float,
                                      _P, _P, _P, _SZ, _P]),
@@ -108,6 +125,9 @@ CAUSAL = 1
 
 # element types of the attention operators (W4A16_DTYPE_* in include/w4a16.h)
 _DTYPES = {torch.float16: 1, torch.bfloat16: 2}
+
+# element types of an 8-bit cache (W4A16_CACHE_* in include/w4a16.h)
+_HELD = {torch.int8: 1, torch.float8_e4m3fn: 2}
 
 # GGUF block formats (W4A16_FORMAT_* in include/w4a16.h)
 BLOCK_FORMATS = {"q4_k": 1, "q5_1": 2}
@@ -490,13 +510,14 @@ def rope_table(rows: int, rotary_dim: int, base: float = 10000.0, device="cuda")
 
 def _packer(c_type) -> struct.Struct:
     """Packs the fields of a ctypes structure, in native alignment: several times faster than making one."""
-    code = {_P: "P", ctypes.c_char_p: "P", _I64: "q", _I32: "i"}
+    code = {_P: "P", ctypes.c_char_p: "P", _I64: "q", _I32: "i", ctypes.c_float: "f"}
     return struct.Struct("".join(code[t] for _, t in c_type._fields_))
 
 
 # The calls below are made once per layer and token, so their checks ask each
 # tensor for little: its device index (-1 off the GPU), type, shape and strides.
 _CACHE, _ROTARY = _packer(_PagedCache), _packer(_Rotary)
+_SCALES, _NORMS = _packer(_CacheScales), _packer(_HeadNorms)
 
 
 def _raw_stream(index: int) -> int:
@@ -560,18 +581,33 @@ def _rotary(table, positions, pair_axes, interleaved: bool, T: int, index: int):
     return _ROTARY.pack(table.data_ptr(), rows, dim, 1 if interleaved else 0, at, axes, axis_ptr), axis_of
 
 
+def _norm(weight, name: str, head_dim: int, index: int) -> int:
+    """The address of a head norm's weights, 0 without."""
+    if weight is None:
+        return 0
+    if not isinstance(weight, torch.Tensor) or weight.dtype != torch.float32 or weight.get_device() != index \
+            or tuple(weight.shape) != (head_dim,) or not weight.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous torch.float32 [head_dim] tensor on the other tensors' device")
+    return weight.data_ptr()
+
+
 def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, pair_axes=None, interleaved: bool = False,
-         out: torch.Tensor | None = None) -> torch.Tensor:
+         out: torch.Tensor | None = None, norm: torch.Tensor | None = None, eps: float = 1e-6) -> torch.Tensor:
     """x turned by its tokens' positions: x fp16 or bf16 [T, heads, head_dim]
     (a view of a fused projection will do), positions int32 [T] or [axes, T],
     table fp32 [rows, rotary_dim] (:func:`rope_table`); elements past rotary_dim
     are copied. Pair i is elements (i, i + rotary_dim / 2), or (2i, 2i + 1) with
     ``interleaved``. ``pair_axes`` gives the axis (0 to 3) whose position turns
     each pair (time, height and width of a video's patches, say); without it
-    axis 0 turns all. ``out`` may be x itself."""
+    axis 0 turns all. ``out`` may be x itself.
+
+    With ``norm`` (fp32 [head_dim]) each head is divided by its root mean square and
+    weighted before it is turned, x / sqrt(mean(x^2) + eps) * norm, in the
+    same pass and in fp32 up to the one rounding of the result."""
     shape, sx = _rows(x, "x")
     index = x.get_device()
     T, H, D = shape
+    weight = _norm(norm, "norm", D, index)
     if positions is None:
         raise ValueError("positions: expected contiguous [T] or [axes, T]")
     r, keep = _rotary(table, positions, pair_axes, interleaved, T, index)
@@ -581,17 +617,43 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, pair_axe
         out_shape, so = _rows(out, "out", x.dtype, index)
         if out_shape != shape:
             raise ValueError("out: must have x's shape")
-    status = (_lib or lib()).w4a16_rope(_DTYPES[x.dtype], x.data_ptr(), sx[0], sx[1], out.data_ptr(), so[0], so[1], T,
-                                        H, D, r, _raw_stream(index))
+    if weight:
+        status = (_lib or lib()).w4a16_rope_norm(_DTYPES[x.dtype], x.data_ptr(), sx[0], sx[1], out.data_ptr(), so[0],
+                                                 so[1], T, H, D, weight, eps, r, _raw_stream(index))
+    else:
+        status = (_lib or lib()).w4a16_rope(_DTYPES[x.dtype], x.data_ptr(), sx[0], sx[1], out.data_ptr(), so[0],
+                                            so[1], T, H, D, r, _raw_stream(index))
     if status:
         raise W4A16Error(status, "w4a16_rope")
     return out
 
 
-def _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, dtype, index: int):
-    """(packed w4a16_paged_cache, batch, kv_heads, head_dim)"""
+def _packed_scales(k_cache, k_scale, v_scale, index: int):
+    """Packed w4a16_cache_scales of an 8-bit cache; None for a 16-bit one, which has none."""
+    form = _HELD.get(k_cache.dtype) if isinstance(k_cache, torch.Tensor) else None
+    if form is None:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale are an 8-bit cache's (torch.int8 or torch.float8_e4m3fn)")
+        return None
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.ndim != 3 or t.get_device() != index:
+            raise ValueError(f"{name}: an 8-bit cache needs a 3-d torch.float32 tensor on the other tensors' device")
+    shape, stride = k_scale.shape, k_scale.stride()
+    if v_scale.shape != shape or v_scale.stride() != stride:
+        raise ValueError("k_scale and v_scale must have the same shape and strides")
+    if k_cache.ndim != 4 or shape != (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1]):
+        raise ValueError("k_scale, v_scale: expected [pages, kv_heads, page_size]")
+    if stride[2] != 1:
+        raise ValueError("k_scale, v_scale: the last dimension must be contiguous")
+    # (a dimension of one has any stride)
+    return _SCALES.pack(form, k_scale.data_ptr(), v_scale.data_ptr(), stride[0] if shape[0] > 1 else 0,
+                        stride[1] if shape[1] > 1 else 0)
+
+
+def _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, dtype, index: int, held=None):
+    """(packed w4a16_paged_cache, batch, kv_heads, head_dim); held: the cache's own type where that is not dtype"""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or t.ndim != 4 or t.dtype != dtype or t.get_device() != index:
+        if not isinstance(t, torch.Tensor) or t.ndim != 4 or t.dtype != (held or dtype) or t.get_device() != index:
             raise ValueError(f"{name}: expected a 4-d tensor of the other tensors' type and device")
     shape, stride = k_cache.shape, k_cache.stride()
     if v_cache.shape != shape or v_cache.stride() != stride:
@@ -618,7 +680,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
               page_table: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor,
               q: torch.Tensor | None = None, table: torch.Tensor | None = None,
               positions: torch.Tensor | None = None, pair_axes=None, interleaved: bool = False,
-              q_out: torch.Tensor | None = None):
+              q_out: torch.Tensor | None = None, q_norm: torch.Tensor | None = None,
+              k_norm: torch.Tensor | None = None, eps: float = 1e-6, k_scale: torch.Tensor | None = None,
+              v_scale: torch.Tensor | None = None):
     """Stores the new tokens' k and v (fp16 or bf16 [T, kv_heads, head_dim]) into
     the paged cache and, with ``table``, turns k and q by their rotary positions
     on the way (``positions`` and the rest as in :func:`rope`; without
@@ -630,14 +694,24 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     b's new tokens are rows q_offsets[b] to q_offsets[b + 1] of k, v and q;
     kv_lens[b] counts its cached tokens with these among them; its place p lives in
     slot p % page_size of page page_table[b, p // page_size]. All three are int32
-    on the device: a captured graph follows their values."""
+    on the device: a captured graph follows their values.
+
+    ``q_norm`` and ``k_norm`` (fp32 [head_dim]) divide the heads of q and k by their
+    root mean squares and weight them before they are turned, as in :func:`rope`.
+
+    The cache may hold 8 bits an element (torch.int8 or torch.float8_e4m3fn, strides
+    multiples of 16): ``k_scale`` and ``v_scale``, fp32 [pages, kv_heads, page_size] in
+    any strides (multiples of 4) with contiguous slots, then get each row's scale, max|x| / 127
+    (or 448), and the cache x / scale, rounded once from fp32."""
     shape, sk = _rows(k, "k")
     index, dtype = k.get_device(), k.dtype
+    scales = _packed_scales(k_cache, k_scale, v_scale, index)
     v_shape, sv = _rows(v, "v", dtype, index)
     if v_shape != shape:
         raise ValueError("k and v must have the same shape")
     T, G, D = shape
-    c, _, cache_heads, cache_dim = _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, dtype, index)
+    c, _, cache_heads, cache_dim = _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, dtype, index,
+                                                 k_cache.dtype if scales else None)
     if cache_heads != G or cache_dim != D:
         raise ValueError("the cache must have k's heads and head_dim")
     H, sq, q_ptr, out_ptr = 0, (0, 0), 0, 0
@@ -655,17 +729,66 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         r, keep = _rotary(table, positions, pair_axes, interleaved, T, index)
     elif positions is not None or pair_axes is not None:
         raise ValueError("positions and pair_axes need table")
-    status = (_lib or lib()).w4a16_kv_append(c, T, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], q_ptr,
-                                             sq[0], sq[1], H, out_ptr, r, _raw_stream(index))
+    if q_norm is not None and q is None:
+        raise ValueError("q_norm without q")
+    if scales or q_norm is not None or k_norm is not None:
+        norms = None
+        if q_norm is not None or k_norm is not None:
+            norms = _NORMS.pack(_norm(q_norm, "q_norm", D, index), _norm(k_norm, "k_norm", D, index), eps)
+        status = (_lib or lib()).w4a16_kv_append_ex(c, scales, T, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0],
+                                                    sv[1], q_ptr, sq[0], sq[1], H, out_ptr, norms, r,
+                                                    _raw_stream(index))
+    else:
+        status = (_lib or lib()).w4a16_kv_append(c, T, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], q_ptr,
+                                                 sq[0], sq[1], H, out_ptr, r, _raw_stream(index))
     if status:
         raise W4A16Error(status, "w4a16_kv_append")
     return q_out
 
 
+def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, q_offsets: torch.Tensor,
+            kv_lens: torch.Tensor, rows: int, dtype: torch.dtype | None = None, k_scale: torch.Tensor | None = None,
+            v_scale: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+            v_out: torch.Tensor | None = None):
+    """The inverse of :func:`kv_append`: the keys and values that the cache holds at
+    the places of ``rows`` rows, each [rows, kv_heads, head_dim] and contiguous (new, or
+    ``k_out`` and ``v_out``). Sequence b's rows are q_offsets[b] to q_offsets[b + 1], and the last of
+    them is its place kv_lens[b] - 1: a prefix of n places is read with kv_lens n and n
+    rows. From an 8-bit cache (``k_scale`` and ``v_scale``) the rows come in ``dtype``,
+    torch.float16 or torch.bfloat16; a 16-bit one's come as they are. A row
+    without a place (its sequence is shorter) is 0."""
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
+        raise ValueError("k_cache: expected a CUDA tensor")
+    index = k_cache.get_device()
+    scales = _packed_scales(k_cache, k_scale, v_scale, index)
+    if dtype is None and k_out is not None:
+        dtype = k_out.dtype
+    if scales is None and dtype is None:
+        dtype = k_cache.dtype
+    if dtype not in _DTYPES:
+        raise ValueError("dtype: expected torch.float16 or torch.bfloat16")
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    c, _, G, D = _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, dtype, index,
+                               k_cache.dtype if scales else None)
+    out = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty((rows, G, D), dtype=dtype, device=k_cache.device)
+        elif _rows(t, name, dtype, index)[0] != (rows, G, D) or not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous [rows, kv_heads, head_dim]")
+        out.append(t)
+    status = (_lib or lib()).w4a16_kv_read(c, scales, rows, out[0].data_ptr(), out[1].data_ptr(), _raw_stream(index))
+    if status:
+        raise W4A16Error(status, "w4a16_kv_read")
+    return out[0], out[1]
+
+
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                     q_offsets: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int, causal: bool = True,
                     window: int = 0, scale: float | None = None, out: torch.Tensor | None = None,
-                    return_lse: bool = False):
+                    return_lse: bool = False, k_scale: torch.Tensor | None = None,
+                    v_scale: torch.Tensor | None = None):
     """Attention of the new tokens' queries (fp16 or bf16 [T, heads, head_dim])
     over the paged cache of :func:`kv_append`: softmax(scale q k^T) v per row,
     heads in groups of heads / kv_heads sharing a cached head. A row sees its sequence's
@@ -674,12 +797,17 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     of new tokens (it chooses the kernels, so one that is larger than need be costs time and
     some accuracy; the lengths themselves stay on the device). ``scale`` defaults to head_dim^-1/2. A row that sees nothing gets 0.
 
+    An 8-bit cache (torch.int8 or torch.float8_e4m3fn) is read with its ``k_scale`` and
+    ``v_scale``, which :func:`kv_append` wrote.
+
     Returns out [T, heads, head_dim], or (out, lse) with ``return_lse``: lse
     fp32 [T, heads] is the natural logarithm of the softmax's sum."""
     shape, sq = _rows(q, "q")
     index = q.get_device()
     T, H, D = shape
-    c, B, G, cache_dim = _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, q.dtype, index)
+    scales = _packed_scales(k_cache, k_scale, v_scale, index)
+    c, B, G, cache_dim = _packed_cache(k_cache, v_cache, page_table, q_offsets, kv_lens, q.dtype, index,
+                                       k_cache.dtype if scales else None)
     if cache_dim != D or G == 0 or H % G != 0:
         raise ValueError("the cache must have q's head_dim, and heads must be a multiple of its heads")
     out = _rows_out(out, q, shape, "out", index)
@@ -690,10 +818,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ws = _ws.get((index, st, "attention"))
     if need and (ws is None or ws.numel() < need):
         ws = _workspace(q.device, ctypes.c_void_p(st), need, "attention")
-    status = h.w4a16_paged_attention(c, T, q.data_ptr(), sq[0], sq[1], H, max_q_len, CAUSAL if causal else 0, window,
-                                     D ** -0.5 if scale is None else scale, out.data_ptr(),
-                                     lse.data_ptr() if return_lse else 0, ws.data_ptr() if need else 0,
-                                     ws.numel() if need else 0, st)
+    rest = (T, q.data_ptr(), sq[0], sq[1], H, max_q_len, CAUSAL if causal else 0, window,
+            D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr() if return_lse else 0,
+            ws.data_ptr() if need else 0, ws.numel() if need else 0, st)
+    status = h.w4a16_paged_attention_ex(c, scales, *rest) if scales else h.w4a16_paged_attention(c, *rest)
     if status:
         raise W4A16Error(status, "w4a16_paged_attention")
     return (out, lse) if return_lse else out
