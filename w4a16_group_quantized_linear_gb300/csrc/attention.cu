@@ -1,35 +1,7 @@
-// Attention of new tokens over a paged cache: which kernel serves which sequences.
-//
-// A sequence's work is a number of rows per cached head: its new tokens times
-// the query heads that share the head. With few rows the cache's bytes are all
-// that counts and attention_step.cu takes them; past 16 the 8-row products
-// of that kernel are what it waits for (with a variant for 32 rows, 25 rows of
-// 16 sequences took 94 us, where the tiles take 87, and 32 of 64 sequences 132
-// against 130), and attention_tile.cu takes 256 rows to a tile on the tensor
-// cores. The lengths are on the device, so where a batch may hold both kinds
-// both kernels are launched, and each passes over the other's.
-#include "attention.cuh"
+// Attention of new tokens over a paged 16-bit cache: the kernels of its plan.
+#include "attention_plan.cuh"
 
 namespace w4a16 {
-namespace {
-
-struct Plan {
-    bool step, tile;
-    int step_rows;  // most rows of a sequence of the step kernel
-};
-
-Plan plan_for(int64_t T, int64_t batch, int heads, int kv_heads, int64_t max_q_len) {
-    const int64_t ratio = heads / kv_heads, most = (max_q_len < T ? max_q_len : T) * ratio;
-    Plan p;
-    p.tile = most > kStepRows;
-    // every sequence has max_q_len new tokens, as one alone has: no second kind
-    const bool alike = T == batch * max_q_len || batch == 1;
-    p.step = !p.tile || (ratio <= kStepRows && !alike);
-    p.step_rows = (int)(most < kStepRows ? most : kStepRows);
-    return p;
-}
-
-}  // namespace
 
 size_t attention_workspace_bytes(const DeviceInfo& dev, int64_t T, int batch, int heads, int kv_heads, int head_dim,
                                  int64_t max_q_len) {

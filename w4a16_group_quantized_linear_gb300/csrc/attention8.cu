@@ -1,5 +1,6 @@
 // Attention of new tokens over a paged cache of 8-bit rows: one warp per row
 // (query head of a new token), the places in order, with the running maximum of the softmax.
+#include "attention_plan.cuh"
 #include "cache8.cuh"
 
 namespace w4a16 {
@@ -10,6 +11,7 @@ constexpr int kThreads = 128;
 struct Args8 {
     AttentionArgs a;
     ScaleArgs s;
+    int min_rows;  // sequences with fewer rows per cached head are attention8_step.cu's
 };
 
 template <class E, class H, int D>
@@ -31,6 +33,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const __grid_constant__ A
         raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
         return;
     }
+    if (count * a.ratio < x.min_rows) return;
     const int length = cache_length(a.c, __ldg(a.c.kv_lens + b));
     const int place = length - count + (int)(t - first);
     const int high = a.causal ? min(length, place + 1) : length;
@@ -89,9 +92,17 @@ w4a16_status launch(const Args8& x, cudaStream_t st) {
 
 }  // namespace
 
-w4a16_status attention8_launch(const DeviceInfo&, int dtype, int format, const AttentionArgs& a, const ScaleArgs& s,
-                               void*, size_t, cudaStream_t st) {
-    const Args8 x{a, s};
+w4a16_status attention8_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
+                               const ScaleArgs& s, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+    if (!workspace || workspace_bytes < attention_workspace_bytes(dev, a.c.T, a.c.batch, a.heads, a.c.kv_heads,
+                                                                  a.c.head_dim, a.max_q_len))
+        return W4A16_ERR_WORKSPACE;
+    const Plan p = plan_for(a.c.T, a.c.batch, a.heads, a.c.kv_heads, a.max_q_len);
+    if (p.step) {
+        const w4a16_status e = attention8_step_launch(dev, dtype, format, a, s, p.step_rows, workspace, st);
+        if (e != W4A16_OK || !p.tile) return e;
+    }
+    const Args8 x{a, s, p.step ? kStepRows + 1 : 1};
     const bool f16 = dtype == W4A16_DTYPE_F16;
     if (format == W4A16_CACHE_INT8) return f16 ? launch<Fp16, HeldInt8>(x, st) : launch<Bf16, HeldInt8>(x, st);
     return f16 ? launch<Fp16, HeldE4m3>(x, st) : launch<Bf16, HeldE4m3>(x, st);

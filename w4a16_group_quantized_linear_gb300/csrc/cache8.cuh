@@ -39,6 +39,23 @@ struct HeldInt8 {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(v >> (8 * i));
     }
+    // Four of them as fp16 pairs, exactly: with its sign bit flipped a byte u is q + 128, and the low byte
+    // of fp16's 1024 + u.
+    __device__ static __forceinline__ uint32_t minus_1152(uint32_t v) {
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&v),
+                                  __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ static __forceinline__ void to_fp16(uint32_t v, uint32_t& b01, uint32_t& b23) {
+        v ^= 0x80808080u;
+        b01 = minus_1152(__byte_perm(v, 0x64646464u, 0x4140));
+        b23 = minus_1152(__byte_perm(v, 0x64646464u, 0x4342));
+    }
+    __device__ static __forceinline__ void to_fp16_apart(uint32_t v, uint32_t& b02, uint32_t& b13) {
+        v ^= 0x80808080u;
+        b02 = minus_1152(__byte_perm(v, 0x64646464u, 0x4240));
+        b13 = minus_1152(__byte_perm(v, 0x64646464u, 0x4341));
+    }
 };
 
 struct HeldE4m3 {
@@ -50,10 +67,18 @@ struct HeldE4m3 {
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * inv), "f"(x[2] * inv));
         return (uint32_t)lo | (uint32_t)hi << 16;
     }
+    __device__ static __forceinline__ void to_fp16(uint32_t v, uint32_t& b01, uint32_t& b23) {
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(b01), "=r"(b23)
+            : "r"(v));
+    }
+    __device__ static __forceinline__ void to_fp16_apart(uint32_t v, uint32_t& b02, uint32_t& b13) {
+        to_fp16(__byte_perm(v, 0, 0x3120), b02, b13);
+    }
     __device__ static __forceinline__ void decode4(uint32_t v, float* x) {
         uint32_t lo, hi;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)v));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(v >> 16)));
+        to_fp16(v, lo, hi);
         const float2 a = Fp16::unpack(lo), b = Fp16::unpack(hi);
         x[0] = a.x;
         x[1] = a.y;
@@ -85,6 +110,8 @@ w4a16_status append_ex_launch(const DeviceInfo& dev, int dtype, int format, cons
                               const w4a16_head_norms* norms, const w4a16_rotary* rotary, cudaStream_t st);
 w4a16_status read_launch(const DeviceInfo& dev, int dtype, int format, const CacheArgs& c, const ScaleArgs& s,
                          uint16_t* k, uint16_t* v, cudaStream_t st);
+w4a16_status attention8_step_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
+                                    const ScaleArgs& s, int max_rows, void* workspace, cudaStream_t st);
 w4a16_status attention8_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
                                const ScaleArgs& s, void* workspace, size_t workspace_bytes, cudaStream_t st);
 
