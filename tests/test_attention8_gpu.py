@@ -1,6 +1,7 @@
 """Attention over an 8-bit paged cache, on the GPU, against the 64-bit oracle
 (oracle/attention.py derives the bounds)."""
 import ctypes
+import time
 
 import numpy as np
 import pytest
@@ -8,6 +9,7 @@ import pytest
 from oracle import attention as oa
 from test_kv_cache8_gpu import FORMS, Rows, _held, _normals, _numbers
 from test_paged_attention_canaries_gpu import GUARD, PATTERN, _guarded, _intact
+from test_paged_attention_errors_gpu import NORMAL_NS, SHORT_NS, TIMEOUT, _tmem, hooks  # noqa: F401
 from test_paged_attention_gpu import DTYPES, HEADS, LENS, Batch, _np, _status_stays_clean, _t, w4  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -66,7 +68,7 @@ class Batch8(Batch):
             empty = np.isneginf(lse_ref)
             assert np.array_equal(np.isneginf(got), empty)
             d = np.abs(np.where(empty, 0, got) - np.where(empty, 0, lse_ref))
-            assert (d <= oa.lse8_tolerance(lse_ref, self.D, parts, tiles)).all(), d.max()
+            assert (d <= oa.lse8_tolerance(lse_ref, self.D, parts, self.dtype, tiles)).all(), d.max()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -388,3 +390,44 @@ def test_append_from_16_bit_views_of_another_shape_is_refused(w4, cuda_device): 
         narrow = narrow[:narrow.numel() // (16 * 2 * 64) * (16 * 2 * 64)].view(-1, 16, 2, 64)
         w4.kv_read(narrow, narrow, *r.args, 2, dtype=torch.float16, k_scale=r.ks[:len(narrow)],
                    v_scale=r.vs[:len(narrow)])
+
+
+# ------------------------------------------------------- bounded waits of the tiles --
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,limits", [([(300, 4000)], (0, 1, 2, 3)), ([(20, 30000)], (0, 1, 2, 3)),
+                                         ([(200, 200), (100, 700)], (0, 1))])
+def test_wait_times_out_and_next_call_is_correct(hooks, cuda_device, lens, limits, D):  # noqa: F811
+    """As for 16-bit caches: converters that stop after a few blocks, and a 1 ms limit."""
+    import torch
+
+    import w4a16_group_quantized_linear_gb300 as w4
+
+    lib = hooks
+    b = Batch8(cuda_device, "bf16", "int8", 10, 2, D, 16, lens, seed=40)
+    T = b.offsets[-1]
+    c = w4._packed_cache(b.k8, b.v8, b.page_table, b.q_offsets, b.kv_lens, b.q.dtype, 0, b.k8.dtype)[0]
+    s = w4._packed_scales(b.k8, b.k_scale, b.v_scale, 0)
+    out = torch.empty(T, 10, D, dtype=torch.bfloat16, device=cuda_device)
+    n = int(lib.w4a16_paged_attention_workspace_bytes(T, len(lens), 10, 2, D, b.max_q))
+    ws = torch.empty(n, dtype=torch.uint8, device=cuda_device)
+    st = w4._stream(cuda_device)
+
+    def call():
+        assert lib.w4a16_workspace_init(w4._ptr(ws), n, st) == 0
+        return lib.w4a16_paged_attention_ex(c, s, T, w4._ptr(b.q), b.q.stride(0), b.q.stride(1), 10, b.max_q, 1, 0,
+                                            D ** -0.5, w4._ptr(out), None, w4._ptr(ws), n, st)
+
+    for issue_limit in limits:
+        a0, f0 = _tmem(lib)
+        assert lib.w4a16_test_set_hooks(SHORT_NS, issue_limit) == 0
+        assert call() == 0
+        t0 = time.perf_counter()
+        assert lib.w4a16_device_status(st) == TIMEOUT, issue_limit
+        assert time.perf_counter() - t0 < 1.0
+        a1, f1 = _tmem(lib)
+        assert a1 - a0 > 0 and a1 - a0 == f1 - f0
+    assert lib.w4a16_test_set_hooks(NORMAL_NS, -1) == 0
+    assert call() == 0
+    assert lib.w4a16_device_status(st) == 0
+    b.check(out)

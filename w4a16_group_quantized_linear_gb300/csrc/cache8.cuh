@@ -27,6 +27,7 @@ struct Held16 {
 struct HeldInt8 {
     static constexpr int kFormat = W4A16_CACHE_INT8;
     static constexpr float kMost = 127.0f;
+    static constexpr int kRoom = 7;  // 2 kMost 2^kRoom is below fp16's 65504
     // x inv, |x inv| <= 127 but for rounding, to the nearest integers (ties to even): with
     // 1.5 * 2^23 added, an integer's two's complement is in the low bits of the sum
     __device__ static __forceinline__ uint32_t encode4(const float* x, float inv) {
@@ -61,6 +62,7 @@ struct HeldInt8 {
 struct HeldE4m3 {
     static constexpr int kFormat = W4A16_CACHE_E4M3;
     static constexpr float kMost = 448.0f;
+    static constexpr int kRoom = 6;
     __device__ static __forceinline__ uint32_t encode4(const float* x, float inv) {
         uint16_t lo, hi;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
@@ -112,6 +114,8 @@ w4a16_status read_launch(const DeviceInfo& dev, int dtype, int format, const Cac
                          uint16_t* k, uint16_t* v, cudaStream_t st);
 w4a16_status attention8_step_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
                                     const ScaleArgs& s, int max_rows, void* workspace, cudaStream_t st);
+w4a16_status attention8_tile_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
+                                    const ScaleArgs& s, int min_rows, void* workspace, cudaStream_t st);
 w4a16_status attention8_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
                                const ScaleArgs& s, void* workspace, size_t workspace_bytes, cudaStream_t st);
 

@@ -203,6 +203,8 @@ cudaError_t split_set_test_hooks(const TestHooks& h);
 cudaError_t split_get_test_counters(TestCounters* c);
 cudaError_t attention_set_test_hooks(const TestHooks& h);
 cudaError_t attention_get_test_counters(TestCounters* c);
+cudaError_t attention8_set_test_hooks(const TestHooks& h);
+cudaError_t attention8_get_test_counters(TestCounters* c);
 #endif
 
 // Records a failed CUDA runtime call for w4a16_last_cuda_error (per host thread).
