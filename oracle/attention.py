@@ -40,11 +40,11 @@ Bounds. With u the half-spacing of the element type (2^-11 fp16, 2^-8 bf16):
   of two of the row's largest element m_q: exact above 2^-14 of it, else off by 2^-25
   of it, a score by r = 2^-24 scale m_q max_j sum_d |k_jd|. Where keys and values are
   brought to fp16 as q s first (whole tiles), divided by a power of two that takes the
-  largest of 128 places past 2^14, each is off by w = 2^-11 of itself, or by 2^-25
-  2^-14 of that largest, below 2^-31 of the sequence's largest scale s_k or s_v (127 of
-  it, or 448, is the element). So a score is off by r = w S + 2^-31 s_k scale sum_d |q_d|
-  more, a weight by twice that (it and the sum), a value by w and 2^-31 s_v:
-      |y - ref| <= ... + 2 (r + w) A + 2^-31 s_v,   |lse - ref| <= ... + r
+  largest of 128 places past 2^14, each is off by w = 2^-11 of itself, or by twice
+  2^-25 in fp16's own units (a product and a sum), of which 2^6 at least make the block's largest scale:
+  below 2^-30 of the sequence's largest scale s_k or s_v. So a score is off by r = w S + 2^-30 s_k scale sum_d |q_d|
+  more, a weight by twice that (it and the sum), a value by w and 2^-30 s_v:
+      |y - ref| <= ... + 2 (r + w) A + 2^-30 s_v,   |lse - ref| <= ... + r
   and the weights' factor is the block's, so tiny takes 2 s_v sum_j |q_jd|.
 """
 from __future__ import annotations
@@ -231,7 +231,7 @@ def attention8(q, k, v, k_scale, v_scale, page_table, q_offsets, kv_lens, **kw):
             parts["V"][t, mine] = vs[pages, g, slots].max() * held
             parts["all_V"][t, mine] = 2 * s_v * held
             parts["Q"][t, mine] = 2.0 ** -24 * scale * q[t, mine].max(-1) * keys.max()
-            parts["K"][t, mine] = 2.0 ** -31 * s_k * scale * q[t, mine].sum(-1)
+            parts["K"][t, mine] = 2.0 ** -30 * s_k * scale * q[t, mine].sum(-1)
             parts["s_v"][t, mine] = s_v
     return out, lse, parts
 
@@ -247,7 +247,7 @@ def attention8_tolerance(out, parts, dtype, rounded=False):
     u, w = UNIT[dtype], UNIT["fp16"]
     e = (_slack(out.shape[2], parts) + 2 * _off8(parts, dtype, rounded) + (2 * w if rounded else 0.0))[..., None]
     tol = u * np.abs(out) + (w + e) * parts["A"] + TINY["fp16"] * (1 + parts["all_V" if rounded else "V"])
-    return tol + (2.0 ** -31 * parts["s_v"][..., None] if rounded else 0.0)
+    return tol + (2.0 ** -30 * parts["s_v"][..., None] if rounded else 0.0)
 
 
 def lse8_tolerance(lse, D, parts, dtype, rounded=False):

@@ -65,7 +65,7 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;      // places per block: MMA N of the scores, K of the output
 constexpr int kLoadK = 8, kMmaWarp = 9, kPlanWarp = 10, kLoadV = 11;
 constexpr int kConvert = 12, kConverters = 4;  // warps of an 8-bit cache in place of the loads
-constexpr int kBarBytes = 1856;  // struct Bars
+constexpr int kBarBytes = 2048;  // struct Bars
 constexpr int kFactors = 16;     // blocks whose factors are kept: more than the converters can be ahead
 constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 // How far (log2) a score may pass the running maximum of a whole tile before the maximum moves. A
@@ -94,14 +94,22 @@ __device__ __forceinline__ constexpr bool may_issue(int) { return true; }
 template <class H>
 constexpr int threads_of() { return H::kFormat != 0 ? (kConvert + kConverters) * 32 : 384; }
 
-template <int D>
+template <class H, int D>
 struct Layout {
     static constexpr int kSlabs = D / 64;              // 64-element slabs: 128-byte swizzled rows
     static constexpr int kSlabBytes = kBlock * 128;
     static constexpr int kStageBytes = kSlabs * kSlabBytes;  // one k or v block; also half a tile's queries
-    static constexpr int kStages = (224 * 1024 - 2 * kStageBytes) / kStageBytes;
+    // An 8-bit cache's rows wait in rings of the converting warps, kRaw entries of 32 rows and the scales of
+    // both k and v. Of what is loaded ahead, no more than two blocks may be past the one that is
+    // converted: the plan lays out the entries of such blocks while the tiles before them are still in work.
+    static constexpr bool kHeld8 = H::kFormat != 0;
+    static constexpr int kRaw = !kHeld8 ? 0 : D == 128 ? 3 : 5;
+    static_assert(kRaw <= 5, "two blocks ahead");
+    static constexpr int kRawBytes = 32 * D + 256;
+    static constexpr int kStages = !kHeld8 ? (224 * 1024 - 2 * kStageBytes) / kStageBytes : D == 128 ? 3 : 7;
     static constexpr int kRingAt = 2 * kStageBytes;
-    static constexpr int kBarsAt = kRingAt + kStages * kStageBytes;
+    static constexpr int kRawAt = kRingAt + kStages * kStageBytes;
+    static constexpr int kBarsAt = kRawAt + kConverters * kRaw * kRawBytes;
     static constexpr int kSmem = kBarsAt + kBarBytes + 1024;  // barriers, and the 1024-byte alignment
 };
 
@@ -135,7 +143,7 @@ struct Bars {
     uint64_t work_full[kEntries], work_empty[kEntries];
     uint64_t mma_done;
     Entry work[kEntries];
-    int factors[kFactors];  // of an 8-bit cache's blocks, by their place in the run
+    int4 factors[kFactors];  // of an 8-bit cache's blocks, by their place in the run
     float2 pair_stats[kHalf];
     uint32_t tmem;
     int abort;
@@ -292,6 +300,10 @@ template <class E>
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major) {
     const uint32_t type = E::kDtype == W4A16_DTYPE_BF16 ? 1u : 0u;
     return ptx::idesc_f16_f32(kHalf, n) | (type << 7) | (type << 10) | ((b_n_major ? 1u : 0u) << 16);
+}
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_size) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_size) : "memory");
 }
 
 // A lane's piece of a bf16 row that PIECES lanes hold, in fp16, divided by the power of two of the row's
@@ -474,46 +486,44 @@ __device__ __forceinline__ bool find_run(const TileArgs& x, int* scratch, Run& r
     return true;
 }
 
-// A block's factors: its keys are formed divided by 2^key, its values by 2^value.
+// The factors of 32 places of a block: keys are formed divided by 2^key, values by 2^value.
 __device__ __forceinline__ int pack_factors(int key, int value) { return (key & 0xFFFF) | (value << 16); }
 __device__ __forceinline__ int key_factor(int f) { return (int)(int16_t)f; }
 __device__ __forceinline__ int value_factor(int f) { return f >> 16; }
 __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(d)
-        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-    return *reinterpret_cast<float2*>(&d);
+// What a row's elements are multiplied by, f = g 2^-h, for products that are rounded once: with G = fp16(g) and
+// d = fp16(g - G),  q f = (q 2^-h) G + (q 2^-h) d.  2^-h, up to 2^-15, keeps g and d normal where f is far
+// below the block's largest; q 2^-h is exact.
+struct RowFactor {
+    uint32_t gd;  // G, d
+    uint32_t pc;  // 2^-h, and -1152 2^-h
+};
+
+__device__ __forceinline__ RowFactor row_factor(float f, int room) {
+    const int h = min(max(room + 127 - (int)((__float_as_uint(f) >> 23) & 0xFF), 0), 15);
+    const float g = f * power_of_2(h), down = power_of_2(-h);
+    const float rounded = __half2float(__float2half_rn(g));
+    return RowFactor{Fp16::pack(g, g - rounded), Fp16::pack(down, -1152.0f * down)};
 }
 
-// 16 held elements times a scale, rounded once to fp16.
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
+// 16 held elements times their row's factor, to fp16.
 template <class H>
-__device__ __forceinline__ void scaled16(const uint4& u, float scale, uint4& lo, uint4& hi) {
-    const float2 f = make_float2(scale, scale);
+__device__ __forceinline__ void scaled16(const uint4& u, const RowFactor& r, uint4& lo, uint4& hi) {
+    const __half2 g = as_half2(__byte_perm(r.gd, 0, 0x1010)), d = as_half2(__byte_perm(r.gd, 0, 0x3232));
+    const __half2 p = as_half2(__byte_perm(r.pc, 0, 0x1010)), c = as_half2(__byte_perm(r.pc, 0, 0x3232));
+    auto two = [&](uint32_t v) {
+        const __half2 q = H::kFormat == W4A16_CACHE_INT8 ? __hfma2(as_half2(v), p, c) : __hmul2(as_half2(v), p);
+        return as_u32(__hfma2(q, g, __hmul2(q, d)));
+    };
     auto four = [&](uint32_t v, uint32_t& a, uint32_t& b) {
-        float2 x, y;
-        if constexpr (H::kFormat == W4A16_CACHE_INT8) {
-            // a byte with its sign bit flipped, q + 128, under fp32's 2^15: 2^15 + 128 + q, exactly
-            v ^= 0x80808080u;
-            const float2 off = make_float2(-32896.0f, -32896.0f);
-            x = make_float2(__uint_as_float(__byte_perm(v, 0x47000000u, 0x7404)),
-                            __uint_as_float(__byte_perm(v, 0x47000000u, 0x7414)));
-            y = make_float2(__uint_as_float(__byte_perm(v, 0x47000000u, 0x7424)),
-                            __uint_as_float(__byte_perm(v, 0x47000000u, 0x7434)));
-            x = add2(x, off);
-            y = add2(y, off);
-        } else {
-            uint32_t p, q;
-            H::to_fp16(v, p, q);
-            x = Fp16::unpack(p);
-            y = Fp16::unpack(q);
-        }
-        x = mul2(x, f);
-        y = mul2(y, f);
-        a = Fp16::pack(x.x, x.y);
-        b = Fp16::pack(y.x, y.y);
+        if constexpr (H::kFormat == W4A16_CACHE_INT8) H::to_fp16_plus_1152(v, a, b);
+        else H::to_fp16(v, a, b);
+        a = two(a);
+        b = two(b);
     };
     four(u.x, lo.x, lo.y);
     four(u.y, lo.z, lo.w);
@@ -525,7 +535,7 @@ template <class E, class H, int D, bool PAIRED>
 __global__ void __launch_bounds__(threads_of<H>(), 1)
     tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                 const __grid_constant__ TileArgs x) {
-    using L = Layout<D>;
+    using L = Layout<H, D>;
     constexpr bool kHeld8 = H::kFormat != 0;
     using M = std::conditional_t<kHeld8, Fp16, E>;  // of the products
     extern __shared__ unsigned char smem_raw[];
@@ -585,9 +595,9 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem;
     if constexpr (kHeld8) {
-        // of the launch's 512 x 128 registers: 256 x 168 and 256 x 88
-        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // of the launch's 512 x 128 registers: 256 x 136 and 256 x 120
+        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     }
     volatile int* abort = &bars->abort;
     const bool idle = !ok;
@@ -645,122 +655,131 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
         if (!ok && lane == 0) fail(x, bars);
     } else if (kHeld8 && warp >= kConvert) {
         // -------------------------------------------------------- conversion
-        // Each warp brings 32 places of every block to fp16, k and then v, from registers that were loaded
-        // half a block before. A place that is not read is zeros.
+        // Each warp brings 32 places of every block to fp16, k and then v, by way of a ring of its own that
+        // is loaded ahead (each lane reads back what it loaded), past the ends of entries too. A place
+        // that is not read is zeros.
         if constexpr (kHeld8) {
             constexpr int kPieces = D / 16, kRowsPer = 32 / kPieces, kLoads = 32 / kRowsPer;
             const int mine = (warp - kConvert) * 32;  // first place of the block
             // neighbouring rows in 8 lanes: their 16-byte stores fall into eight bank groups
             const int piece = kPieces == 8 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
             const int row0 = kPieces == 8 ? ((lane >> 2) & 1) + (lane >> 4) * 2 : lane >> 2;
-            int n = 0;  // of the ring
-            uint4 raw[kLoads];
-            for (int k = 0; entry(k); ++k) {
-                const Entry& e = bars->work[k % kEntries];
-                const int to = e.to, length = e.length, low = e.low, b = e.b, g = e.g, from = e.from;
-                const int ordinal = e.ordinal;
-                const bool last = e.last;
-                // the pages of 32 runs of 16 places (4 blocks), a lane each
-                int pages = 0, pages_from = -1;
-                auto page_at = [&](int run) { return __shfl_sync(0xffffffffu, pages, run - pages_from * 8); };
-                auto load_pages = [&](int j) {
-                    if (pages_from >= 0 && j < pages_from + 4) return;
-                    pages_from = j;
-                    const int p = (j * 8 + lane) * 16;
-                    pages = -1;
-                    if (p < length && p + 16 > low && p < to * kBlock) pages = (int)page_of(a.c, b, p);
-                };
-                auto load = [&](int j, const uint16_t* base) {
+            unsigned char* raw = smem + L::kRawAt + (warp - kConvert) * L::kRaw * L::kRawBytes;
+            const int64_t halves = 2 * (run.end - run.begin);  // k and v blocks
+            // where the loads are: a block of an entry, and the pages of its two runs of 16 places and those of the
+            // 15 blocks after it, a lane each
+            int k = -1, j = 0, to = 0, length = 0, low = 0, b = 0, g = 0, pages = -1, pages_from = 0;
+            auto advance = [&] {
+                if (++j >= to) {
+                    if (k >= 0) done_with(k);
+                    if (!entry(++k)) return;
+                    const Entry& e = bars->work[k % kEntries];
+                    j = e.from;
+                    to = e.to;
+                    length = e.length;
+                    low = e.low;
+                    b = e.b;
+                    g = e.g;
+                } else if (j < pages_from + 16) {
+                    return;
+                }
+                pages_from = j;
+                const int p = (j + (lane >> 1)) * kBlock + mine + (lane & 1) * 16;
+                pages = -1;
+                if (j + (lane >> 1) < to && p < length && p + 16 > low) pages = (int)page_of(a.c, b, p);
+            };
+            auto issue = [&](int64_t h) {
+                if (h < halves) {
+                    const bool values = h & 1;
+                    if (!values) advance();
+                    if (!ok) return;
+                    const uint32_t dst = ptx::smem_u32(raw + (int)(h % L::kRaw) * L::kRawBytes);
+                    const uint8_t* base = reinterpret_cast<const uint8_t*>(values ? a.c.v : a.c.k);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int p0 = j * kBlock + mine + half * 16;
-                        const int page = page_at(p0 >> 4);
-                        const uint8_t* src = reinterpret_cast<const uint8_t*>(base) + (int64_t)page * a.c.page_stride +
-                                             (int64_t)a.c.by_page.remainder(p0) * a.c.slot_stride +
+                        const int page = __shfl_sync(0xffffffffu, pages, (j - pages_from) * 2 + half);
+                        const int first = page >= 0 ? low - p0 : 16, end = length - p0;
+                        const uint8_t* src = base + (int64_t)page * a.c.page_stride +
+                                             (int64_t)(a.c.by_page.remainder(p0) + row0) * a.c.slot_stride +
                                              (int64_t)g * a.c.head_stride + piece * 16;
 #pragma unroll
                         for (int i = 0; i < kLoads / 2; ++i) {
                             const int row = i * kRowsPer + row0;
-                            raw[half * (kLoads / 2) + i] = make_uint4(0, 0, 0, 0);
-                            if (page >= 0 && p0 + row >= low && p0 + row < length)
-                                raw[half * (kLoads / 2) + i] =
-                                    __ldg(reinterpret_cast<const uint4*>(src + row * a.c.slot_stride));
+                            const bool real = row >= first && row < end;
+                            ptx::cp_async_16(dst + ((half * (kLoads / 2) + i) * 32 + lane) * 16, real ? src : base,
+                                             real ? 16u : 0u);
+                            src += kRowsPer * a.c.slot_stride;
                         }
                     }
-                };
-                // The scale of this warp's place `lane`, and the largest of the block (not NaN).
-                auto load_scales = [&](int j, const float* base, float& own) {
-                    float top = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < kBlock / 32; ++c) {
-                        const int p = j * kBlock + c * 32 + lane;
-                        const int page = page_at(p >> 4);
-                        float v = 0.0f;
-                        if (page >= 0 && p >= low && p < length)
-                            v = __ldg(base + (int64_t)page * x.s.page_stride + (int64_t)g * x.s.head_stride +
-                                      a.c.by_page.remainder(p));
-                        if (c == warp - kConvert) own = v;
-                        top = fmaxf(top, v);
-                    }
-                    return top;
-                };
-                // The power of two that takes the block's largest element to fp16's last ones, 2^15 to 2^16, held to
-                // what leaves room on either side: what is 2^21 times smaller than that is still exact to fp16.
-                auto factor = [&](float top) {
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    return min(max((int)(__float_as_uint(top) >> 23) - 127, -60), 60) - H::kRoom;
-                };
-                auto convert = [&](float own, int f, int st) {
-                    const float down = power_of_2(-f);
-                    unsigned char* dst = ring + st * L::kStageBytes + (piece >> 2) * L::kSlabBytes;
-#pragma unroll
-                    for (int i = 0; i < kLoads; ++i) {
-                        const int row = mine + i * kRowsPer + row0;
-                        const float scale = __shfl_sync(0xffffffffu, own, row & 31) * down;
-                        uint4 lo, hi;
-                        scaled16<H>(raw[i], scale, lo, hi);
-                        unsigned char* at = dst + row * 128;
-                        const int chunk = (piece & 3) * 2;
-                        *reinterpret_cast<uint4*>(at + ((chunk ^ (row & 7)) << 4)) = lo;
-                        *reinterpret_cast<uint4*>(at + (((chunk + 1) ^ (row & 7)) << 4)) = hi;
-                    }
-                    ptx::fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bars->full[st]);
-                };
-                auto wait_empty = [&] {
-                    const int st = n % L::kStages, round = n / L::kStages;
-                    if (round > 0 && !wait_bar(&bars->empty[st], (round - 1) & 1, abort, wait_limit())) ok = false;
-                    ok = ok && may_issue(n);
-                    ok = __all_sync(0xffffffffu, ok);
-                    ++n;
-                    return st;
-                };
-                load_pages(from);
-                load(from, a.c.k);
-                for (int j = from; j < to; ++j) {
-                    float ks, vs;
-                    const float kt = load_scales(j, x.s.k, ks), vt = load_scales(j, x.s.v, vs);
-                    const int fk = factor(kt), fv = factor(vt);
-                    int st = wait_empty();
-                    if (!ok) break;
-                    if (warp == kConvert && lane == 0)
-                        bars->factors[(ordinal + j - from) % kFactors] = pack_factors(fk, fv);
-                    convert(ks, fk, st);
-                    load(j, a.c.v);
-                    st = wait_empty();
-                    if (!ok) break;
-                    convert(vs, fv, st);
-                    if (j + 1 < to) {
-                        load_pages(j + 1);
-                        load(j + 1, a.c.k);
+                    if (!values) {
+                        const int p = j * kBlock + mine + lane;
+                        const int page = __shfl_sync(0xffffffffu, pages, (j - pages_from) * 2 + (lane >> 4));
+                        const bool real = page >= 0 && p >= low && p < length;
+                        const int64_t at = real ? (int64_t)page * x.s.page_stride + (int64_t)g * x.s.head_stride +
+                                                      a.c.by_page.remainder(p)
+                                                : 0;
+                        cp_async_4(dst + 32 * D + lane * 4, x.s.k + at, real ? 4u : 0u);
+                        cp_async_4(dst + 32 * D + 128 + lane * 4, x.s.v + at, real ? 4u : 0u);
                     }
                 }
-                done_with(k);
-                if (!ok || last) break;
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            // The power of two that takes the largest of 32 rows' elements to fp16's last ones, 2^15 to 2^16, held to
+            // what leaves room on either side: what is 2^21 times smaller than that is still exact to fp16.
+            auto factor = [&](float scale) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(scale, 0.0f)));  // not NaN
+                return min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
+            };
+            float scale_v = 0.0f;
+            int factor_v = 0;
+#pragma unroll 1
+            for (int64_t h = 0; ok && h < L::kRaw - 1; ++h) issue(h);
+#pragma unroll 1
+            for (int64_t h = 0; ok && h < halves; ++h) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(L::kRaw - 2) : "memory");
+                issue(h + L::kRaw - 1);
+                const int st = (int)(h % L::kStages);
+                const int64_t round = h / L::kStages;
+                if (round > 0 && !wait_bar(&bars->empty[st], (uint32_t)(round - 1) & 1, abort, wait_limit())) ok = false;
+                ok = ok && may_issue((int)h);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const unsigned char* src = raw + (int)(h % L::kRaw) * L::kRawBytes;
+                float scale = scale_v;
+                int f = factor_v;
+                if (!(h & 1)) {
+                    scale = reinterpret_cast<const float*>(src + 32 * D)[lane];
+                    scale_v = reinterpret_cast<const float*>(src + 32 * D + 128)[lane];
+                    f = factor(scale);
+                    factor_v = factor(scale_v);
+                    if (lane == 0)
+                        reinterpret_cast<int*>(&bars->factors[(h >> 1) % kFactors])[warp - kConvert] =
+                            pack_factors(f, factor_v);
+                }
+                const RowFactor rf = row_factor(scale * power_of_2(-f), H::kRoom);
+                unsigned char* dst = ring + st * L::kStageBytes + (piece >> 2) * L::kSlabBytes;
+                uint4 held[kLoads];  // all before the first store, which might be to the same place for all the compiler knows
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) held[i] = *reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16);
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int row = i * kRowsPer + row0;
+                    const RowFactor r{__shfl_sync(0xffffffffu, rf.gd, row), __shfl_sync(0xffffffffu, rf.pc, row)};
+                    uint4 lo, hi;
+                    scaled16<H>(held[i], r, lo, hi);
+                    unsigned char* at = dst + (mine + row) * 128;
+                    const int chunk = (piece & 3) * 2;
+                    *reinterpret_cast<uint4*>(at + ((chunk ^ (row & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(at + (((chunk + 1) ^ (row & 7)) << 4)) = hi;
+                }
+                ptx::fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bars->full[st]);
             }
+            if (ok) done_with(k);
             if (!ok && lane == 0) fail(x, bars);
+            ptx::cp_async_wait_all();
             __syncwarp();
         }
     } else if (kHeld8 && (warp == kLoadK || warp == kLoadV)) {
@@ -1236,24 +1255,22 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     }
                     ptx::tmem_st_wait();
                 }
-                // An 8-bit cache's keys and values are divided by powers of two, their blocks' factors: those
+                // An 8-bit cache's keys and values are divided by powers of two, the factors of 32 places: those
                 // of the keys multiply the scores, and the maximum and the weights are those of 2^s times the
                 // values' factor, which the sum is divided by again.
-                float score_scale = a.scale_log2, value_log2 = 0.0f, value_down = 1.0f;
-                if constexpr (kHeld8) {
-                    const int f = *(volatile int*)&bars->factors[(e.ordinal + j - e.from) % kFactors];
-                    score_scale = row_scale * power_of_2(key_factor(f));
-                    value_log2 = (float)value_factor(f);
-                    value_down = power_of_2(-value_factor(f));
-                }
+                int4 factors = make_int4(0, 0, 0, 0);
+                if constexpr (kHeld8) factors = bars->factors[(e.ordinal + j - e.from) % kFactors];
+                float top;
                 uint32_t s0[32], s1[32];
-                float t[4];
                 ptx::tmem_ld_32x32b_x32(s_addr, s0);
                 ptx::tmem_ld_32x32b_x32(s_addr + 32, s1);
                 tmem_ld_wait(s0);
                 tmem_ld_wait(s1);
+                float t[4];
+                auto start = [&](const uint32_t (&s)[32]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s0[i]);
+                    for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[i]);
+                };
                 auto largest = [&](const uint32_t (&s)[32]) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
@@ -1261,17 +1278,34 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         for (int u = 0; u < 4; ++u)
                             t[u] = max3(t[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
                 };
+                auto top_of = [&](int f) {  // of 32 columns with their own factors
+                    return fmaf(fmaxf(max3(t[0], t[1], t[2]), t[3]), row_scale * power_of_2(key_factor(f)),
+                                (float)value_factor(f));
+                };
+                start(s0);
                 largest(s0);
                 ptx::tmem_ld_32x32b_x32(s_addr + 64, s0);
+                if constexpr (kHeld8) {
+                    top = top_of(factors.x);
+                    start(s1);
+                }
                 largest(s1);
                 ptx::tmem_ld_32x32b_x32(s_addr + 96, s1);
                 tmem_ld_wait(s0);
                 tmem_ld_wait(s1);
+                if constexpr (kHeld8) {
+                    top = fmaxf(top, top_of(factors.y));
+                    start(s0);
+                }
                 largest(s0);
                 ptx::tmem_ld_32x32b_x32(s_addr, s0);
+                if constexpr (kHeld8) {
+                    top = fmaxf(top, top_of(factors.z));
+                    start(s1);
+                }
                 largest(s1);
-                float top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * score_scale;
-                if constexpr (kHeld8) top += value_log2;
+                if constexpr (kHeld8) top = fmaxf(top, top_of(factors.w));
+                else top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * a.scale_log2;
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {
                     top = fmaxf(top, m);
                     const float keep = m == -INFINITY ? 0.0f : fast_exp2(m - top);
@@ -1291,10 +1325,15 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         ptx::tmem_st_wait();
                     }
                 }
-                const float base = m == -INFINITY ? 0.0f : kHeld8 ? value_log2 - m : -m;
-                const float2 c2 = make_float2(score_scale, score_scale), m2 = make_float2(base, base);
-                float2 part = kHeld8 ? make_float2(0.0f, 0.0f) : sum;
-                auto weights = [&](int c, uint32_t (&s)[32]) {
+                const float base = m == -INFINITY ? 0.0f : -m;
+                auto weights = [&](int c, uint32_t (&s)[32], int f) {
+                    float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(base, base), part = sum;
+                    if constexpr (kHeld8) {
+                        const float by = row_scale * power_of_2(key_factor(f)), from = base + (float)value_factor(f);
+                        c2 = make_float2(by, by);
+                        m2 = make_float2(from, from);
+                        part = make_float2(0.0f, 0.0f);
+                    }
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -1305,23 +1344,27 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         p[i] = M::pack(v.x, v.y);
                     }
                     ptx::tmem_st_32x32b_x16(s_addr + (c >> 1), p);
+                    if constexpr (kHeld8) {
+                        const float down = power_of_2(-value_factor(f));
+                        sum = fma2(part, make_float2(down, down), sum);
+                    } else {
+                        sum = part;
+                    }
                 };
 #pragma unroll 1
                 for (int c = 0; c < kBlock; c += 64) {
                     tmem_ld_wait(s0);
                     ptx::tmem_ld_32x32b_x32(s_addr + c + 32, s1);
-                    weights(c, s0);
+                    weights(c, s0, c == 0 ? factors.x : factors.z);
                     tmem_ld_wait(s1);
                     ptx::tmem_ld_32x32b_x32(s_addr + 64, s0);  // (the last time for nothing)
-                    weights(c + 32, s1);
+                    weights(c + 32, s1, c == 0 ? factors.y : factors.w);
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(c == 0 ? &bars->p_part[w] : &bars->p_full[w]);
                 }
                 tmem_ld_wait(s0);
-                if constexpr (kHeld8) sum = fma2(part, make_float2(value_down, value_down), sum);
-                else sum = part;
             }
             if (!ok) break;
             if (begin >= end && !last) {
@@ -1480,7 +1523,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
 template <class E, class H, int D, bool PAIRED>
 w4a16_status launch_with_maps(const DeviceInfo& dev, const CUtensorMap& mk, const CUtensorMap& mv, const TileArgs& x,
                               cudaStream_t st) {
-    using L = Layout<D>;
+    using L = Layout<H, D>;
     static_assert(L::kStages <= kMaxStages, "ring");
     static_assert(L::kStages / 2 + 3 < kFactors, "the converters' lead");
     static PerDeviceOnce once;

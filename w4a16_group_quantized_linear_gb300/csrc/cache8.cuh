@@ -47,10 +47,15 @@ struct HeldInt8 {
                                   __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
         return *reinterpret_cast<const uint32_t*>(&h);
     }
-    __device__ static __forceinline__ void to_fp16(uint32_t v, uint32_t& b01, uint32_t& b23) {
+    __device__ static __forceinline__ void to_fp16_plus_1152(uint32_t v, uint32_t& b01, uint32_t& b23) {
         v ^= 0x80808080u;
-        b01 = minus_1152(__byte_perm(v, 0x64646464u, 0x4140));
-        b23 = minus_1152(__byte_perm(v, 0x64646464u, 0x4342));
+        b01 = __byte_perm(v, 0x64646464u, 0x4140);
+        b23 = __byte_perm(v, 0x64646464u, 0x4342);
+    }
+    __device__ static __forceinline__ void to_fp16(uint32_t v, uint32_t& b01, uint32_t& b23) {
+        to_fp16_plus_1152(v, b01, b23);
+        b01 = minus_1152(b01);
+        b23 = minus_1152(b23);
     }
     __device__ static __forceinline__ void to_fp16_apart(uint32_t v, uint32_t& b02, uint32_t& b13) {
         v ^= 0x80808080u;
