@@ -1,30 +1,14 @@
 // Attention for many rows over an 8-bit cache: the kernel is attention_tile.cuh's.
-#include <cuda.h>
-
 #include "attention_tile.cuh"
 
 namespace w4a16 {
-namespace {
-
-template <class E, class H, int D>
-w4a16_status launch_rows(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
-    const CUtensorMap none{};
-    return x.a.max_q_len * x.a.ratio <= kHalf ? launch_with_maps<E, H, D, true>(dev, none, none, x, st)
-                                              : launch_with_maps<E, H, D, false>(dev, none, none, x, st);
-}
-
-template <class E, class H>
-w4a16_status launch_dim(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
-    return x.a.c.head_dim == 128 ? launch_rows<E, H, 128>(dev, x, st) : launch_rows<E, H, 64>(dev, x, st);
-}
-
-}  // namespace
 
 w4a16_status attention8_tile_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
                                     const ScaleArgs& s, int min_rows, void* workspace, cudaStream_t st) {
     const TileArgs x = tile_args(dev, a, s, min_rows, workspace);
     const bool f16 = dtype == W4A16_DTYPE_F16;
-    if (format == W4A16_CACHE_INT8) return f16 ? launch_dim<Fp16, HeldInt8>(dev, x, st) : launch_dim<Bf16, HeldInt8>(dev, x, st);
+    if (format == W4A16_CACHE_INT8)
+        return f16 ? launch_dim<Fp16, HeldInt8>(dev, x, st) : launch_dim<Bf16, HeldInt8>(dev, x, st);
     return f16 ? launch_dim<Fp16, HeldE4m3>(dev, x, st) : launch_dim<Bf16, HeldE4m3>(dev, x, st);
 }
 

@@ -53,6 +53,9 @@
 // W4A16_ERR_TIMEOUT and the thread block unwinds (its copies and MMAs finish, TMEM is freed).
 #pragma once
 
+#include <cudaTypedefs.h>
+
+#include <mutex>
 #include <type_traits>
 
 #include "cache8.cuh"
@@ -64,9 +67,9 @@ constexpr int kHalf = 128;       // rows of a half tile: MMA M, TMEM lanes
 constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;      // places per block: MMA N of the scores, K of the output
 constexpr int kLoadK = 8, kMmaWarp = 9, kPlanWarp = 10, kLoadV = 11;
-constexpr int kConvert = 12, kConverters = 4;  // warps of an 8-bit cache in place of the loads
-constexpr int kBarBytes = 2048;  // struct Bars
-constexpr int kFactors = 16;     // blocks whose factors are kept: more than the converters can be ahead
+constexpr int kConvert = 12, kConverters = 4;  // warps that bring an 8-bit cache's blocks to fp16
+constexpr int kBarBytes = 1792, kBar8Bytes = 512;  // struct Bars, struct Bars8
+constexpr int kFactors = 16;     // blocks whose factors are kept: more than the converters can be ahead of the softmax
 constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 // How far (log2) a score may pass the running maximum of a whole tile before the maximum moves. A
 // weight reaches 2^14, inside fp16's 2^16, and o, not divided by l yet, that many times the values'
@@ -99,21 +102,19 @@ struct Layout {
     static constexpr int kSlabs = D / 64;              // 64-element slabs: 128-byte swizzled rows
     static constexpr int kSlabBytes = kBlock * 128;
     static constexpr int kStageBytes = kSlabs * kSlabBytes;  // one k or v block; also half a tile's queries
-    // An 8-bit cache's rows wait in rings of the converting warps, kRaw entries of 32 rows and the scales of
-    // both k and v. Of what is loaded ahead, no more than two blocks may be past the one that is
-    // converted: the plan lays out the entries of such blocks while the tiles before them are still in work.
+    // An 8-bit cache's blocks land in a ring of their own, as they are held, with the scales of their places (the
+    // k block's both its own and the v block's).
     static constexpr bool kHeld8 = H::kFormat != 0;
-    static constexpr int kRaw = !kHeld8 ? 0 : D == 128 ? 3 : 5;
-    static_assert(kRaw <= 5, "two blocks ahead");
-    static constexpr int kRawBytes = 32 * D + 256;
+    static constexpr int kRaw = !kHeld8 ? 0 : D == 128 ? 3 : 6;
+    static constexpr int kRawBlock = kBlock * D, kRawBytes = kRawBlock + 2 * kBlock * 4;
     static constexpr int kStages = !kHeld8 ? (224 * 1024 - 2 * kStageBytes) / kStageBytes : D == 128 ? 3 : 7;
     static constexpr int kRingAt = 2 * kStageBytes;
     static constexpr int kRawAt = kRingAt + kStages * kStageBytes;
-    static constexpr int kBarsAt = kRawAt + kConverters * kRaw * kRawBytes;
-    static constexpr int kSmem = kBarsAt + kBarBytes + 1024;  // barriers, and the 1024-byte alignment
+    static constexpr int kBarsAt = kRawAt + kRaw * kRawBytes;
+    static constexpr int kSmem = kBarsAt + kBarBytes + (kHeld8 ? kBar8Bytes : 0) + 1024;  // barriers, and the 1024-byte alignment
 };
 
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 12, kMaxRaw = 6;
 
 // A tile, or a stretch of its blocks, for the warps to work on.
 struct Entry {
@@ -143,13 +144,20 @@ struct Bars {
     uint64_t work_full[kEntries], work_empty[kEntries];
     uint64_t mma_done;
     Entry work[kEntries];
-    int4 factors[kFactors];  // of an 8-bit cache's blocks, by their place in the run
     float2 pair_stats[kHalf];
     uint32_t tmem;
     int abort;
     int last[2];
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers");
+
+// And those of an 8-bit cache.
+struct Bars8 {
+    int4 factors[kFactors];  // of blocks, by their place in the run
+    uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+    int2 span[kMaxRaw];      // places from a block's first to the first that is seen, and past the last
+};
+static_assert(sizeof(Bars8) <= kBar8Bytes, "barriers");
 
 struct TileArgs {
     AttentionArgs a;
@@ -300,10 +308,6 @@ template <class E>
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major) {
     const uint32_t type = E::kDtype == W4A16_DTYPE_BF16 ? 1u : 0u;
     return ptx::idesc_f16_f32(kHalf, n) | (type << 7) | (type << 10) | ((b_n_major ? 1u : 0u) << 16);
-}
-
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_size) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_size) : "memory");
 }
 
 // A lane's piece of a bf16 row that PIECES lanes hold, in fp16, divided by the power of two of the row's
@@ -542,6 +546,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
     unsigned char* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = smem + L::kRingAt;
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kBarsAt);
+    Bars8* bars8 = reinterpret_cast<Bars8*>(smem + L::kBarsAt + kBarBytes);  // (of an 8-bit cache)
     const AttentionArgs& a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ratio = a.ratio;
@@ -552,6 +557,10 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
             for (int i = 0; i < L::kStages; ++i) {
                 ptx::mbar_init(&bars->full[i], kHeld8 ? kConverters : 1);
                 ptx::mbar_init(&bars->empty[i], 1);
+            }
+            for (int i = 0; i < L::kRaw; ++i) {
+                ptx::mbar_init(&bars8->raw_full[i], 1 + 32);  // the issuing lane, and each lane's scales
+                ptx::mbar_init(&bars8->raw_empty[i], kConverters);
             }
             for (int w = 0; w < 2; ++w) {
                 ptx::mbar_init(&bars->q_full[w], kHalf);
@@ -564,8 +573,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
             }
             for (int i = 0; i < kEntries; ++i) {
                 ptx::mbar_init(&bars->work_full[i], 1);
-                // loads, MMAs (of each half), softmax warps
-                ptx::mbar_init(&bars->work_empty[i], (kHeld8 ? kConverters : 2) + (PAIRED ? 2 : 1) + 8);
+                ptx::mbar_init(&bars->work_empty[i], PAIRED ? 12 : 11);  // loads, MMAs (of each half), softmax warps
             }
             ptx::mbar_init(&bars->landed, 1);
             ptx::mbar_init(&bars->pair_in, kHalf);
@@ -573,10 +581,8 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
             ptx::mbar_init(&bars->mma_done, 1);
             bars->abort = 0;
             ptx::fence_mbar_init();
-            if constexpr (!kHeld8) {
-                ptx::prefetch_tensormap(&map_k);
-                ptx::prefetch_tensormap(&map_v);
-            }
+            ptx::prefetch_tensormap(&map_k);
+            ptx::prefetch_tensormap(&map_v);
         }
         __syncwarp();
         ptx::tmem_alloc(&bars->tmem, kTmemCols);
@@ -655,113 +661,65 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
         if (!ok && lane == 0) fail(x, bars);
     } else if (kHeld8 && warp >= kConvert) {
         // -------------------------------------------------------- conversion
-        // Each warp brings 32 places of every block to fp16, k and then v, by way of a ring of its own that
-        // is loaded ahead (each lane reads back what it loaded), past the ends of entries too. A place
-        // that is not read is zeros.
+        // Each warp brings 32 places of every block to fp16, k and then v, as soon as there is room.
+        // A place that is not seen becomes zeros.
         if constexpr (kHeld8) {
             constexpr int kPieces = D / 16, kRowsPer = 32 / kPieces, kLoads = 32 / kRowsPer;
             const int mine = (warp - kConvert) * 32;  // first place of the block
-            // neighbouring rows in 8 lanes: their 16-byte stores fall into eight bank groups
-            const int piece = kPieces == 8 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
-            const int row0 = kPieces == 8 ? ((lane >> 2) & 1) + (lane >> 4) * 2 : lane >> 2;
-            unsigned char* raw = smem + L::kRawAt + (warp - kConvert) * L::kRaw * L::kRawBytes;
+            // 8 lanes take the pieces of neighbouring rows whose 16 bytes are in eight bank groups, both as they are
+            // read and as the halves of their fp16 are written
+            const int piece = lane & (kPieces - 1);
+            const int row0 = kPieces == 8 ? (((lane >> 2) ^ (lane >> 3)) & 1) + (lane >> 4) * 2 : lane >> 2;
             const int64_t halves = 2 * (run.end - run.begin);  // k and v blocks
-            // where the loads are: a block of an entry, and the pages of its two runs of 16 places and those of the
-            // 15 blocks after it, a lane each
-            int k = -1, j = 0, to = 0, length = 0, low = 0, b = 0, g = 0, pages = -1, pages_from = 0;
-            auto advance = [&] {
-                if (++j >= to) {
-                    if (k >= 0) done_with(k);
-                    if (!entry(++k)) return;
-                    const Entry& e = bars->work[k % kEntries];
-                    j = e.from;
-                    to = e.to;
-                    length = e.length;
-                    low = e.low;
-                    b = e.b;
-                    g = e.g;
-                } else if (j < pages_from + 16) {
-                    return;
-                }
-                pages_from = j;
-                const int p = (j + (lane >> 1)) * kBlock + mine + (lane & 1) * 16;
-                pages = -1;
-                if (j + (lane >> 1) < to && p < length && p + 16 > low) pages = (int)page_of(a.c, b, p);
-            };
-            auto issue = [&](int64_t h) {
-                if (h < halves) {
-                    const bool values = h & 1;
-                    if (!values) advance();
-                    if (!ok) return;
-                    const uint32_t dst = ptx::smem_u32(raw + (int)(h % L::kRaw) * L::kRawBytes);
-                    const uint8_t* base = reinterpret_cast<const uint8_t*>(values ? a.c.v : a.c.k);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int p0 = j * kBlock + mine + half * 16;
-                        const int page = __shfl_sync(0xffffffffu, pages, (j - pages_from) * 2 + half);
-                        const int first = page >= 0 ? low - p0 : 16, end = length - p0;
-                        const uint8_t* src = base + (int64_t)page * a.c.page_stride +
-                                             (int64_t)(a.c.by_page.remainder(p0) + row0) * a.c.slot_stride +
-                                             (int64_t)g * a.c.head_stride + piece * 16;
-#pragma unroll
-                        for (int i = 0; i < kLoads / 2; ++i) {
-                            const int row = i * kRowsPer + row0;
-                            const bool real = row >= first && row < end;
-                            ptx::cp_async_16(dst + ((half * (kLoads / 2) + i) * 32 + lane) * 16, real ? src : base,
-                                             real ? 16u : 0u);
-                            src += kRowsPer * a.c.slot_stride;
-                        }
-                    }
-                    if (!values) {
-                        const int p = j * kBlock + mine + lane;
-                        const int page = __shfl_sync(0xffffffffu, pages, (j - pages_from) * 2 + (lane >> 4));
-                        const bool real = page >= 0 && p >= low && p < length;
-                        const int64_t at = real ? (int64_t)page * x.s.page_stride + (int64_t)g * x.s.head_stride +
-                                                      a.c.by_page.remainder(p)
-                                                : 0;
-                        cp_async_4(dst + 32 * D + lane * 4, x.s.k + at, real ? 4u : 0u);
-                        cp_async_4(dst + 32 * D + 128 + lane * 4, x.s.v + at, real ? 4u : 0u);
-                    }
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            };
             // The power of two that takes the largest of 32 rows' elements to fp16's last ones, 2^15 to 2^16, held to
             // what leaves room on either side: what is 2^21 times smaller than that is still exact to fp16.
             auto factor = [&](float scale) {
                 const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(scale, 0.0f)));  // not NaN
                 return min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
             };
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (!wait_bar(bar, parity & 1u, abort, wait_limit())) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                return ok;
+            };
             float scale_v = 0.0f;
             int factor_v = 0;
+            int st = 0, rst = 0;                // stages of the two rings
+            uint32_t parity = 1, rparity = 0;   // of the one's empty and the other's full barriers
 #pragma unroll 1
-            for (int64_t h = 0; ok && h < L::kRaw - 1; ++h) issue(h);
-#pragma unroll 1
-            for (int64_t h = 0; ok && h < halves; ++h) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(L::kRaw - 2) : "memory");
-                issue(h + L::kRaw - 1);
-                const int st = (int)(h % L::kStages);
-                const int64_t round = h / L::kStages;
-                if (round > 0 && !wait_bar(&bars->empty[st], (uint32_t)(round - 1) & 1, abort, wait_limit())) ok = false;
-                ok = ok && may_issue((int)h);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const unsigned char* src = raw + (int)(h % L::kRaw) * L::kRawBytes;
+            for (int64_t h = 0; h < halves; ++h) {
+                const unsigned char* src = smem + L::kRawAt + rst * L::kRawBytes;
+                if (!wait(&bars8->raw_full[rst], rparity)) break;
+                const int2 span = bars8->span[rst];
                 float scale = scale_v;
                 int f = factor_v;
                 if (!(h & 1)) {
-                    scale = reinterpret_cast<const float*>(src + 32 * D)[lane];
-                    scale_v = reinterpret_cast<const float*>(src + 32 * D + 128)[lane];
+                    const bool seen = mine + lane >= span.x && mine + lane < span.y;
+                    const float* scales = reinterpret_cast<const float*>(src + L::kRawBlock);
+                    scale = seen ? scales[mine + lane] : 0.0f;
+                    scale_v = seen ? scales[kBlock + mine + lane] : 0.0f;
                     f = factor(scale);
                     factor_v = factor(scale_v);
-                    if (lane == 0)
-                        reinterpret_cast<int*>(&bars->factors[(h >> 1) % kFactors])[warp - kConvert] =
-                            pack_factors(f, factor_v);
                 }
-                const RowFactor rf = row_factor(scale * power_of_2(-f), H::kRoom);
-                unsigned char* dst = ring + st * L::kStageBytes + (piece >> 2) * L::kSlabBytes;
-                uint4 held[kLoads];  // all before the first store, which might be to the same place for all the compiler knows
+                uint4 held[kLoads];
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) held[i] = *reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16);
+                for (int i = 0; i < kLoads; ++i)
+                    held[i] = *reinterpret_cast<const uint4*>(src + (mine + i * kRowsPer + row0) * D + piece * 16);
+                if (span.x > mine || span.y < mine + 32) {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int row = mine + i * kRowsPer + row0;
+                        if (row < span.x || row >= span.y) held[i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bars8->raw_empty[rst]);
+                const RowFactor rf = row_factor(scale * power_of_2(-f), H::kRoom);
+                if (!wait(&bars->empty[st], parity)) break;  // (the first round's, before any: done)
+                if (!(h & 1) && lane == 0)
+                    reinterpret_cast<int*>(&bars8->factors[(h >> 1) % kFactors])[warp - kConvert] =
+                        pack_factors(f, factor_v);
+                unsigned char* dst = ring + st * L::kStageBytes + (piece >> 2) * L::kSlabBytes;
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
                     const int row = i * kRowsPer + row0;
@@ -776,21 +734,28 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 ptx::fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bars->full[st]);
+                if (++st == L::kStages) {
+                    st = 0;
+                    parity ^= 1u;
+                }
+                if (++rst == L::kRaw) {
+                    rst = 0;
+                    rparity ^= 1u;
+                }
             }
-            if (ok) done_with(k);
             if (!ok && lane == 0) fail(x, bars);
-            ptx::cp_async_wait_all();
             __syncwarp();
         }
-    } else if (kHeld8 && (warp == kLoadK || warp == kLoadV)) {
-        // no loads of 16-bit blocks
     } else if (warp == kLoadK || warp == kLoadV) {
         // ------------------------------------------------------------- loads
         // k blocks are the ring's even entries, v blocks the odd ones
+        // (of an 8-bit cache: of the blocks as they are held)
+        constexpr int kRing = kHeld8 ? L::kRaw : L::kStages, kSlabs = kHeld8 ? 1 : L::kSlabs;
+        uint64_t *full = kHeld8 ? bars8->raw_full : bars->full, *empty = kHeld8 ? bars8->raw_empty : bars->empty;
         const bool values = warp == kLoadV;
         const CUtensorMap* map = values ? &map_v : &map_k;
         const int pieces = kBlock / x.box;
-        const int piece = lane / L::kSlabs, slab = lane % L::kSlabs;
+        const int piece = lane / kSlabs, slab = lane % kSlabs;
         int n = 0, issued = -1;
         // The v block of a sequence's last place, or of a window's first, lands on a barrier
         // of its own; then its slots past the one and before the other are zeroed (0 times what
@@ -846,13 +811,38 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 // warp's too: a barrier's parity tells only its next phase from the one before.
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int st = n % L::kStages, round = n / L::kStages;
+                    const int st = n % kRing, round = n / kRing;
                     if (dirty >= 0 && __all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->landed, landed_parity)))
                         clean();
-                    if (round > 0 && !wait_clean(&bars->empty[st], (round - 1) & 1)) break;
+                    if (round > 0 && !wait_clean(&empty[st], (round - 1) & 1)) break;
                     if (kv != (values ? 1 : 0)) continue;
                     ok = may_issue(n);
                     if (!ok) break;
+                    if constexpr (kHeld8) {
+                        unsigned char* dst = smem + L::kRawAt + st * L::kRawBytes;
+                        if (!values) {  // both blocks' scales, of 4 places a lane
+                            const int p = j * kBlock + lane * 4;
+                            const int its = __shfl_sync(0xffffffffu, pages, j * pieces - group + lane * 4 / x.box);
+                            const bool any = its < a.c.pages && p + 4 > low && p < length;
+                            const int64_t at = any ? (int64_t)its * x.s.page_stride + (int64_t)g * x.s.head_stride +
+                                                         a.c.by_page.remainder(p)
+                                                   : 0;
+                            const uint32_t to_scales = ptx::smem_u32(dst + L::kRawBlock) + lane * 16;
+                            ptx::cp_async_16(to_scales, x.s.k + at, any ? 16u : 0u);
+                            ptx::cp_async_16(to_scales + kBlock * 4, x.s.v + at, any ? 16u : 0u);
+                        }
+                        if (lane == 0) {
+                            bars8->span[st] = make_int2(low - j * kBlock, length - j * kBlock);
+                            ptx::mbar_arrive_expect_tx(&full[st], L::kRawBlock);
+                        }
+                        ptx::cp_async_mbar_arrive_noinc(&full[st]);
+                        __syncwarp();
+                        if (piece < pieces)
+                            tma_load_4d(dst + piece * x.box * D, map, &full[st], 0,
+                                        a.c.by_page.remainder(j * kBlock + piece * x.box), g, page);
+                        issued = n;
+                        continue;
+                    }
                     const int rows = values ? tail_rows(length - j * kBlock, x.box) : 0;
                     const int heads = values ? head_rows(low - j * kBlock, x.box) : 0;
                     const bool unclean = rows + heads > 0;
@@ -884,9 +874,8 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
             fail(x, bars);
             volatile int never = 0;  // our own copies land before the thread block ends
             if (dirty >= 0) wait_bar(&bars->landed, landed_parity, &never, kDrainLimitNs);
-            for (int i = issued; i >= 0 && i > issued - L::kStages; i -= 2)
-                if (i != dirty)
-                    wait_bar(&bars->full[i % L::kStages], (i / L::kStages) & 1, &never, kDrainLimitNs);
+            for (int i = issued; i >= 0 && i > issued - kRing; i -= 2)
+                if (i != dirty) wait_bar(&full[i % kRing], (i / kRing) & 1, &never, kDrainLimitNs);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -1259,7 +1248,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 // of the keys multiply the scores, and the maximum and the weights are those of 2^s times the
                 // values' factor, which the sum is divided by again.
                 int4 factors = make_int4(0, 0, 0, 0);
-                if constexpr (kHeld8) factors = bars->factors[(e.ordinal + j - e.from) % kFactors];
+                if constexpr (kHeld8) factors = bars8->factors[(e.ordinal + j - e.from) % kFactors];
                 float top;
                 uint32_t s0[32], s1[32];
                 ptx::tmem_ld_32x32b_x32(s_addr, s0);
@@ -1520,9 +1509,46 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
 
 // ------------------------------------------------------------------- host --
 
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// [pages][heads][slots][elements] of k or v: boxes of `box` slots, of 64 16-bit elements (in rows of 128 swizzled
+// bytes) or of the whole of an 8-bit row
+template <class E, class H>
+w4a16_status make_map(const CacheArgs& c, const uint16_t* base, int box, CUtensorMap* map) {
+    constexpr bool kHeld8 = H::kFormat != 0;
+    constexpr cuuint64_t kSize = kHeld8 ? 1 : 2;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) return cuda_status(cudaErrorNotSupported, "paged_attention: cuTensorMapEncodeTiled entry point");
+    cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
+                          (cuuint64_t)c.pages};
+    cuuint64_t strides[3] = {(cuuint64_t)c.slot_stride * kSize, (cuuint64_t)c.head_stride * kSize,
+                             (cuuint64_t)c.page_stride * kSize};
+    cuuint32_t boxes[4] = {kHeld8 ? (cuuint32_t)c.head_dim : 64, (cuuint32_t)box, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = kHeld8                            ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : E::kDtype == W4A16_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (enc(map, type, 4, const_cast<uint16_t*>(base), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            kHeld8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cuda_status(cudaErrorInvalidValue, "paged_attention: cuTensorMapEncodeTiled");
+    return W4A16_OK;
+}
+
 template <class E, class H, int D, bool PAIRED>
-w4a16_status launch_with_maps(const DeviceInfo& dev, const CUtensorMap& mk, const CUtensorMap& mv, const TileArgs& x,
-                              cudaStream_t st) {
+w4a16_status launch(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
     using L = Layout<H, D>;
     static_assert(L::kStages <= kMaxStages, "ring");
     static_assert(L::kStages / 2 + 3 < kFactors, "the converters' lead");
@@ -1532,8 +1558,28 @@ w4a16_status launch_with_maps(const DeviceInfo& dev, const CUtensorMap& mk, cons
                                     L::kSmem);
     });
     if (e != cudaSuccess) return cuda_status(e, "paged_attention: cudaFuncSetAttribute");
+    CUtensorMap mk, mv;
+    w4a16_status s = make_map<E, H>(x.a.c, x.a.c.k, x.box, &mk);
+    if (s == W4A16_OK) s = make_map<E, H>(x.a.c, x.a.c.v, x.box, &mv);
+    if (s != W4A16_OK) return s;
     return launch_overlapped("paged_attention", tile_kernel<E, H, D, PAIRED>, dim3((unsigned)dev.sms),
                              threads_of<H>(), L::kSmem, st, mk, mv, x);
+}
+
+template <class E, class H, int D>
+w4a16_status launch_rows(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
+    // Sequences that all fit half a tile (drafts being verified, short chunks)
+    // share out their blocks between the halves: 5 tokens x 5 heads over 2000 to
+    // 9000 places, 16 sequences, 87 us against 103 with one half idle (and the
+    // maximum that lags). For tiles of both halves the issuing loop that
+    // knows of no pairs is the faster one (2048 tokens over 30048 places 807
+    // against 868 us when both were built with that maximum).
+    return x.a.max_q_len * x.a.ratio <= kHalf ? launch<E, H, D, true>(dev, x, st) : launch<E, H, D, false>(dev, x, st);
+}
+
+template <class E, class H>
+w4a16_status launch_dim(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
+    return x.a.c.head_dim == 128 ? launch_rows<E, H, 128>(dev, x, st) : launch_rows<E, H, 64>(dev, x, st);
 }
 
 // The arguments, with the workspace laid out.
