@@ -38,14 +38,13 @@ Bounds. With u the half-spacing of the element type (2^-11 fp16, 2^-8 bf16):
   a largest weight times scale: fp16's tiny (1 + max_j s_j sum_j |q_jd|), as the
   products run in fp16 whatever the type. bf16 queries go to fp16 divided by a power
   of two of the row's largest element m_q: exact above 2^-14 of it, else off by 2^-25
-  of it, a score by r = 2^-24 scale m_q max_j sum_d |k_jd|. Where keys and values are
-  brought to fp16 as q s first (whole tiles), divided by a power of two that takes the
-  largest of 128 places past 2^14, each is off by w = 2^-11 of itself, or by twice
-  2^-25 in fp16's own units (a product and a sum), of which 2^6 at least make the block's largest scale:
-  below 2^-30 of the sequence's largest scale s_k or s_v. So a score is off by r = w S + 2^-30 s_k scale sum_d |q_d|
-  more, a weight by twice that (it and the sum), a value by w and 2^-30 s_v:
-      |y - ref| <= ... + 2 (r + w) A + 2^-30 s_v,   |lse - ref| <= ... + r
-  and the weights' factor is the block's, so tiny takes 2 s_v sum_j |q_jd|.
+  of it, a score by r = 2^-24 scale m_q max_j sum_d |k_jd|, and a weight by twice that
+  (it and the sum). Where values are brought to fp16 as q s first (whole tiles), divided
+  by a power of two that takes the largest of 32 places past 2^14, each is off by w = 2^-11 of
+  itself, or by twice 2^-25 in fp16's own units (a product and a sum), of which 2^6
+  at least make the largest scale: below 2^-30 of the sequence's largest scale s_v:
+      |y - ref| <= u |ref| + (w + e + 2 r + w) A + 2^-30 s_v + ...,   |lse - ref| <= ... + r
+  and the weights' factor is that of 32 places, so tiny takes 2 s_v sum_j |q_jd|.
 """
 from __future__ import annotations
 
@@ -211,8 +210,7 @@ def attention8(q, k, v, k_scale, v_scale, page_table, q_offsets, kv_lens, **kw):
     causal, window = kw.get("causal", True), kw.get("window", 0)
     scale = D ** -0.5 if kw.get("scale") is None else kw["scale"]
     q = np.abs(np.asarray(q, np.float64))
-    parts.update(V=np.zeros((T, H, D)), all_V=np.zeros((T, H, D)), Q=np.zeros((T, H)), K=np.zeros((T, H)),
-                 s_v=np.zeros((T, H)))
+    parts.update(V=np.zeros((T, H, D)), all_V=np.zeros((T, H, D)), Q=np.zeros((T, H)), s_v=np.zeros((T, H)))
     for t, (b, p) in enumerate(zip(*places(q_offsets, kv_lens))):
         end = min(kv_lens[b], p + 1) if causal else kv_lens[b]
         at = range(max(0, p - window + 1) if window else 0, end)
@@ -226,29 +224,22 @@ def attention8(q, k, v, k_scale, v_scale, page_table, q_offsets, kv_lens, **kw):
             ks, vs = (np.asarray(s, np.float64) for s in (k_scale, v_scale))
             held = np.abs(np.asarray(v, np.float64)[pages, slots, g]).sum(0)
             keys = np.abs(np.asarray(k, np.float64)[pages, slots, g]).sum(1) * ks[pages, g, slots]
-            s_k = np.nanmax([ks[i, g, j] for i, j in live])
             s_v = np.nanmax([vs[i, g, j] for i, j in live])
             parts["V"][t, mine] = vs[pages, g, slots].max() * held
             parts["all_V"][t, mine] = 2 * s_v * held
             parts["Q"][t, mine] = 2.0 ** -24 * scale * q[t, mine].max(-1) * keys.max()
-            parts["K"][t, mine] = 2.0 ** -30 * s_k * scale * q[t, mine].sum(-1)
             parts["s_v"][t, mine] = s_v
     return out, lse, parts
 
 
-def _off8(parts, dtype, rounded):
-    """How far a score may be off beyond the sums in fp32."""
-    off = parts["Q"] if dtype == "bf16" else 0.0
-    return off + (UNIT["fp16"] * parts["S"] + parts["K"] if rounded else 0.0)
-
-
 def attention8_tolerance(out, parts, dtype, rounded=False):
-    """rounded: keys and values are brought to fp16 as q s first."""
+    """rounded: values are brought to fp16 as q s first."""
     u, w = UNIT[dtype], UNIT["fp16"]
-    e = (_slack(out.shape[2], parts) + 2 * _off8(parts, dtype, rounded) + (2 * w if rounded else 0.0))[..., None]
+    r = parts["Q"] if dtype == "bf16" else 0.0
+    e = (_slack(out.shape[2], parts) + 2 * r + (w if rounded else 0.0))[..., None]
     tol = u * np.abs(out) + (w + e) * parts["A"] + TINY["fp16"] * (1 + parts["all_V" if rounded else "V"])
     return tol + (2.0 ** -30 * parts["s_v"][..., None] if rounded else 0.0)
 
 
-def lse8_tolerance(lse, D, parts, dtype, rounded=False):
-    return lse_tolerance(lse, D, parts) + np.where(np.isfinite(lse), _off8(parts, dtype, rounded), 0.0)
+def lse8_tolerance(lse, D, parts, dtype):
+    return lse_tolerance(lse, D, parts) + np.where(np.isfinite(lse), parts["Q"] if dtype == "bf16" else 0.0, 0.0)

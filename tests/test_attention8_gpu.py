@@ -68,7 +68,7 @@ class Batch8(Batch):
             empty = np.isneginf(lse_ref)
             assert np.array_equal(np.isneginf(got), empty)
             d = np.abs(np.where(empty, 0, got) - np.where(empty, 0, lse_ref))
-            assert (d <= oa.lse8_tolerance(lse_ref, self.D, parts, self.dtype, tiles)).all(), d.max()
+            assert (d <= oa.lse8_tolerance(lse_ref, self.D, parts, self.dtype)).all(), d.max()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -68,8 +68,8 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;      // places per block: MMA N of the scores, K of the output
 constexpr int kLoadK = 8, kMmaWarp = 9, kPlanWarp = 10, kLoadV = 11;
 constexpr int kConvert = 12, kConverters = 4;  // warps that bring an 8-bit cache's blocks to fp16
-constexpr int kBarBytes = 1792, kBar8Bytes = 512;  // struct Bars, struct Bars8
-constexpr int kFactors = 16;     // blocks whose factors are kept: more than the converters can be ahead of the softmax
+constexpr int kBarBytes = 1792, kBar8Bytes = 4608;  // struct Bars, struct Bars8
+constexpr int kFactors = 8;      // blocks whose scales are kept: more than the converters can be ahead of the softmax
 constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 // How far (log2) a score may pass the running maximum of a whole tile before the maximum moves. A
 // weight reaches 2^14, inside fp16's 2^16, and o, not divided by l yet, that many times the values'
@@ -105,7 +105,7 @@ struct Layout {
     // An 8-bit cache's blocks land in a ring of their own, as they are held, with the scales of their places (the
     // k block's both its own and the v block's).
     static constexpr bool kHeld8 = H::kFormat != 0;
-    static constexpr int kRaw = !kHeld8 ? 0 : D == 128 ? 3 : 6;
+    static constexpr int kRaw = !kHeld8 ? 0 : D == 128 ? 3 : 6;  // (the rest is for scales)
     static constexpr int kRawBlock = kBlock * D, kRawBytes = kRawBlock + 2 * kBlock * 4;
     static constexpr int kStages = !kHeld8 ? (224 * 1024 - 2 * kStageBytes) / kStageBytes : D == 128 ? 3 : 7;
     static constexpr int kRingAt = 2 * kStageBytes;
@@ -153,7 +153,8 @@ static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 
 // And those of an 8-bit cache.
 struct Bars8 {
-    int4 factors[kFactors];  // of blocks, by their place in the run
+    float key_scale[kFactors][kBlock];  // of blocks, by their place in the run, times that of the softmax in base 2
+    int4 value_log2[kFactors];          // what their values are divided by, of 32 places each
     uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
     int2 span[kMaxRaw];      // places from a block's first to the first that is seen, and past the last
 };
@@ -490,11 +491,15 @@ __device__ __forceinline__ bool find_run(const TileArgs& x, int* scratch, Run& r
     return true;
 }
 
-// The factors of 32 places of a block: keys are formed divided by 2^key, values by 2^value.
-__device__ __forceinline__ int pack_factors(int key, int value) { return (key & 0xFFFF) | (value << 16); }
-__device__ __forceinline__ int key_factor(int f) { return (int)(int16_t)f; }
-__device__ __forceinline__ int value_factor(int f) { return f >> 16; }
 __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
 
 // What a row's elements are multiplied by, f = g 2^-h, for products that are rounded once: with G = fp16(g) and
 // d = fp16(g - G),  q f = (q 2^-h) G + (q 2^-h) d.  2^-h, up to 2^-15, keeps g and d normal where f is far
@@ -514,7 +519,16 @@ __device__ __forceinline__ RowFactor row_factor(float f, int room) {
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
-// 16 held elements times their row's factor, to fp16.
+// 16 held elements to fp16, exactly.
+template <class H>
+__device__ __forceinline__ void exact16(const uint4& u, uint4& lo, uint4& hi) {
+    H::to_fp16(u.x, lo.x, lo.y);
+    H::to_fp16(u.y, lo.z, lo.w);
+    H::to_fp16(u.z, hi.x, hi.y);
+    H::to_fp16(u.w, hi.z, hi.w);
+}
+
+// And times their row's factor.
 template <class H>
 __device__ __forceinline__ void scaled16(const uint4& u, const RowFactor& r, uint4& lo, uint4& hi) {
     const __half2 g = as_half2(__byte_perm(r.gd, 0, 0x1010)), d = as_half2(__byte_perm(r.gd, 0, 0x3232));
@@ -661,75 +675,72 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
         if (!ok && lane == 0) fail(x, bars);
     } else if (kHeld8 && warp >= kConvert) {
         // -------------------------------------------------------- conversion
-        // Each warp brings 32 places of every block to fp16, k and then v, as soon as there is room.
-        // A place that is not seen becomes zeros.
+        // Each warp brings 32 places of every block to fp16, a lane each, k and then v, as soon as there is room:
+        // keys as they are held, values times their scales. A place that is not seen becomes zeros.
         if constexpr (kHeld8) {
-            constexpr int kPieces = D / 16, kRowsPer = 32 / kPieces, kLoads = 32 / kRowsPer;
-            const int mine = (warp - kConvert) * 32;  // first place of the block
-            // 8 lanes take the pieces of neighbouring rows whose 16 bytes are in eight bank groups, both as they are
-            // read and as the halves of their fp16 are written
-            const int piece = lane & (kPieces - 1);
-            const int row0 = kPieces == 8 ? (((lane >> 2) ^ (lane >> 3)) & 1) + (lane >> 4) * 2 : lane >> 2;
+            constexpr int kPieces = D / 16;
+            const int place = (warp - kConvert) * 32 + lane;  // of the block
+            // Piece i ^ turn is the lane's i-th: of eight rows the 16 bytes that are read, and those that are written,
+            // are in eight bank groups. (64-byte rows: turn is a product in GF(4), so that it and
+            // its difference from the row both take all four values.)
+            const int r = lane & 7, x2 = r >> 1;
+            const int turn = kPieces == 8 ? r : ((((x2 >> 1) ^ x2) & 1) << 1) | (x2 >> 1);
             const int64_t halves = 2 * (run.end - run.begin);  // k and v blocks
-            // The power of two that takes the largest of 32 rows' elements to fp16's last ones, 2^15 to 2^16, held to
-            // what leaves room on either side: what is 2^21 times smaller than that is still exact to fp16.
-            auto factor = [&](float scale) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(scale, 0.0f)));  // not NaN
-                return min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
-            };
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 if (!wait_bar(bar, parity & 1u, abort, wait_limit())) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
                 return ok;
             };
-            float scale_v = 0.0f;
-            int factor_v = 0;
+            float value_scale = 0.0f;
             int st = 0, rst = 0;                // stages of the two rings
             uint32_t parity = 1, rparity = 0;   // of the one's empty and the other's full barriers
-#pragma unroll 1
-            for (int64_t h = 0; h < halves; ++h) {
+            auto half = [&](int64_t h, auto is_value) {
+                constexpr bool kValue = decltype(is_value)::value;
+                if (!wait(&bars8->raw_full[rst], rparity)) return;
                 const unsigned char* src = smem + L::kRawAt + rst * L::kRawBytes;
-                if (!wait(&bars8->raw_full[rst], rparity)) break;
                 const int2 span = bars8->span[rst];
-                float scale = scale_v;
-                int f = factor_v;
-                if (!(h & 1)) {
-                    const bool seen = mine + lane >= span.x && mine + lane < span.y;
+                const bool seen = place >= span.x && place < span.y;
+                float key_scale = 0.0f;
+                if constexpr (!kValue) {
                     const float* scales = reinterpret_cast<const float*>(src + L::kRawBlock);
-                    scale = seen ? scales[mine + lane] : 0.0f;
-                    scale_v = seen ? scales[kBlock + mine + lane] : 0.0f;
-                    f = factor(scale);
-                    factor_v = factor(scale_v);
+                    key_scale = seen ? scales[place] * a.scale_log2 : 1.0f;
+                    if (key_scale == 0.0f) key_scale = power_of_2(-126);  // times minus infinity, not NaN
+                    value_scale = seen ? scales[kBlock + place] : 0.0f;
                 }
-                uint4 held[kLoads];
+                uint4 held[kPieces];
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    held[i] = *reinterpret_cast<const uint4*>(src + (mine + i * kRowsPer + row0) * D + piece * 16);
-                if (span.x > mine || span.y < mine + 32) {
+                for (int i = 0; i < kPieces; ++i)
+                    held[i] = *reinterpret_cast<const uint4*>(src + place * D + ((i ^ turn) << 4));
+                if (!__all_sync(0xffffffffu, seen)) {
 #pragma unroll
-                    for (int i = 0; i < kLoads; ++i) {
-                        const int row = mine + i * kRowsPer + row0;
-                        if (row < span.x || row >= span.y) held[i] = make_uint4(0, 0, 0, 0);
-                    }
+                    for (int i = 0; i < kPieces; ++i)
+                        if (!seen) held[i] = make_uint4(0, 0, 0, 0);
                 }
-                __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bars8->raw_empty[rst]);
-                const RowFactor rf = row_factor(scale * power_of_2(-f), H::kRoom);
-                if (!wait(&bars->empty[st], parity)) break;  // (the first round's, before any: done)
-                if (!(h & 1) && lane == 0)
-                    reinterpret_cast<int*>(&bars8->factors[(h >> 1) % kFactors])[warp - kConvert] =
-                        pack_factors(f, factor_v);
-                unsigned char* dst = ring + st * L::kStageBytes + (piece >> 2) * L::kSlabBytes;
+                // The power of two that takes the largest of 32 rows' values to fp16's last ones, 2^15 to 2^16, held
+                // to what leaves room on either side: what is 2^21 times smaller than that is still exact to fp16.
+                // (The largest of the scales' bits: not of NaN.)
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(value_scale, 0.0f)));
+                const int log2 = min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
+                RowFactor rf{};
+                if constexpr (kValue) rf = row_factor(value_scale * power_of_2(-log2), H::kRoom);
+                if (!wait(&bars->empty[st], parity)) return;  // (the first round's, before any: done)
+                if constexpr (!kValue) {
+                    const int at = (int)(h >> 1) % kFactors;
+                    bars8->key_scale[at][place] = key_scale;
+                    if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
+                }
+                unsigned char* dst = ring + st * L::kStageBytes + place * 128;
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int row = i * kRowsPer + row0;
-                    const RowFactor r{__shfl_sync(0xffffffffu, rf.gd, row), __shfl_sync(0xffffffffu, rf.pc, row)};
+                for (int i = 0; i < kPieces; ++i) {
                     uint4 lo, hi;
-                    scaled16<H>(held[i], r, lo, hi);
-                    unsigned char* at = dst + (mine + row) * 128;
-                    const int chunk = (piece & 3) * 2;
-                    *reinterpret_cast<uint4*>(at + ((chunk ^ (row & 7)) << 4)) = lo;
-                    *reinterpret_cast<uint4*>(at + (((chunk + 1) ^ (row & 7)) << 4)) = hi;
+                    if constexpr (kValue) scaled16<H>(held[i], rf, lo, hi);
+                    else exact16<H>(held[i], lo, hi);
+                    const int piece = i ^ turn;
+                    unsigned char* to = dst + (piece >> 2) * L::kSlabBytes;
+                    const int chunk = ((piece & 3) * 2) ^ r;
+                    *reinterpret_cast<uint4*>(to + (chunk << 4)) = lo;
+                    *reinterpret_cast<uint4*>(to + ((chunk ^ 1) << 4)) = hi;
                 }
                 ptx::fence_proxy_async_shared();
                 __syncwarp();
@@ -742,6 +753,12 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     rst = 0;
                     rparity ^= 1u;
                 }
+            };
+#pragma unroll 1
+            for (int64_t h = 0; h < halves; h += 2) {
+                half(h, std::false_type{});
+                if (ok) half(h + 1, std::true_type{});
+                if (!ok) break;
             }
             if (!ok && lane == 0) fail(x, bars);
             __syncwarp();
@@ -1154,7 +1171,8 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
         const uint32_t s_addr = lane_base + w * kBlock, o_addr = lane_base + kOutCol + w * D;
         const uint32_t q_smem = ptx::smem_u32(smem) + w * L::kStageBytes;
         int ns = 0, no = 0, nj = 0, npair = 0;
-        float up = 1.0f;  // what this row's queries were divided by (bf16 queries of an 8-bit cache)
+        // what this row's queries are divided by (bf16 queries of an 8-bit cache), and those of the next entry
+        float up = 1.0f, next_up = 1.0f;
         // this half's queries of an entry, 16 bytes a lane; rows past the sequence's are zeros
         auto load_q = [&](const Entry& e) {
             constexpr int kPieces = D / 8, kRowsPer = 32 / kPieces;
@@ -1181,7 +1199,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                                  "r"(u.w)
                                  : "memory");
                     const float of = __shfl_sync(0xffffffffu, by, lane % kRowsPer * kPieces);
-                    if (lane / kRowsPer == i) up = of;
+                    if (lane / kRowsPer == i) next_up = of;
                 } else {
                     ptx::cp_async_16(dst, src, real ? 16u : 0u);
                 }
@@ -1211,7 +1229,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 high = token >= e.count ? 0 : a.causal ? min(e.length, place + 1) : e.length;
             }
             bool load_next = false;
-            const float row_scale = a.scale_log2 * up;
+            up = next_up;
             float m = -INFINITY;
             float2 sum = make_float2(0.0f, 0.0f);
             for (int j = begin; j < end; j += step) {
@@ -1244,57 +1262,71 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     }
                     ptx::tmem_st_wait();
                 }
-                // An 8-bit cache's keys and values are divided by powers of two, the factors of 32 places: those
-                // of the keys multiply the scores, and the maximum and the weights are those of 2^s times the
-                // values' factor, which the sum is divided by again.
-                int4 factors = make_int4(0, 0, 0, 0);
-                if constexpr (kHeld8) factors = bars8->factors[(e.ordinal + j - e.from) % kFactors];
+                // Over an 8-bit cache the keys' scales multiply the scores, and the values are divided by powers of
+                // two, of 32 places each: the maximum and the weights are those of 2^s times that power, by which the
+                // sum is divided again.
+                int4 value_log2 = make_int4(0, 0, 0, 0);
+                const float4* key_scale = nullptr;
+                if constexpr (kHeld8) {
+                    const int at = (e.ordinal + j - e.from) % kFactors;
+                    value_log2 = bars8->value_log2[at];
+                    key_scale = reinterpret_cast<const float4*>(bars8->key_scale[at]);
+                }
                 float top;
                 uint32_t s0[32], s1[32];
                 ptx::tmem_ld_32x32b_x32(s_addr, s0);
                 ptx::tmem_ld_32x32b_x32(s_addr + 32, s1);
                 tmem_ld_wait(s0);
                 tmem_ld_wait(s1);
-                float t[4];
-                auto start = [&](const uint32_t (&s)[32]) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[i]);
-                };
-                auto largest = [&](const uint32_t (&s)[32]) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            t[u] = max3(t[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
-                };
-                auto top_of = [&](int f) {  // of 32 columns with their own factors
-                    return fmaf(fmaxf(max3(t[0], t[1], t[2]), t[3]), row_scale * power_of_2(key_factor(f)),
-                                (float)value_factor(f));
-                };
-                start(s0);
-                largest(s0);
-                ptx::tmem_ld_32x32b_x32(s_addr + 64, s0);
                 if constexpr (kHeld8) {
-                    top = top_of(factors.x);
-                    start(s1);
+                    // the largest of 32 columns from c on
+                    auto largest = [&](const uint32_t (&s)[32], int c, int log2) {
+                        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            const float4 k0 = key_scale[(c + i) / 4], k1 = key_scale[(c + i) / 4 + 1];
+                            auto scaled = [&](int n, float k, float l) {
+                                return mul2(make_float2(__uint_as_float(s[i + n]), __uint_as_float(s[i + n + 1])),
+                                            make_float2(k, l));
+                            };
+                            const float2 v[4] = {scaled(0, k0.x, k0.y), scaled(2, k0.z, k0.w), scaled(4, k1.x, k1.y),
+                                                 scaled(6, k1.z, k1.w)};
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) t[u] = max3(t[u], v[u].x, v[u].y);
+                        }
+                        return fmaf(fmaxf(max3(t[0], t[1], t[2]), t[3]), up, (float)log2);
+                    };
+                    top = largest(s0, 0, value_log2.x);
+                    ptx::tmem_ld_32x32b_x32(s_addr + 64, s0);
+                    top = fmaxf(top, largest(s1, 32, value_log2.y));
+                    ptx::tmem_ld_32x32b_x32(s_addr + 96, s1);
+                    tmem_ld_wait(s0);
+                    tmem_ld_wait(s1);
+                    top = fmaxf(top, largest(s0, 64, value_log2.z));
+                    ptx::tmem_ld_32x32b_x32(s_addr, s0);
+                    top = fmaxf(top, largest(s1, 96, value_log2.w));
+                } else {
+                    float t[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s0[i]);
+                    auto largest = [&](const uint32_t (&s)[32]) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                t[u] = max3(t[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+                    };
+                    largest(s0);
+                    ptx::tmem_ld_32x32b_x32(s_addr + 64, s0);
+                    largest(s1);
+                    ptx::tmem_ld_32x32b_x32(s_addr + 96, s1);
+                    tmem_ld_wait(s0);
+                    tmem_ld_wait(s1);
+                    largest(s0);
+                    ptx::tmem_ld_32x32b_x32(s_addr, s0);
+                    largest(s1);
+                    top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * a.scale_log2;
                 }
-                largest(s1);
-                ptx::tmem_ld_32x32b_x32(s_addr + 96, s1);
-                tmem_ld_wait(s0);
-                tmem_ld_wait(s1);
-                if constexpr (kHeld8) {
-                    top = fmaxf(top, top_of(factors.y));
-                    start(s0);
-                }
-                largest(s0);
-                ptx::tmem_ld_32x32b_x32(s_addr, s0);
-                if constexpr (kHeld8) {
-                    top = fmaxf(top, top_of(factors.z));
-                    start(s1);
-                }
-                largest(s1);
-                if constexpr (kHeld8) top = fmaxf(top, top_of(factors.w));
-                else top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * a.scale_log2;
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {
                     top = fmaxf(top, m);
                     const float keep = m == -INFINITY ? 0.0f : fast_exp2(m - top);
@@ -1315,18 +1347,22 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     }
                 }
                 const float base = m == -INFINITY ? 0.0f : -m;
-                auto weights = [&](int c, uint32_t (&s)[32], int f) {
+                auto weights = [&](int c, uint32_t (&s)[32], int log2) {
                     float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(base, base), part = sum;
                     if constexpr (kHeld8) {
-                        const float by = row_scale * power_of_2(key_factor(f)), from = base + (float)value_factor(f);
-                        c2 = make_float2(by, by);
-                        m2 = make_float2(from, from);
+                        m2 = make_float2(base + (float)log2, base + (float)log2);
                         part = make_float2(0.0f, 0.0f);
                     }
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float2 v = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2);
+                        float2 v = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                        if constexpr (kHeld8) {
+                            const float4 k = key_scale[c / 4 + i / 2];
+                            c2 = i % 2 ? make_float2(k.z, k.w) : make_float2(k.x, k.y);
+                            if constexpr (!std::is_same_v<E, M>) v = mul2(v, make_float2(up, up));
+                        }
+                        v = fma2(v, c2, m2);
                         v.x = fast_exp2(v.x);
                         v.y = fast_exp2(v.y);
                         part = add2(part, v);
@@ -1334,7 +1370,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     }
                     ptx::tmem_st_32x32b_x16(s_addr + (c >> 1), p);
                     if constexpr (kHeld8) {
-                        const float down = power_of_2(-value_factor(f));
+                        const float down = power_of_2(-log2);
                         sum = fma2(part, make_float2(down, down), sum);
                     } else {
                         sum = part;
@@ -1344,10 +1380,10 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 for (int c = 0; c < kBlock; c += 64) {
                     tmem_ld_wait(s0);
                     ptx::tmem_ld_32x32b_x32(s_addr + c + 32, s1);
-                    weights(c, s0, c == 0 ? factors.x : factors.z);
+                    weights(c, s0, c == 0 ? value_log2.x : value_log2.z);
                     tmem_ld_wait(s1);
                     ptx::tmem_ld_32x32b_x32(s_addr + 64, s0);  // (the last time for nothing)
-                    weights(c + 32, s1, c == 0 ? factors.y : factors.w);
+                    weights(c + 32, s1, c == 0 ? value_log2.y : value_log2.w);
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -1551,7 +1587,7 @@ template <class E, class H, int D, bool PAIRED>
 w4a16_status launch(const DeviceInfo& dev, const TileArgs& x, cudaStream_t st) {
     using L = Layout<H, D>;
     static_assert(L::kStages <= kMaxStages, "ring");
-    static_assert(L::kStages / 2 + 3 < kFactors, "the converters' lead");
+    static_assert(!L::kHeld8 || L::kStages / 2 + 3 < kFactors, "the converters' lead");
     static PerDeviceOnce once;
     const cudaError_t e = once.run(dev.device, [] {
         return cudaFuncSetAttribute(tile_kernel<E, H, D, PAIRED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
