@@ -353,6 +353,23 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                  : "memory");
 }
 
+// As above, with nothing said of memory: shared memory that was written before may be read while the loads go on.
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31]));
+}
+
+__device__ __forceinline__ float4 lds_float4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -614,11 +631,6 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem;
-    if constexpr (kHeld8) {
-        // of the launch's 512 x 128 registers: 256 x 136 and 256 x 120
-        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    }
     volatile int* abort = &bars->abort;
     const bool idle = !ok;
     // entry k of the work, for this warp to read; false if it gave up
@@ -634,530 +646,545 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
 
     if (idle) {
         // straight to the end
-    } else if (warp == kPlanWarp) {
-        // -------------------------------------------------------------- plan
-        int64_t left = run.end - run.begin, unit = run.begin;
-        for (int k = 0; ok; ++k) {
-            if (k >= kEntries &&
-                !wait_bar(&bars->work_empty[k % kEntries], (k / kEntries - 1) & 1, abort, wait_limit()))
-                ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const int n = seg.to - seg.from;
-            if (lane == 0) {
-                Entry& e = bars->work[k % kEntries];
-                e.b = seg.b;
-                e.g = seg.g;
-                e.row = seg.tile * kTile;
-                e.first = seg.s.first;
-                e.count = seg.s.count;
-                e.length = seg.s.length;
-                e.low = seg.low;
-                e.from = seg.from;
-                e.to = seg.to;
-                e.ordinal = (int)(unit - run.begin);
-                e.paired = PAIRED && seg.paired(ratio);
-                e.begin[0] = max(seg.half0.block, seg.from);
-                e.begin[1] = e.paired ? seg.from + 1 : max(seg.half1.block, seg.from);
-                e.end[0] = min(seg.half0.end, seg.to);
-                e.end[1] = e.paired ? e.end[0] : min(seg.half1.end, seg.to);
-                const int64_t item = unit - (seg.from - seg.block);
-                e.c0 = run.shares.owner(item, blockIdx.x);
-                e.c1 = run.shares.owner(item + (seg.end - seg.block) - 1, blockIdx.x);
-                e.last = left == n;
-                ptx::mbar_arrive(&bars->work_full[k % kEntries]);
-            }
-            left -= n;
-            unit += n;
-            if (left == 0) break;
-            next_segment(x, left, seg);
-        }
-        if (!ok && lane == 0) fail(x, bars);
-    } else if (kHeld8 && warp >= kConvert) {
-        // -------------------------------------------------------- conversion
-        // Each warp brings 32 places of every block to fp16, a lane each, k and then v, as soon as there is room:
-        // keys as they are held, values times their scales. A place that is not seen becomes zeros.
-        if constexpr (kHeld8) {
-            constexpr int kPieces = D / 16;
-            const int place = (warp - kConvert) * 32 + lane;  // of the block
-            // Piece i ^ turn is the lane's i-th: of eight rows the 16 bytes that are read, and those that are written,
-            // are in eight bank groups. (64-byte rows: turn is a product in GF(4), so that it and
-            // its difference from the row both take all four values.)
-            const int r = lane & 7, x2 = r >> 1;
-            const int turn = kPieces == 8 ? r : ((((x2 >> 1) ^ x2) & 1) << 1) | (x2 >> 1);
-            const int64_t halves = 2 * (run.end - run.begin);  // k and v blocks
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (!wait_bar(bar, parity & 1u, abort, wait_limit())) ok = false;
+    } else if (warp >= kLoadK) {
+        // of the launch's 512 x 128 registers: 256 x 88 and, for the softmax, 256 x 168
+        if constexpr (kHeld8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kPlanWarp) {
+            // -------------------------------------------------------------- plan
+            int64_t left = run.end - run.begin, unit = run.begin;
+            for (int k = 0; ok; ++k) {
+                if (k >= kEntries &&
+                    !wait_bar(&bars->work_empty[k % kEntries], (k / kEntries - 1) & 1, abort, wait_limit()))
+                    ok = false;
                 ok = __all_sync(0xffffffffu, ok);
-                return ok;
-            };
-            float value_scale = 0.0f;
-            int st = 0, rst = 0;                // stages of the two rings
-            uint32_t parity = 1, rparity = 0;   // of the one's empty and the other's full barriers
-            auto half = [&](int64_t h, auto is_value) {
-                constexpr bool kValue = decltype(is_value)::value;
-                if (!wait(&bars8->raw_full[rst], rparity)) return;
-                const unsigned char* src = smem + L::kRawAt + rst * L::kRawBytes;
-                const int2 span = bars8->span[rst];
-                const bool seen = place >= span.x && place < span.y;
-                float key_scale = 0.0f;
-                if constexpr (!kValue) {
-                    const float* scales = reinterpret_cast<const float*>(src + L::kRawBlock);
-                    key_scale = seen ? scales[place] * a.scale_log2 : 1.0f;
-                    if (key_scale == 0.0f) key_scale = power_of_2(-126);  // times minus infinity, not NaN
-                    value_scale = seen ? scales[kBlock + place] : 0.0f;
-                }
-                uint4 held[kPieces];
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-                    held[i] = *reinterpret_cast<const uint4*>(src + place * D + ((i ^ turn) << 4));
-                if (!__all_sync(0xffffffffu, seen)) {
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i)
-                        if (!seen) held[i] = make_uint4(0, 0, 0, 0);
-                }
-                if (lane == 0) ptx::mbar_arrive(&bars8->raw_empty[rst]);
-                // The power of two that takes the largest of 32 rows' values to fp16's last ones, 2^15 to 2^16, held
-                // to what leaves room on either side: what is 2^21 times smaller than that is still exact to fp16.
-                // (The largest of the scales' bits: not of NaN.)
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(value_scale, 0.0f)));
-                const int log2 = min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
-                RowFactor rf{};
-                if constexpr (kValue) rf = row_factor(value_scale * power_of_2(-log2), H::kRoom);
-                if (!wait(&bars->empty[st], parity)) return;  // (the first round's, before any: done)
-                if constexpr (!kValue) {
-                    const int at = (int)(h >> 1) % kFactors;
-                    bars8->key_scale[at][place] = key_scale;
-                    if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
-                }
-                unsigned char* dst = ring + st * L::kStageBytes + place * 128;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    uint4 lo, hi;
-                    if constexpr (kValue) scaled16<H>(held[i], rf, lo, hi);
-                    else exact16<H>(held[i], lo, hi);
-                    const int piece = i ^ turn;
-                    unsigned char* to = dst + (piece >> 2) * L::kSlabBytes;
-                    const int chunk = ((piece & 3) * 2) ^ r;
-                    *reinterpret_cast<uint4*>(to + (chunk << 4)) = lo;
-                    *reinterpret_cast<uint4*>(to + ((chunk ^ 1) << 4)) = hi;
-                }
-                ptx::fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->full[st]);
-                if (++st == L::kStages) {
-                    st = 0;
-                    parity ^= 1u;
-                }
-                if (++rst == L::kRaw) {
-                    rst = 0;
-                    rparity ^= 1u;
-                }
-            };
-#pragma unroll 1
-            for (int64_t h = 0; h < halves; h += 2) {
-                half(h, std::false_type{});
-                if (ok) half(h + 1, std::true_type{});
                 if (!ok) break;
+                const int n = seg.to - seg.from;
+                if (lane == 0) {
+                    Entry& e = bars->work[k % kEntries];
+                    e.b = seg.b;
+                    e.g = seg.g;
+                    e.row = seg.tile * kTile;
+                    e.first = seg.s.first;
+                    e.count = seg.s.count;
+                    e.length = seg.s.length;
+                    e.low = seg.low;
+                    e.from = seg.from;
+                    e.to = seg.to;
+                    e.ordinal = (int)(unit - run.begin);
+                    e.paired = PAIRED && seg.paired(ratio);
+                    e.begin[0] = max(seg.half0.block, seg.from);
+                    e.begin[1] = e.paired ? seg.from + 1 : max(seg.half1.block, seg.from);
+                    e.end[0] = min(seg.half0.end, seg.to);
+                    e.end[1] = e.paired ? e.end[0] : min(seg.half1.end, seg.to);
+                    const int64_t item = unit - (seg.from - seg.block);
+                    e.c0 = run.shares.owner(item, blockIdx.x);
+                    e.c1 = run.shares.owner(item + (seg.end - seg.block) - 1, blockIdx.x);
+                    e.last = left == n;
+                    ptx::mbar_arrive(&bars->work_full[k % kEntries]);
+                }
+                left -= n;
+                unit += n;
+                if (left == 0) break;
+                next_segment(x, left, seg);
             }
             if (!ok && lane == 0) fail(x, bars);
-            __syncwarp();
-        }
-    } else if (warp == kLoadK || warp == kLoadV) {
-        // ------------------------------------------------------------- loads
-        // k blocks are the ring's even entries, v blocks the odd ones
-        // (of an 8-bit cache: of the blocks as they are held)
-        constexpr int kRing = kHeld8 ? L::kRaw : L::kStages, kSlabs = kHeld8 ? 1 : L::kSlabs;
-        uint64_t *full = kHeld8 ? bars8->raw_full : bars->full, *empty = kHeld8 ? bars8->raw_empty : bars->empty;
-        const bool values = warp == kLoadV;
-        const CUtensorMap* map = values ? &map_v : &map_k;
-        const int pieces = kBlock / x.box;
-        const int piece = lane / kSlabs, slab = lane % kSlabs;
-        int n = 0, issued = -1;
-        // The v block of a sequence's last place, or of a window's first, lands on a barrier
-        // of its own; then its slots past the one and before the other are zeroed (0 times what
-        // they hold might not be 0), and only then is it handed on. Other copies go out meanwhile,
-        // but nothing is waited for before that.
-        int dirty = -1, dirty_head = 0, dirty_heads = 0, dirty_row = 0, dirty_rows = 0;
-        uint32_t landed_parity = 0;
-        auto clean = [&] {
-            ok = ok && wait_bar(&bars->landed, landed_parity, abort, wait_limit());
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            landed_parity ^= 1u;
-            const int st = dirty % L::kStages;
-            for (int c = lane; c < (dirty_heads + dirty_rows) * (D / 8); c += 32) {
-                const int i = c / (D / 8), part = c % (D / 8);
-                const int row = i < dirty_heads ? dirty_head + i : dirty_row + i - dirty_heads;
-                *reinterpret_cast<uint4*>(ring + st * L::kStageBytes + (part >> 3) * L::kSlabBytes + row * 128 +
-                                          (part & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            ptx::fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->full[st]);
-            dirty = -1;
-        };
-        auto wait_clean = [&](uint64_t* bar, uint32_t parity) {
-            if (__all_sync(0xffffffffu, ok && ptx::mbar_try_wait(bar, parity))) return true;
-            if (dirty >= 0) clean();
-            ok = ok && wait_bar(bar, parity, abort, wait_limit());
-            ok = __all_sync(0xffffffffu, ok);
-            return ok;
-        };
-        for (int k = 0; wait_clean(&bars->work_full[k % kEntries], (k / kEntries) & 1); ++k) {
-            const Entry& e = bars->work[k % kEntries];
-            const int to = e.to, length = e.length, low = e.low, b = e.b, g = e.g;
-            const bool last = e.last;
-            // the pages of 32 pieces, a lane each, read a group ahead; outside the cache: zeros
-            auto pages_from = [&](int first) {
-                const int p = (first + lane) * x.box;
-                int64_t page = -1;
-                if (p < length && p + x.box > low && p < to * kBlock) page = page_of(a.c, b, p);
-                return (int)(page < 0 ? a.c.pages : page);
-            };
-            int group = e.from * pieces;  // its first piece
-            int pages = pages_from(group), more_pages = pages_from(group + 32);
-            for (int j = e.from; ok && j < to; ++j) {
-                if (j * pieces >= group + 32) {
-                    group += 32;
-                    pages = more_pages;
-                    more_pages = pages_from(group + 32);
-                }
-                const int page = __shfl_sync(0xffffffffu, pages, j * pieces - group + (piece & (pieces - 1)));
-                // Both of a block's stages are waited for in the ring's order, the other
-                // warp's too: a barrier's parity tells only its next phase from the one before.
+        } else if (kHeld8 && warp >= kConvert) {
+            // -------------------------------------------------------- conversion
+            // Each warp brings 32 places of every block to fp16, a lane each, k and then v, as soon as there is room:
+            // keys as they are held, values times their scales. A place that is not seen becomes zeros.
+            if constexpr (kHeld8) {
+                constexpr int kPieces = D / 16;
+                const int place = (warp - kConvert) * 32 + lane;  // of the block
+                // Piece i ^ turn is the lane's i-th: of eight rows the 16 bytes that are read, and those that are written,
+                // are in eight bank groups. (64-byte rows: turn is a product in GF(4), so that it and
+                // its difference from the row both take all four values.)
+                const int r = lane & 7, x2 = r >> 1;
+                const int turn = kPieces == 8 ? r : ((((x2 >> 1) ^ x2) & 1) << 1) | (x2 >> 1);
+                const int64_t halves = 2 * (run.end - run.begin);  // k and v blocks
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    if (!wait_bar(bar, parity & 1u, abort, wait_limit())) ok = false;
+                    ok = __all_sync(0xffffffffu, ok);
+                    return ok;
+                };
+                float value_scale = 0.0f;
+                int st = 0, rst = 0;                // stages of the two rings
+                uint32_t parity = 1, rparity = 0;   // of the one's empty and the other's full barriers
+                auto half = [&](int64_t h, auto is_value) {
+                    constexpr bool kValue = decltype(is_value)::value;
+                    if (!wait(&bars8->raw_full[rst], rparity)) return;
+                    const unsigned char* src = smem + L::kRawAt + rst * L::kRawBytes;
+                    const int2 span = bars8->span[rst];
+                    const bool seen = place >= span.x && place < span.y;
+                    float key_scale = 0.0f;
+                    if constexpr (!kValue) {
+                        const float* scales = reinterpret_cast<const float*>(src + L::kRawBlock);
+                        key_scale = seen ? scales[place] * a.scale_log2 : 1.0f;
+                        if (key_scale == 0.0f) key_scale = power_of_2(-126);  // times minus infinity, not NaN
+                        value_scale = seen ? scales[kBlock + place] : 0.0f;
+                    }
+                    // The power of two that takes the largest of 32 rows' values to fp16's last ones, 2^15 to 2^16, held
+                    // to what leaves room on either side: what is 2^21 times smaller than that is still exact to fp16.
+                    // (The largest of the scales' bits: not of NaN.)
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(value_scale, 0.0f)));
+                    const int log2 = min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
+                    RowFactor rf{};
+                    if constexpr (kValue) rf = row_factor(value_scale * power_of_2(-log2), H::kRoom);
+                    if (!wait(&bars->empty[st], parity)) return;  // (the first round's, before any: done)
+                    if constexpr (!kValue) {
+                        const int at = (int)(h >> 1) % kFactors;
+                        bars8->key_scale[at][place] = key_scale;
+                            if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
+                    }
+                    unsigned char* dst = ring + st * L::kStageBytes + place * 128;
+                    const bool whole = __all_sync(0xffffffffu, seen);
+                    // A loop: straight code for all pieces is longer than the instruction cache has room for beside
+                    // the softmax's (2048 tokens over 30048 places: 8, 4, 2, 1 pieces at once 1303, 1153, 1176,
+                    // 1243 us; 14 sequences of heads of 64 with a window of 1024: 4, 2 pieces 208, 201).
+                    constexpr int kAtOnce = D / 32;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kPieces; i0 += kAtOnce) {
+                        uint4 held[kAtOnce];  // all before the first store: it could be to the same place
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int st = n % kRing, round = n / kRing;
-                    if (dirty >= 0 && __all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->landed, landed_parity)))
-                        clean();
-                    if (round > 0 && !wait_clean(&empty[st], (round - 1) & 1)) break;
-                    if (kv != (values ? 1 : 0)) continue;
-                    ok = may_issue(n);
-                    if (!ok) break;
-                    if constexpr (kHeld8) {
-                        unsigned char* dst = smem + L::kRawAt + st * L::kRawBytes;
-                        if (!values) {  // both blocks' scales, of 4 places a lane
-                            const int p = j * kBlock + lane * 4;
-                            const int its = __shfl_sync(0xffffffffu, pages, j * pieces - group + lane * 4 / x.box);
-                            const bool any = its < a.c.pages && p + 4 > low && p < length;
-                            const int64_t at = any ? (int64_t)its * x.s.page_stride + (int64_t)g * x.s.head_stride +
-                                                         a.c.by_page.remainder(p)
-                                                   : 0;
-                            const uint32_t to_scales = ptx::smem_u32(dst + L::kRawBlock) + lane * 16;
-                            ptx::cp_async_16(to_scales, x.s.k + at, any ? 16u : 0u);
-                            ptx::cp_async_16(to_scales + kBlock * 4, x.s.v + at, any ? 16u : 0u);
+                        for (int i = 0; i < kAtOnce; ++i)
+                            held[i] = *reinterpret_cast<const uint4*>(src + place * D + (((i0 + i) ^ turn) << 4));
+                        if (!whole) {
+#pragma unroll
+                            for (int i = 0; i < kAtOnce; ++i)
+                                if (!seen) held[i] = make_uint4(0, 0, 0, 0);
                         }
-                        if (lane == 0) {
-                            bars8->span[st] = make_int2(low - j * kBlock, length - j * kBlock);
-                            ptx::mbar_arrive_expect_tx(&full[st], L::kRawBlock);
+#pragma unroll
+                        for (int i = 0; i < kAtOnce; ++i) {
+                            uint4 lo, hi;
+                            if constexpr (kValue) scaled16<H>(held[i], rf, lo, hi);
+                            else exact16<H>(held[i], lo, hi);
+                            const int piece = (i0 + i) ^ turn;
+                            unsigned char* to = dst + (piece >> 2) * L::kSlabBytes;
+                            const int chunk = ((piece & 3) * 2) ^ r;
+                            *reinterpret_cast<uint4*>(to + (chunk << 4)) = lo;
+                            *reinterpret_cast<uint4*>(to + ((chunk ^ 1) << 4)) = hi;
                         }
-                        ptx::cp_async_mbar_arrive_noinc(&full[st]);
-                        __syncwarp();
-                        if (piece < pieces)
-                            tma_load_4d(dst + piece * x.box * D, map, &full[st], 0,
-                                        a.c.by_page.remainder(j * kBlock + piece * x.box), g, page);
-                        issued = n;
-                        continue;
                     }
-                    const int rows = values ? tail_rows(length - j * kBlock, x.box) : 0;
-                    const int heads = values ? head_rows(low - j * kBlock, x.box) : 0;
-                    const bool unclean = rows + heads > 0;
-                    if (unclean && dirty >= 0) {
-                        clean();
-                        if (!ok) break;
-                    }
-                    uint64_t* bar = unclean ? &bars->landed : &bars->full[st];
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
+                    ptx::fence_proxy_async_shared();
                     __syncwarp();
-                    if (piece < pieces)
-                        tma_load_4d(ring + st * L::kStageBytes + slab * L::kSlabBytes + piece * x.box * 128, map, bar,
-                                    slab * 64, a.c.by_page.remainder(j * kBlock + piece * x.box), g, page);
-                    issued = n;
-                    if (unclean) {
-                        dirty = n;
-                        dirty_head = low - j * kBlock - heads;
-                        dirty_heads = heads;
-                        dirty_row = length - j * kBlock;
-                        dirty_rows = rows;
+                    if (lane == 0) {
+                        ptx::mbar_arrive(&bars->full[st]);
+                        ptx::mbar_arrive(&bars8->raw_empty[rst]);
                     }
-                }
-            }
-            done_with(k);
-            if (!ok || last) break;
-        }
-        if (ok && dirty >= 0) clean();
-        if (!ok && lane == 0) {
-            fail(x, bars);
-            volatile int never = 0;  // our own copies land before the thread block ends
-            if (dirty >= 0) wait_bar(&bars->landed, landed_parity, &never, kDrainLimitNs);
-            for (int i = issued; i >= 0 && i > issued - kRing; i -= 2)
-                if (i != dirty) wait_bar(&full[i % kRing], (i / kRing) & 1, &never, kDrainLimitNs);
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // --------------------------------------------------------------- MMA
-        // One thread. The tensor core's queue holds about 200 cycles of products, so what
-        // this thread does between two of them is kept below that: what comes next is
-        // worked out while products are queued, not at its turn.
-        constexpr uint32_t kIdescS = idesc<M>(kBlock, false), kIdescO = idesc<M>(D, true);
-        if (elect_one()) {
-            const uint32_t ring_u = ptx::smem_u32(ring);
-            const uint64_t q_desc = ptx::smem_desc_sw128(ptx::smem_u32(smem));
-            const uint64_t k_desc = ptx::smem_desc_sw128(ring_u), v_desc = desc_v(ring_u, L::kSlabBytes);
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (!ptx::mbar_try_wait(bar, parity) && !wait_bar(bar, parity, abort, wait_limit())) ok = false;
-                ptx::tc_fence_after();
-                return ok;
-            };
-            auto scores = [&](int w, uint32_t st) {
-                const uint64_t q = q_desc + (uint64_t)(w * (L::kStageBytes >> 4));
-                const uint64_t k = k_desc + (uint64_t)(st * (L::kStageBytes >> 4));
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t at = (uint64_t)(((ks >> 2) * L::kSlabBytes + (ks & 3) * 32) >> 4);
-                    mma_ss(tmem + w * kBlock, q + at, k + at, kIdescS, ks > 0);
-                }
-                ptx::mma_commit(&bars->s_full[w]);
-            };
-            // p v; where p is not complete yet, the first half of the contraction goes ahead
-            auto output = [&](int w, uint32_t st, uint32_t parity, bool first, bool last) {
-                const uint64_t v = v_desc + (uint64_t)(st * (L::kStageBytes >> 4));
-                const uint32_t o = tmem + kOutCol + w * D, p = tmem + w * kBlock;
-                if (!wait(&bars->p_part[w], parity)) return false;
-                ptx::mma_f16_ts(o, p, v, kIdescO, !first);
-#pragma unroll
-                for (int kk = 1; kk < kBlock / 32; ++kk)
-                    ptx::mma_f16_ts(o, p + kk * 8, v + (uint64_t)((kk * 2048) >> 4), kIdescO, 1u);
-                if (!wait(&bars->p_full[w], parity)) return false;
-#pragma unroll
-                for (int kk = kBlock / 32; kk < kBlock / 16; ++kk)
-                    ptx::mma_f16_ts(o, p + kk * 8, v + (uint64_t)((kk * 2048) >> 4), kIdescO, 1u);
-                if (last) ptx::mma_commit(&bars->o_done[w]);
-                return true;
-            };
-            if constexpr (!PAIRED) {
-                // Block by block, one half and then the other.
-                // what a block needs of its entry
-                struct View {
-                    int to, begin0, end0, begin1, end1, last;
-                };
-                auto view = [&](int k) {
-                    const Entry& e = bars->work[k % kEntries];
-                    return View{e.to, e.begin[0], e.end[0], e.begin[1], e.end[1], e.last};
-                };
-                auto advance = [](uint32_t& st, uint32_t& parity) {
                     if (++st == L::kStages) {
                         st = 0;
                         parity ^= 1u;
                     }
-                };
-                int k = 0;                                // entry of the block whose p v comes next
-                int j = 0, i = 0;                         // that block, and the one whose scores come next
-                uint32_t vst = 0, vparity = 0, kst = 0, kparity = 0;  // their ring stages
-                uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0;
-                bool turn = false, more = true;           // the two are of different entries; there is a second one
-                View cur{}, nxt{};
-                auto plan = [&] {
-                    vst = kst;
-                    vparity = kparity;
-                    advance(vst, vparity);
-                    kst = vst;
-                    kparity = vparity;
-                    advance(kst, kparity);
-                    i = j + 1;
-                    turn = i == cur.to;
-                    more = !turn || !cur.last;
-                    if (turn && more && wait(&bars->work_full[(k + 1) % kEntries], ((k + 1) / kEntries) & 1)) {
-                        nxt = view(k + 1);
-                        i = bars->work[(k + 1) % kEntries].from;
+                    if (++rst == L::kRaw) {
+                        rst = 0;
+                        rparity ^= 1u;
                     }
                 };
-                if (wait(&bars->work_full[0], 0)) {  // the first block's scores
-                    cur = nxt = view(0);
-                    j = bars->work[0].from;
-                    wait(&bars->full[0], 0);
-                    if (ok && j >= cur.begin0 && j < cur.end0 && wait(&bars->q_full[0], 0)) {
-                        scores(0, 0);
-                        q_parity0 = 1;
-                    }
-                    if (ok && j >= cur.begin1 && j < cur.end1 && wait(&bars->q_full[1], 0)) {
-                        scores(1, 0);
-                        q_parity1 = 1;
-                    }
-                    ptx::mma_commit(&bars->empty[0]);
-                    plan();
-                }
-                while (ok) {
-                    if (!wait(&bars->full[vst], vparity)) break;
-                    if (j >= cur.begin0 && j < cur.end0) {
-                        if (!output(0, vst, p_parity0, j == cur.begin0, j == cur.end0 - 1)) break;
-                        p_parity0 ^= 1u;
-                    }
-                    if (more) {
-                        if (!wait(&bars->full[kst], kparity)) break;
-                        if (i >= nxt.begin0 && i < nxt.end0) {
-                            if (i == nxt.begin0) {
-                                if (!wait(&bars->q_full[0], q_parity0)) break;
-                                q_parity0 ^= 1u;
-                            }
-                            scores(0, kst);
-                        }
-                    }
-                    if (j >= cur.begin1 && j < cur.end1) {
-                        if (!output(1, vst, p_parity1, j == cur.begin1, j == cur.end1 - 1)) break;
-                        p_parity1 ^= 1u;
-                    }
-                    ptx::mma_commit(&bars->empty[vst]);
-                    if (!more) break;
-                    // the round after this one, while the products above are queued
-                    const bool second = i >= nxt.begin1 && i < nxt.end1;
-                    if (second && i == nxt.begin1) {
-                        if (!wait(&bars->q_full[1], q_parity1)) break;
-                        q_parity1 ^= 1u;
-                    }
-                    const uint32_t st = kst;
-                    if (turn) {
-                        ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
-                        ++k;
-                        cur = nxt;
-                    }
-                    j = i;
-                    plan();
+#pragma unroll 1
+                for (int64_t h = 0; h < halves; h += 2) {
+                    half(h, std::false_type{});
+                    if (ok) half(h + 1, std::true_type{});
                     if (!ok) break;
-                    if (second) scores(1, st);
-                    ptx::mma_commit(&bars->empty[st]);
                 }
-            } else {
-                // The two halves are two streams of blocks: each has its next scores formed as
-                // soon as its last p is used up. The one that is further behind goes first, and neither
-                // passes the other by more than two blocks. Every block of the run is waited
-                // for by each, in order, whether the half sees it or not.
-                //
-                // A half's p may depend on what the other has yet to do: at the end of a paired
-                // tile each waits for the other's o (pair_in, pair_out) before its next p, and
-                // the stream ahead may be in the tile after that. So nothing is waited for here
-                // that is not on its way whatever this thread does: the first part of p is polled
-                // for like all else (its second part follows from the same pass). The stream
-                // behind can always go on, and that is enough: all of the other's products of the tiles
-                // before it are issued, so its half gets past them, fetches its queries and
-                // announces p; and its blocks are loaded, as the ring holds the two blocks that the
-                // other may be ahead.
-                struct Stream {
-                    int k = -1, j = 0, to = 0;          // entry, block, and the end of the entry's blocks
-                    int begin = 0, end = 0, step = 1;   // the half's blocks of the entry
-                    int shift = 0;                      // from block to place in the run
-                    bool last = false, more = true;
-                    bool formed = false;                // the block's scores are on their way
-                    uint32_t q_parity = 0, p_parity = 0;
-                    __device__ __forceinline__ int at() const { return j + shift; }
-                } s0, s1;
-                // gives a ring entry back, if the other stream is through with it too (else it will)
-                auto release = [&](int n, const Stream& other) {
-                    if (other.at() > n >> 1 || (other.at() == n >> 1 && other.formed && !(n & 1)))
-                        ptx::mma_commit(&bars->empty[n % L::kStages]);
+                if (!ok && lane == 0) fail(x, bars);
+                __syncwarp();
+            }
+        } else if (warp == kLoadK || warp == kLoadV) {
+            // ------------------------------------------------------------- loads
+            // k blocks are the ring's even entries, v blocks the odd ones
+            // (of an 8-bit cache: of the blocks as they are held)
+            constexpr int kRing = kHeld8 ? L::kRaw : L::kStages, kSlabs = kHeld8 ? 1 : L::kSlabs;
+            uint64_t *full = kHeld8 ? bars8->raw_full : bars->full, *empty = kHeld8 ? bars8->raw_empty : bars->empty;
+            const bool values = warp == kLoadV;
+            const CUtensorMap* map = values ? &map_v : &map_k;
+            const int pieces = kBlock / x.box;
+            const int piece = lane / kSlabs, slab = lane % kSlabs;
+            int n = 0, issued = -1;
+            // The v block of a sequence's last place, or of a window's first, lands on a barrier
+            // of its own; then its slots past the one and before the other are zeroed (0 times what
+            // they hold might not be 0), and only then is it handed on. Other copies go out meanwhile,
+            // but nothing is waited for before that.
+            int dirty = -1, dirty_head = 0, dirty_heads = 0, dirty_row = 0, dirty_rows = 0;
+            uint32_t landed_parity = 0;
+            auto clean = [&] {
+                ok = ok && wait_bar(&bars->landed, landed_parity, abort, wait_limit());
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                landed_parity ^= 1u;
+                const int st = dirty % L::kStages;
+                for (int c = lane; c < (dirty_heads + dirty_rows) * (D / 8); c += 32) {
+                    const int i = c / (D / 8), part = c % (D / 8);
+                    const int row = i < dirty_heads ? dirty_head + i : dirty_row + i - dirty_heads;
+                    *reinterpret_cast<uint4*>(ring + st * L::kStageBytes + (part >> 3) * L::kSlabBytes + row * 128 +
+                                              (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bars->full[st]);
+                dirty = -1;
+            };
+            auto wait_clean = [&](uint64_t* bar, uint32_t parity) {
+                if (__all_sync(0xffffffffu, ok && ptx::mbar_try_wait(bar, parity))) return true;
+                if (dirty >= 0) clean();
+                ok = ok && wait_bar(bar, parity, abort, wait_limit());
+                ok = __all_sync(0xffffffffu, ok);
+                return ok;
+            };
+            for (int k = 0; wait_clean(&bars->work_full[k % kEntries], (k / kEntries) & 1); ++k) {
+                const Entry& e = bars->work[k % kEntries];
+                const int to = e.to, length = e.length, low = e.low, b = e.b, g = e.g;
+                const bool last = e.last;
+                // the pages of 32 pieces, a lane each, read a group ahead; outside the cache: zeros
+                auto pages_from = [&](int first) {
+                    const int p = (first + lane) * x.box;
+                    int64_t page = -1;
+                    if (p < length && p + x.box > low && p < to * kBlock) page = page_of(a.c, b, p);
+                    return (int)(page < 0 ? a.c.pages : page);
                 };
-                auto here = [&](int n) {  // entry n of the ring has landed
-                    return ptx::mbar_try_wait(&bars->full[n % L::kStages], (n / L::kStages) & 1);
-                };
-                // towards the half's next block, as far as that goes without waiting
-                auto advance = [&](int w, Stream& s, const Stream& other) {
-                    bool moved = false;
-                    while (s.more && !s.formed) {
-                        if (s.j == s.to) {
-                            if (s.last) {
-                                ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
-                                s.more = false;
-                                return true;
-                            }
-                            const int k = s.k + 1;
-                            if (!ptx::mbar_try_wait(&bars->work_full[k % kEntries], (k / kEntries) & 1)) return moved;
-                            if (k > 0) ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
-                            const Entry& e = bars->work[k % kEntries];
-                            s.k = k;
-                            s.j = e.from;
-                            s.to = e.to;
-                            s.begin = e.begin[w];
-                            s.end = e.end[w];
-                            s.step = e.paired ? 2 : 1;
-                            s.shift = e.ordinal - e.from;
-                            s.last = e.last;
-                            moved = true;
-                        }
-                        const int n = 2 * s.at();
-                        if ((other.more && s.at() > other.at() + 2) || !here(n)) return moved;
-                        if (s.j >= s.begin && s.j < s.end && ((s.j - s.begin) & (s.step - 1)) == 0) {
-                            if (s.j == s.begin) {
-                                if (!ptx::mbar_try_wait(&bars->q_full[w], s.q_parity)) return moved;
-                                s.q_parity ^= 1u;
-                            }
-                            ptx::tc_fence_after();
-                            scores(w, n % L::kStages);
-                            release(n, other);
-                            s.formed = true;
-                            return true;
-                        }
-                        if (!here(n + 1)) return moved;
-                        release(n, other);
-                        release(n + 1, other);
-                        ++s.j;
-                        moved = true;
+                int group = e.from * pieces;  // its first piece
+                int pages = pages_from(group), more_pages = pages_from(group + 32);
+                for (int j = e.from; ok && j < to; ++j) {
+                    if (j * pieces >= group + 32) {
+                        group += 32;
+                        pages = more_pages;
+                        more_pages = pages_from(group + 32);
                     }
-                    return moved;
-                };
-                auto add_values = [&](int w, Stream& s, const Stream& other) {
-                    const int n = 2 * s.at() + 1;
-                    if (!here(n)) return false;
-                    // Where the half goes on in the same tile and the blocks up to its next one are
-                    // here, that is found out before the wait for p, and the next scores follow
-                    // the products at once.
-                    const int ahead = n - 1 + 2 * s.step;  // the next block's k
-                    bool on = s.j + s.step < s.end && (!other.more || s.at() + s.step <= other.at() + 2) && here(ahead);
-                    if (s.step == 2) on = on && here(n + 1) && here(n + 2);
-                    const int st = ahead % L::kStages;
-                    if (!ptx::mbar_try_wait(&bars->p_part[w], s.p_parity)) return false;
-                    if (!output(w, n % L::kStages, s.p_parity, s.j == s.begin, s.j + s.step >= s.end)) return false;
-                    s.p_parity ^= 1u;
-                    release(n, other);
-                    if (on) scores(w, st);
-                    if (on) {
-                        if (s.step == 2) {
-                            release(n + 1, other);
-                            release(n + 2, other);
+                    const int page = __shfl_sync(0xffffffffu, pages, j * pieces - group + (piece & (pieces - 1)));
+                    // Both of a block's stages are waited for in the ring's order, the other
+                    // warp's too: a barrier's parity tells only its next phase from the one before.
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++n) {
+                        const int st = n % kRing, round = n / kRing;
+                        if (dirty >= 0 && __all_sync(0xffffffffu, ptx::mbar_try_wait(&bars->landed, landed_parity)))
+                            clean();
+                        if (round > 0 && !wait_clean(&empty[st], (round - 1) & 1)) break;
+                        if (kv != (values ? 1 : 0)) continue;
+                        ok = may_issue(n);
+                        if (!ok) break;
+                        if constexpr (kHeld8) {
+                            unsigned char* dst = smem + L::kRawAt + st * L::kRawBytes;
+                            if (!values) {  // both blocks' scales, of 4 places a lane
+                                const int p = j * kBlock + lane * 4;
+                                const int its = __shfl_sync(0xffffffffu, pages, j * pieces - group + lane * 4 / x.box);
+                                const bool any = its < a.c.pages && p + 4 > low && p < length;
+                                const int64_t at = any ? (int64_t)its * x.s.page_stride + (int64_t)g * x.s.head_stride +
+                                                             a.c.by_page.remainder(p)
+                                                       : 0;
+                                const uint32_t to_scales = ptx::smem_u32(dst + L::kRawBlock) + lane * 16;
+                                ptx::cp_async_16(to_scales, x.s.k + at, any ? 16u : 0u);
+                                ptx::cp_async_16(to_scales + kBlock * 4, x.s.v + at, any ? 16u : 0u);
+                            }
+                            if (lane == 0) {
+                                bars8->span[st] = make_int2(low - j * kBlock, length - j * kBlock);
+                                ptx::mbar_arrive_expect_tx(&full[st], L::kRawBlock);
+                            }
+                            ptx::cp_async_mbar_arrive_noinc(&full[st]);
+                            __syncwarp();
+                            if (piece < pieces)
+                                tma_load_4d(dst + piece * x.box * D, map, &full[st], 0,
+                                            a.c.by_page.remainder(j * kBlock + piece * x.box), g, page);
+                            issued = n;
+                            continue;
                         }
-                        release(ahead, other);
-                        s.j += s.step;
-                    } else {
-                        ++s.j;
-                        s.formed = false;
+                        const int rows = values ? tail_rows(length - j * kBlock, x.box) : 0;
+                        const int heads = values ? head_rows(low - j * kBlock, x.box) : 0;
+                        const bool unclean = rows + heads > 0;
+                        if (unclean && dirty >= 0) {
+                            clean();
+                            if (!ok) break;
+                        }
+                        uint64_t* bar = unclean ? &bars->landed : &bars->full[st];
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
+                        __syncwarp();
+                        if (piece < pieces)
+                            tma_load_4d(ring + st * L::kStageBytes + slab * L::kSlabBytes + piece * x.box * 128, map, bar,
+                                        slab * 64, a.c.by_page.remainder(j * kBlock + piece * x.box), g, page);
+                        issued = n;
+                        if (unclean) {
+                            dirty = n;
+                            dirty_head = low - j * kBlock - heads;
+                            dirty_heads = heads;
+                            dirty_row = length - j * kBlock;
+                            dirty_rows = rows;
+                        }
                     }
+                }
+                done_with(k);
+                if (!ok || last) break;
+            }
+            if (ok && dirty >= 0) clean();
+            if (!ok && lane == 0) {
+                fail(x, bars);
+                volatile int never = 0;  // our own copies land before the thread block ends
+                if (dirty >= 0) wait_bar(&bars->landed, landed_parity, &never, kDrainLimitNs);
+                for (int i = issued; i >= 0 && i > issued - kRing; i -= 2)
+                    if (i != dirty) wait_bar(&full[i % kRing], (i / kRing) & 1, &never, kDrainLimitNs);
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp) {
+            // --------------------------------------------------------------- MMA
+            // One thread. The tensor core's queue holds about 200 cycles of products, so what
+            // this thread does between two of them is kept below that: what comes next is
+            // worked out while products are queued, not at its turn.
+            constexpr uint32_t kIdescS = idesc<M>(kBlock, false), kIdescO = idesc<M>(D, true);
+            if (elect_one()) {
+                const uint32_t ring_u = ptx::smem_u32(ring);
+                const uint64_t q_desc = ptx::smem_desc_sw128(ptx::smem_u32(smem));
+                const uint64_t k_desc = ptx::smem_desc_sw128(ring_u), v_desc = desc_v(ring_u, L::kSlabBytes);
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    if (!ptx::mbar_try_wait(bar, parity) && !wait_bar(bar, parity, abort, wait_limit())) ok = false;
+                    ptx::tc_fence_after();
+                    return ok;
+                };
+                auto scores = [&](int w, uint32_t st) {
+                    const uint64_t q = q_desc + (uint64_t)(w * (L::kStageBytes >> 4));
+                    const uint64_t k = k_desc + (uint64_t)(st * (L::kStageBytes >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t at = (uint64_t)(((ks >> 2) * L::kSlabBytes + (ks & 3) * 32) >> 4);
+                        mma_ss(tmem + w * kBlock, q + at, k + at, kIdescS, ks > 0);
+                    }
+                    ptx::mma_commit(&bars->s_full[w]);
+                };
+                // p v; where p is not complete yet, the first half of the contraction goes ahead
+                auto output = [&](int w, uint32_t st, uint32_t parity, bool first, bool last) {
+                    const uint64_t v = v_desc + (uint64_t)(st * (L::kStageBytes >> 4));
+                    const uint32_t o = tmem + kOutCol + w * D, p = tmem + w * kBlock;
+                    if (!wait(&bars->p_part[w], parity)) return false;
+                    ptx::mma_f16_ts(o, p, v, kIdescO, !first);
+#pragma unroll
+                    for (int kk = 1; kk < kBlock / 32; ++kk)
+                        ptx::mma_f16_ts(o, p + kk * 8, v + (uint64_t)((kk * 2048) >> 4), kIdescO, 1u);
+                    if (!wait(&bars->p_full[w], parity)) return false;
+#pragma unroll
+                    for (int kk = kBlock / 32; kk < kBlock / 16; ++kk)
+                        ptx::mma_f16_ts(o, p + kk * 8, v + (uint64_t)((kk * 2048) >> 4), kIdescO, 1u);
+                    if (last) ptx::mma_commit(&bars->o_done[w]);
                     return true;
                 };
-                uint64_t since = 0;
-                int idle = 0;
-                while (ok && (s0.more || s1.more)) {
-                    bool moved = s0.formed && (!s1.formed || s0.at() <= s1.at()) && add_values(0, s0, s1);
-                    if (!moved && s1.formed) moved = add_values(1, s1, s0);
-                    moved |= advance(0, s0, s1);
-                    moved |= advance(1, s1, s0);
-                    if (moved) {
-                        idle = 0;
-                        since = 0;
-                    } else if ((++idle & 31) == 0) {  // bounded, like every wait
-                        const uint64_t now = ptx::globaltimer_ns();
-                        if (since == 0) since = now;
-                        if (*abort || now - since > wait_limit()) ok = false;
+                if constexpr (!PAIRED) {
+                    // Block by block, one half and then the other.
+                    // what a block needs of its entry
+                    struct View {
+                        int to, begin0, end0, begin1, end1, last;
+                    };
+                    auto view = [&](int k) {
+                        const Entry& e = bars->work[k % kEntries];
+                        return View{e.to, e.begin[0], e.end[0], e.begin[1], e.end[1], e.last};
+                    };
+                    auto advance = [](uint32_t& st, uint32_t& parity) {
+                        if (++st == L::kStages) {
+                            st = 0;
+                            parity ^= 1u;
+                        }
+                    };
+                    int k = 0;                                // entry of the block whose p v comes next
+                    int j = 0, i = 0;                         // that block, and the one whose scores come next
+                    uint32_t vst = 0, vparity = 0, kst = 0, kparity = 0;  // their ring stages
+                    uint32_t q_parity0 = 0, q_parity1 = 0, p_parity0 = 0, p_parity1 = 0;
+                    bool turn = false, more = true;           // the two are of different entries; there is a second one
+                    View cur{}, nxt{};
+                    auto plan = [&] {
+                        vst = kst;
+                        vparity = kparity;
+                        advance(vst, vparity);
+                        kst = vst;
+                        kparity = vparity;
+                        advance(kst, kparity);
+                        i = j + 1;
+                        turn = i == cur.to;
+                        more = !turn || !cur.last;
+                        if (turn && more && wait(&bars->work_full[(k + 1) % kEntries], ((k + 1) / kEntries) & 1)) {
+                            nxt = view(k + 1);
+                            i = bars->work[(k + 1) % kEntries].from;
+                        }
+                    };
+                    if (wait(&bars->work_full[0], 0)) {  // the first block's scores
+                        cur = nxt = view(0);
+                        j = bars->work[0].from;
+                        wait(&bars->full[0], 0);
+                        if (ok && j >= cur.begin0 && j < cur.end0 && wait(&bars->q_full[0], 0)) {
+                            scores(0, 0);
+                            q_parity0 = 1;
+                        }
+                        if (ok && j >= cur.begin1 && j < cur.end1 && wait(&bars->q_full[1], 0)) {
+                            scores(1, 0);
+                            q_parity1 = 1;
+                        }
+                        ptx::mma_commit(&bars->empty[0]);
+                        plan();
+                    }
+                    while (ok) {
+                        if (!wait(&bars->full[vst], vparity)) break;
+                        if (j >= cur.begin0 && j < cur.end0) {
+                            if (!output(0, vst, p_parity0, j == cur.begin0, j == cur.end0 - 1)) break;
+                            p_parity0 ^= 1u;
+                        }
+                        if (more) {
+                            if (!wait(&bars->full[kst], kparity)) break;
+                            if (i >= nxt.begin0 && i < nxt.end0) {
+                                if (i == nxt.begin0) {
+                                    if (!wait(&bars->q_full[0], q_parity0)) break;
+                                    q_parity0 ^= 1u;
+                                }
+                                scores(0, kst);
+                            }
+                        }
+                        if (j >= cur.begin1 && j < cur.end1) {
+                            if (!output(1, vst, p_parity1, j == cur.begin1, j == cur.end1 - 1)) break;
+                            p_parity1 ^= 1u;
+                        }
+                        ptx::mma_commit(&bars->empty[vst]);
+                        if (!more) break;
+                        // the round after this one, while the products above are queued
+                        const bool second = i >= nxt.begin1 && i < nxt.end1;
+                        if (second && i == nxt.begin1) {
+                            if (!wait(&bars->q_full[1], q_parity1)) break;
+                            q_parity1 ^= 1u;
+                        }
+                        const uint32_t st = kst;
+                        if (turn) {
+                            ptx::mbar_arrive(&bars->work_empty[k % kEntries]);
+                            ++k;
+                            cur = nxt;
+                        }
+                        j = i;
+                        plan();
+                        if (!ok) break;
+                        if (second) scores(1, st);
+                        ptx::mma_commit(&bars->empty[st]);
+                    }
+                } else {
+                    // The two halves are two streams of blocks: each has its next scores formed as
+                    // soon as its last p is used up. The one that is further behind goes first, and neither
+                    // passes the other by more than two blocks. Every block of the run is waited
+                    // for by each, in order, whether the half sees it or not.
+                    //
+                    // A half's p may depend on what the other has yet to do: at the end of a paired
+                    // tile each waits for the other's o (pair_in, pair_out) before its next p, and
+                    // the stream ahead may be in the tile after that. So nothing is waited for here
+                    // that is not on its way whatever this thread does: the first part of p is polled
+                    // for like all else (its second part follows from the same pass). The stream
+                    // behind can always go on, and that is enough: all of the other's products of the tiles
+                    // before it are issued, so its half gets past them, fetches its queries and
+                    // announces p; and its blocks are loaded, as the ring holds the two blocks that the
+                    // other may be ahead.
+                    struct Stream {
+                        int k = -1, j = 0, to = 0;          // entry, block, and the end of the entry's blocks
+                        int begin = 0, end = 0, step = 1;   // the half's blocks of the entry
+                        int shift = 0;                      // from block to place in the run
+                        bool last = false, more = true;
+                        bool formed = false;                // the block's scores are on their way
+                        uint32_t q_parity = 0, p_parity = 0;
+                        __device__ __forceinline__ int at() const { return j + shift; }
+                    } s0, s1;
+                    // gives a ring entry back, if the other stream is through with it too (else it will)
+                    auto release = [&](int n, const Stream& other) {
+                        if (other.at() > n >> 1 || (other.at() == n >> 1 && other.formed && !(n & 1)))
+                            ptx::mma_commit(&bars->empty[n % L::kStages]);
+                    };
+                    auto here = [&](int n) {  // entry n of the ring has landed
+                        return ptx::mbar_try_wait(&bars->full[n % L::kStages], (n / L::kStages) & 1);
+                    };
+                    // towards the half's next block, as far as that goes without waiting
+                    auto advance = [&](int w, Stream& s, const Stream& other) {
+                        bool moved = false;
+                        while (s.more && !s.formed) {
+                            if (s.j == s.to) {
+                                if (s.last) {
+                                    ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
+                                    s.more = false;
+                                    return true;
+                                }
+                                const int k = s.k + 1;
+                                if (!ptx::mbar_try_wait(&bars->work_full[k % kEntries], (k / kEntries) & 1)) return moved;
+                                if (k > 0) ptx::mbar_arrive(&bars->work_empty[s.k % kEntries]);
+                                const Entry& e = bars->work[k % kEntries];
+                                s.k = k;
+                                s.j = e.from;
+                                s.to = e.to;
+                                s.begin = e.begin[w];
+                                s.end = e.end[w];
+                                s.step = e.paired ? 2 : 1;
+                                s.shift = e.ordinal - e.from;
+                                s.last = e.last;
+                                moved = true;
+                            }
+                            const int n = 2 * s.at();
+                            if ((other.more && s.at() > other.at() + 2) || !here(n)) return moved;
+                            if (s.j >= s.begin && s.j < s.end && ((s.j - s.begin) & (s.step - 1)) == 0) {
+                                if (s.j == s.begin) {
+                                    if (!ptx::mbar_try_wait(&bars->q_full[w], s.q_parity)) return moved;
+                                    s.q_parity ^= 1u;
+                                }
+                                ptx::tc_fence_after();
+                                scores(w, n % L::kStages);
+                                release(n, other);
+                                s.formed = true;
+                                return true;
+                            }
+                            if (!here(n + 1)) return moved;
+                            release(n, other);
+                            release(n + 1, other);
+                            ++s.j;
+                            moved = true;
+                        }
+                        return moved;
+                    };
+                    auto add_values = [&](int w, Stream& s, const Stream& other) {
+                        const int n = 2 * s.at() + 1;
+                        if (!here(n)) return false;
+                        // Where the half goes on in the same tile and the blocks up to its next one are
+                        // here, that is found out before the wait for p, and the next scores follow
+                        // the products at once.
+                        const int ahead = n - 1 + 2 * s.step;  // the next block's k
+                        bool on = s.j + s.step < s.end && (!other.more || s.at() + s.step <= other.at() + 2) && here(ahead);
+                        if (s.step == 2) on = on && here(n + 1) && here(n + 2);
+                        const int st = ahead % L::kStages;
+                        if (!ptx::mbar_try_wait(&bars->p_part[w], s.p_parity)) return false;
+                        if (!output(w, n % L::kStages, s.p_parity, s.j == s.begin, s.j + s.step >= s.end)) return false;
+                        s.p_parity ^= 1u;
+                        release(n, other);
+                        if (on) scores(w, st);
+                        if (on) {
+                            if (s.step == 2) {
+                                release(n + 1, other);
+                                release(n + 2, other);
+                            }
+                            release(ahead, other);
+                            s.j += s.step;
+                        } else {
+                            ++s.j;
+                            s.formed = false;
+                        }
+                        return true;
+                    };
+                    uint64_t since = 0;
+                    int idle = 0;
+                    while (ok && (s0.more || s1.more)) {
+                        bool moved = s0.formed && (!s1.formed || s0.at() <= s1.at()) && add_values(0, s0, s1);
+                        if (!moved && s1.formed) moved = add_values(1, s1, s0);
+                        moved |= advance(0, s0, s1);
+                        moved |= advance(1, s1, s0);
+                        if (moved) {
+                            idle = 0;
+                            since = 0;
+                        } else if ((++idle & 31) == 0) {  // bounded, like every wait
+                            const uint64_t now = ptx::globaltimer_ns();
+                            if (since == 0) since = now;
+                            if (*abort || now - since > wait_limit()) ok = false;
+                        }
                     }
                 }
+                if (!ok) fail(x, bars);
+                ptx::mma_commit(&bars->mma_done);
+                volatile int never = 0;
+                wait_bar(&bars->mma_done, 0, &never, kDrainLimitNs);
             }
-            if (!ok) fail(x, bars);
-            ptx::mma_commit(&bars->mma_done);
-            volatile int never = 0;
-            wait_bar(&bars->mma_done, 0, &never, kDrainLimitNs);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
         // ----------------------------------------------------------- softmax
+        if constexpr (kHeld8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // How far a score may pass the maximum before it moves. Not at all where there are few rows,
         // whose time is the cache's: the largest weight is then 1 and exact, and the error of
         // rounding p next to nothing (87 against 85 us at 25 rows; errors 1.0 to 1.1 times
@@ -1266,46 +1293,60 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 // two, of 32 places each: the maximum and the weights are those of 2^s times that power, by which the
                 // sum is divided again.
                 int4 value_log2 = make_int4(0, 0, 0, 0);
-                const float4* key_scale = nullptr;
+                uint32_t key_scale = 0;
+                float4 k0[4], k1[4];  // scales of 16 columns each
+                auto load_scales = [&](float4 (&k)[4], int c) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) k[i] = lds_float4(key_scale + (c + 4 * i) * 4);
+                };
                 if constexpr (kHeld8) {
                     const int at = (e.ordinal + j - e.from) % kFactors;
                     value_log2 = bars8->value_log2[at];
-                    key_scale = reinterpret_cast<const float4*>(bars8->key_scale[at]);
+                    key_scale = ptx::smem_u32(bars8->key_scale[at]);
                 }
                 float top;
                 uint32_t s0[32], s1[32];
                 ptx::tmem_ld_32x32b_x32(s_addr, s0);
                 ptx::tmem_ld_32x32b_x32(s_addr + 32, s1);
-                tmem_ld_wait(s0);
-                tmem_ld_wait(s1);
                 if constexpr (kHeld8) {
-                    // the largest of 32 columns from c on
-                    auto largest = [&](const uint32_t (&s)[32], int c, int log2) {
-                        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    // The largest of 16 columns; the scales of 16 others are on their way meanwhile.
+                    auto largest = [&](const uint32_t (&s)[32], int from, const float4 (&k)[4], float t) {
+                        float u = t;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            const float4 k0 = key_scale[(c + i) / 4], k1 = key_scale[(c + i) / 4 + 1];
-                            auto scaled = [&](int n, float k, float l) {
-                                return mul2(make_float2(__uint_as_float(s[i + n]), __uint_as_float(s[i + n + 1])),
-                                            make_float2(k, l));
-                            };
-                            const float2 v[4] = {scaled(0, k0.x, k0.y), scaled(2, k0.z, k0.w), scaled(4, k1.x, k1.y),
-                                                 scaled(6, k1.z, k1.w)};
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) t[u] = max3(t[u], v[u].x, v[u].y);
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 a = mul2(make_float2(__uint_as_float(s[from + 4 * i]),
+                                                              __uint_as_float(s[from + 4 * i + 1])),
+                                                  make_float2(k[i].x, k[i].y));
+                            const float2 b = mul2(make_float2(__uint_as_float(s[from + 4 * i + 2]),
+                                                              __uint_as_float(s[from + 4 * i + 3])),
+                                                  make_float2(k[i].z, k[i].w));
+                            t = max3(t, a.x, a.y);
+                            u = max3(u, b.x, b.y);
                         }
-                        return fmaf(fmaxf(max3(t[0], t[1], t[2]), t[3]), up, (float)log2);
+                        return fmaxf(t, u);
                     };
-                    top = largest(s0, 0, value_log2.x);
+                    auto largest32 = [&](const uint32_t (&s)[32], int c, int log2) {
+                        load_scales(k1, c + 16);
+                        float t = largest(s, 0, k0, -INFINITY);
+                        load_scales(k0, (c + 32) & (kBlock - 1));
+                        t = largest(s, 16, k1, t);
+                        return fmaf(t, up, (float)log2);
+                    };
+                    load_scales(k0, 0);
+                    wait_loads(s0);
+                    wait_loads(s1);
+                    top = largest32(s0, 0, value_log2.x);
                     ptx::tmem_ld_32x32b_x32(s_addr + 64, s0);
-                    top = fmaxf(top, largest(s1, 32, value_log2.y));
+                    top = fmaxf(top, largest32(s1, 32, value_log2.y));
                     ptx::tmem_ld_32x32b_x32(s_addr + 96, s1);
+                    wait_loads(s0);
+                    wait_loads(s1);
+                    top = fmaxf(top, largest32(s0, 64, value_log2.z));
+                    ptx::tmem_ld_32x32b_x32(s_addr, s0);
+                    top = fmaxf(top, largest32(s1, 96, value_log2.w));
+                } else {
                     tmem_ld_wait(s0);
                     tmem_ld_wait(s1);
-                    top = fmaxf(top, largest(s0, 64, value_log2.z));
-                    ptx::tmem_ld_32x32b_x32(s_addr, s0);
-                    top = fmaxf(top, largest(s1, 96, value_log2.w));
-                } else {
                     float t[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s0[i]);
@@ -1358,7 +1399,9 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     for (int i = 0; i < 16; ++i) {
                         float2 v = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
                         if constexpr (kHeld8) {
-                            const float4 k = key_scale[c / 4 + i / 2];
+                            if (i == 0) load_scales(k1, c + 16);
+                            if (i == 8) load_scales(k0, (c + 32) & (kBlock - 1));
+                            const float4 k = i < 8 ? k0[i / 2] : k1[i / 2 - 4];
                             c2 = i % 2 ? make_float2(k.z, k.w) : make_float2(k.x, k.y);
                             if constexpr (!std::is_same_v<E, M>) v = mul2(v, make_float2(up, up));
                         }
