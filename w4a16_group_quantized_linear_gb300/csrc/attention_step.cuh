@@ -153,7 +153,9 @@ struct StepArgs {
     int* counters;   // one per thread block, zero between calls
     float* parts;    // [2 * blocks][rows][D]: o of the parts of divided items
     float2* stats;   // [2 * blocks][rows]: their m and l
-    ScaleArgs s;     // of an 8-bit cache
+    // of an 8-bit cache:
+    ScaleArgs s;
+    int lanes, turns;  // cached heads that are worked on side by side, and how many times that makes them all
 };
 
 // A sequence as this kernel sees it; blocks == 0: not one of its own.
@@ -175,12 +177,13 @@ __device__ __forceinline__ void load_sequence(const AttentionArgs& a, int b, int
     s.blocks = max(1, (s.length + kBlock - 1) / kBlock - s.block);
 }
 
-// This thread block's run of `total` units.
-__device__ __forceinline__ void share_out(int64_t total, Shares& shares, int64_t& begin, int64_t& end) {
-    shares.base = total / gridDim.x;
-    shares.more = (int)(total - shares.base * gridDim.x);
-    begin = shares.start(blockIdx.x);
-    end = shares.start(blockIdx.x + 1);
+// Run `run` of `runs` of `total` units.
+__device__ __forceinline__ void share_out(int64_t total, unsigned run, unsigned runs, Shares& shares, int64_t& begin,
+                                          int64_t& end) {
+    shares.base = total / runs;
+    shares.more = (int)(total - shares.base * runs);
+    begin = shares.start(run);
+    end = shares.start(run + 1);
 }
 
 // A position in the work list, as a warp walks it.
@@ -189,8 +192,9 @@ struct Cursor {
     Sequence s;
 };
 
-__device__ __forceinline__ void next_item(const AttentionArgs& a, int max_rows, Cursor& c) {
-    if (++c.g == a.c.kv_heads) {
+// turns: of the cached heads of a sequence (each, or `lanes` of them, is an item)
+__device__ __forceinline__ void next_item(const AttentionArgs& a, int max_rows, int turns, Cursor& c) {
+    if (++c.g == turns) {
         c.g = 0;
         do {
             if (++c.b >= a.c.batch) {  // past the list's end: never used
@@ -221,10 +225,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp = lane >> 2, quad = lane & 3;
     const int ratio = a.ratio;
+    // Over an 8-bit cache a run of blocks is that of `lanes` thread blocks, a cached head each: the rows of a place's heads
+    // are neighbours in memory, and so are read at the same time. (As runs of one head after another, whose
+    // 128 bytes of a place are read alone, two sequences of 120 to 150 thousand places took 118 us.)
+    const int lanes = kHeld8 ? arg.lanes : 1, turns = kHeld8 ? arg.turns : a.c.kv_heads;
+    const unsigned run = blockIdx.x / lanes, runs = gridDim.x / lanes;
+    const int head0 = kHeld8 ? (int)(blockIdx.x - run * lanes) : 0;
+    auto head_of = [&](int g) { return kHeld8 ? min(g * lanes + head0, a.c.kv_heads - 1) : g; };
 
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     if (blockIdx.x == 0) check_offsets(a.c);
+    if (kHeld8 && run >= runs) return;
 
     // the length of the work list, then the item in which this thread block's
     // run starts; one round does for both while there are no more sequences than threads
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             int64_t n = 0;
             if (b0 + tid < a.c.batch) {
                 load_sequence(a, b0 + tid, kRows, s);
-                n = (int64_t)s.blocks * a.c.kv_heads;
+                n = (int64_t)s.blocks * turns;
                 if (blockIdx.x == 0 && s.count > a.max_q_len) raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
             }
             int64_t upto = n;  // inclusive sum over the threads
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                 before += s_sum[w];
             }
             if (round == 0 && a.c.batch <= kThreads) {
-                share_out(before, shares, run_begin, run_end);
+                share_out(before, run, runs, shares, run_begin, run_end);
                 round = 1;
             }
             if (round == 1 && run_begin >= upto - n && run_begin < upto) {
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             }
             if (round == 1 && before > run_begin) break;
         }
-        if (round == 0) share_out(before, shares, run_begin, run_end);
+        if (round == 0) share_out(before, run, runs, shares, run_begin, run_end);
         if (run_begin >= run_end) return;
     }
     __syncthreads();
@@ -288,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     int pages_from = -1;  // this lane holds the page of block pages_from + lane of the sequence
     int my_page = -1;
     int pages_b = -1;
-    auto load_step = [&](int stage) {
+    // The step of a 16-bit cache.
+    auto load_step16 = [&](int stage) {
         if (to_load > 0) {
             if (pages_b != to.b || to.block < pages_from || to.block >= pages_from + 32) {
                 pages_b = to.b;
@@ -311,32 +324,83 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                 const int p = p0 + row;
                 // places outside the sequence or before every row's window: zeros, nothing read
                 const uint32_t size = page >= 0 && p >= to.s.low && p < to.s.length ? 16u : 0u;
-                const int64_t off = size ? base + row * a.c.slot_stride + chunk * (kHeld8 ? 16 : 8) : 0;
-                if constexpr (kHeld8) {
-                    ptx::cp_async_16(dst + L::at(row, chunk), reinterpret_cast<const uint8_t*>(a.c.k) + off, size);
-                    ptx::cp_async_16(dst + L::kHalfStage + L::at(row, chunk),
-                                     reinterpret_cast<const uint8_t*>(a.c.v) + off, size);
-                } else {
-                    ptx::cp_async_16(dst + L::at(row, chunk), a.c.k + off, size);
-                    ptx::cp_async_16(dst + L::kHalfStage + L::at(row, chunk), a.c.v + off, size);
-                }
-            }
-            if constexpr (kHeld8) {
-                // scales of 4 places a lane, keys' and then values'; those of places that are not read, 0
-                if (lane < kStep / 2) {
-                    const int p = p0 + (lane & 3) * 4;
-                    const bool any = page >= 0 && p + 4 > to.s.low && p < to.s.length;
-                    const int64_t off = any ? (int64_t)page * arg.s.page_stride + (int64_t)to.g * arg.s.head_stride +
-                                                  a.c.by_page.remainder(p0) + (lane & 3) * 4
-                                            : 0;
-                    ptx::cp_async_16(dst + 2 * L::kHalfStage + lane * 16, (lane < 4 ? arg.s.k : arg.s.v) + off,
-                                     any ? 16u : 0u);
-                }
+                const int64_t off = size ? base + row * a.c.slot_stride + chunk * 8 : 0;
+                ptx::cp_async_16(dst + L::at(row, chunk), a.c.k + off, size);
+                ptx::cp_async_16(dst + L::kHalfStage + L::at(row, chunk), a.c.v + off, size);
             }
             --to_load;
-            if (++to.block == to.end && to_load > 0) next_item(a, kRows, to);
+            if (++to.block == to.end && to_load > 0) next_item(a, kRows, turns, to);
         }
         cp_async_commit();
+    };
+
+    // Of an 8-bit cache: steps are half as long, so what they cost beside the copies counts. Where a block's rows are
+    // is worked out 32 blocks at a time, a lane each.
+    int64_t my_rows = -1, my_scales = -1;  // of the lane's block: offsets of the warp's first row and scale in a head
+    auto load_step8 = [&](int stage) {
+        if (to_load > 0) {
+            if (pages_b != to.b || to.block < pages_from || to.block >= pages_from + 32) {
+                pages_b = to.b;
+                pages_from = to.block;
+                const int p = (to.block + lane) * kBlock + warp * kStep;
+                my_rows = my_scales = -1;
+                if (p < to.s.length && p + kStep > to.s.low) {
+                    const int64_t page = page_of(a.c, to.b, p);
+                    if (page >= 0) {
+                        my_rows = page * a.c.page_stride + (int64_t)a.c.by_page.remainder(p) * a.c.slot_stride;
+                        my_scales = page * arg.s.page_stride + a.c.by_page.remainder(p);
+                    }
+                }
+            }
+            const int64_t rows = __shfl_sync(0xffffffffu, my_rows, to.block - pages_from);
+            const int64_t scales = __shfl_sync(0xffffffffu, my_scales, to.block - pages_from);
+            const int p0 = to.block * kBlock + warp * kStep;
+            const uint32_t dst = ring_u + stage * L::kStage;
+            constexpr int kRowsPer = 32 / L::kChunks;
+            const int chunk = lane % L::kChunks, row0 = lane / L::kChunks;
+            const uint8_t *k8 = reinterpret_cast<const uint8_t*>(a.c.k), *v8 = reinterpret_cast<const uint8_t*>(a.c.v);
+            const int g = head_of(to.g);
+            const int64_t first = rows + (int64_t)g * a.c.head_stride + row0 * a.c.slot_stride + chunk * 16;
+            const int64_t stride = kRowsPer * a.c.slot_stride;
+            const uint8_t *k_row = k8 + first, *v_row = v8 + first;
+            if (rows >= 0 && p0 >= to.s.low && p0 + kStep <= to.s.length) {
+#pragma unroll
+                for (int i = 0; i < kStep / kRowsPer; ++i) {
+                    const uint32_t at = dst + L::at(i * kRowsPer + row0, chunk);
+                    ptx::cp_async_16(at, k_row, 16u);
+                    ptx::cp_async_16(at + L::kHalfStage, v_row, 16u);
+                    k_row += stride;
+                    v_row += stride;
+                }
+            } else {
+                // places outside the sequence or before every row's window: zeros, nothing read
+#pragma unroll
+                for (int i = 0; i < kStep / kRowsPer; ++i) {
+                    const int row = i * kRowsPer + row0;
+                    const bool real = rows >= 0 && p0 + row >= to.s.low && p0 + row < to.s.length;
+                    const uint32_t at = dst + L::at(row, chunk);
+                    ptx::cp_async_16(at, real ? k_row : k8, real ? 16u : 0u);
+                    ptx::cp_async_16(at + L::kHalfStage, real ? v_row : v8, real ? 16u : 0u);
+                    k_row += stride;
+                    v_row += stride;
+                }
+            }
+            // scales of 4 places a lane, keys' and then values'; those of places that are not read, 0
+            if (lane < kStep / 2) {
+                const int p = p0 + (lane & 3) * 4;
+                const bool any = rows >= 0 && p + 4 > to.s.low && p < to.s.length;
+                const int64_t at = any ? scales + (int64_t)g * arg.s.head_stride + (lane & 3) * 4 : 0;
+                ptx::cp_async_16(dst + 2 * L::kHalfStage + lane * 16, (lane < 4 ? arg.s.k : arg.s.v) + at,
+                                 any ? 16u : 0u);
+            }
+            --to_load;
+            if (++to.block == to.end && to_load > 0) next_item(a, kRows, turns, to);
+        }
+        cp_async_commit();
+    };
+    auto load_step = [&](int stage) {
+        if constexpr (kHeld8) load_step8(stage);
+        else load_step16(stage);
     };
 
     // ------------------------------------------------------- computation --
@@ -345,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     float m[NT][2], l[NT][2];
     float scale[NT][2];  // of the columns' scores (8-bit cache)
     int low[NT][2], high[NT][2];  // places that this lane's columns (rows of q) see
+    int all_low = 0, all_high = 0;  // and those that all columns do (8-bit cache)
 
     auto start_item = [&]() {
 #pragma unroll
@@ -353,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             const bool real = r < at.s.count * ratio;
             const int64_t t = at.s.first + a.by_ratio.quotient(r);
             const uint16_t* q =
-                a.q + t * a.q_row_stride + (int64_t)(at.g * ratio + a.by_ratio.remainder(r)) * a.q_head_stride;
+                a.q + t * a.q_row_stride + (int64_t)(head_of(at.g) * ratio + a.by_ratio.remainder(r)) * a.q_head_stride;
             if constexpr (kHeld8) {
                 // Lane quad holds elements quad * D / 4 + 4 ks to + 3, of keys too: the order of a sum does not matter.
 #pragma unroll
@@ -390,9 +455,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[ks][n][i] = 0.0f;
         }
+        if constexpr (kHeld8) {
+            int lowest = 0, highest = 0x7FFFFFFF;  // (columns that are no rows: anything)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (n * 8 + quad * 2 + j < at.s.count * ratio) {
+                        lowest = max(lowest, low[n][j]);
+                        highest = min(highest, high[n][j]);
+                    }
+            all_low = __reduce_max_sync(0xffffffffu, lowest);
+            all_high = __reduce_min_sync(0xffffffffu, highest);
+        }
     };
 
-    auto compute_step = [&](int stage) {
+    // `edge`: not all of the places are seen by all columns
+    auto compute_step = [&](int stage, auto edge) {
+        constexpr bool kEdge = decltype(edge)::value;
         const int p0 = at.block * kBlock + warp * kStep;
         if (p0 >= at.s.length || p0 + kStep <= at.s.low) return;
         const uint32_t kb = ring_u + stage * L::kStage;
@@ -403,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[0][n][i] = s[1][n][i] = 0.0f;
         // The scales of the lane's places, grp and grp + 8.
-        float key_scale[2], value_scale[2], value_log2[2];
+        [[maybe_unused]] float key_scale[2], value_scale[2], value_log2[2];
         if constexpr (kHeld8) {
             const float* sc = reinterpret_cast<const float*>(ring + stage * L::kStage + 2 * L::kHalfStage);
 #pragma unroll
@@ -446,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                 float v = s[0][n][i] + s[1][n][i];
                 if constexpr (kHeld8) v = v * key_scale[i >> 1] * scale[n][i & 1];
                 else v *= a.scale_log2;
-                if (p < low[n][i & 1] || p >= high[n][i & 1]) v = -INFINITY;
+                if (kEdge && (p < low[n][i & 1] || p >= high[n][i & 1])) v = -INFINITY;
                 s[0][n][i] = v;
-                if constexpr (kHeld8) s[1][n][i] = v == -INFINITY ? v : v + value_log2[i >> 1];
+                if constexpr (kHeld8) s[1][n][i] = kEdge && v == -INFINITY ? v : v + value_log2[i >> 1];
                 rise = rise || s[kHeld8][n][i] > m[n][i & 1];
             }
         if (__any_sync(0xffffffffu, rise)) {
@@ -484,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             if constexpr (kHeld8) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)  // (a place that is not seen may have any scale)
-                    p[i] = s[0][n][i] == -INFINITY ? 0.0f : p[i] * (value_scale[i >> 1] * kWeightUp);
+                    p[i] = kEdge && s[0][n][i] == -INFINITY ? 0.0f : p[i] * (value_scale[i >> 1] * kWeightUp);
             }
             pf[n][0] = transpose_8x8(M::pack(p[0], p[1]));
             pf[n][1] = transpose_8x8(M::pack(p[2], p[3]));
@@ -521,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     // here) and writes the result, or the part for the last of its thread blocks to join.
     float* join = reinterpret_cast<float*>(smem + kWarps * kRingBytes);
     auto write_row = [&](int r, int d, float (&acc)[8], float top, float sum) {
-        const int64_t row = (int64_t)(at.s.first + a.by_ratio.quotient(r)) * a.heads + at.g * ratio +
+        if (kHeld8 && at.g * lanes + head0 >= a.c.kv_heads) return;  // (a head too many in the last turn)
+        const int64_t row = (int64_t)(at.s.first + a.by_ratio.quotient(r)) * a.heads + head_of(at.g) * ratio +
                             a.by_ratio.remainder(r);
         const float inv = sum > 0.0f || sum != sum ? (kHeld8 ? 1.0f / kWeightUp : 1.0f) / sum : 0.0f;
         uint4 w;
@@ -533,8 +614,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     };
     auto finish_item = [&](int64_t item_begin, int64_t item_end) {
-        const int c0 = shares.owner(item_begin, blockIdx.x), c1 = shares.owner(item_end - 1, blockIdx.x);
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x ? 1 : 0);
+        const int c0 = shares.owner(item_begin, run), c1 = shares.owner(item_end - 1, run);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (c0 == (int)run ? 1 : 0);
+        int* counter = arg.counters + c0 * lanes + head0;
         const int rows = at.s.count * ratio;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -599,9 +681,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         __threadfence();
         __syncthreads();
         if (tid == 0) {
-            const int done = ptx::atom_add_acq_rel_gpu(arg.counters + c0, 1);
+            const int done = ptx::atom_add_acq_rel_gpu(counter, 1);
             s_last = done == c1 - c0;
-            if (s_last) arg.counters[c0] = 0;
+            if (s_last) *counter = 0;
         }
         __syncthreads();
         if (!s_last) return;
@@ -618,7 +700,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
             for (int p0 = c0; p0 <= c1; p0 += 64) {
                 const int n = min(64, c1 + 1 - p0);
-                auto slot_of = [&](int k) { return (int64_t)(2 * (p0 + k) + (p0 + k == c0)); };
+                auto slot_of = [&](int k) {
+                    return (int64_t)(2 * ((p0 + k) * lanes + head0) + (p0 + k == c0));
+                };
                 __syncthreads();
                 for (int k = tid; k < n * rows; k += kThreads) {
                     const int part = k / rows, row = k - part * rows;
@@ -662,33 +746,55 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             cp_async_wait<L::kStages - 2>();
             __syncwarp();
             load_step(stage == 0 ? L::kStages - 1 : stage - 1);
-            compute_step(stage);
+            if constexpr (kHeld8) {
+                const int p0 = at.block * kBlock + warp * kStep;
+                if (p0 >= all_low && p0 + kStep <= all_high) compute_step(stage, std::false_type{});
+                else compute_step(stage, std::true_type{});
+            } else {
+                compute_step(stage, std::true_type{});
+            }
             stage = stage + 1 == L::kStages ? 0 : stage + 1;
         }
         finish_item(item_begin, item_end);
         if (unit == run_end) break;
-        next_item(a, kRows, at);
+        next_item(a, kRows, turns, at);
     }
 }
 
 // ------------------------------------------------------------------- host --
 
+inline int step_blocks(const DeviceInfo& dev) { return dev.sms * kBlocksPerSm; }
+
 template <class E, class H, int D, int NT>
-w4a16_status launch(const DeviceInfo& dev, const StepArgs& arg, int blocks, cudaStream_t st) {
+w4a16_status launch(const DeviceInfo& dev, StepArgs arg, cudaStream_t st) {
+    using L = Layout<H, D>;
+    const int blocks = step_blocks(dev);
+    if constexpr (L::kHeld8) {
+        // As many heads side by side as there are, or in as few turns as leave at most 1 thread block in 32 idle.
+        const int heads = arg.a.c.kv_heads;
+        double best = 0.0;
+        for (int turns = 1; turns <= heads && best < 0.97; ++turns) {
+            const int lanes = (heads + turns - 1) / turns;
+            const double busy = (double)(blocks / lanes) * heads / turns / blocks;
+            if (busy <= best) continue;
+            best = busy;
+            arg.lanes = lanes;
+            arg.turns = turns;
+        }
+    }
     static PerDeviceOnce once;
     const cudaError_t e = once.run(dev.device, [] {
         return cudaFuncSetAttribute(step_kernel<E, H, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    Layout<H, D>::kSmem);
+                                    L::kSmem);
     });
     if (e != cudaSuccess) return cuda_status(e, "paged_attention: cudaFuncSetAttribute");
     return launch_overlapped("paged_attention", step_kernel<E, H, D, NT>, dim3((unsigned)blocks), kThreads,
-                             Layout<H, D>::kSmem, st, arg);
+                             L::kSmem, st, arg);
 }
 
-inline int step_blocks(const DeviceInfo& dev) { return dev.sms * kBlocksPerSm; }
-
 // The arguments, with the workspace laid out.
-inline StepArgs step_args(const AttentionArgs& a, const ScaleArgs& s, int blocks, void* workspace) {
+inline StepArgs step_args(const DeviceInfo& dev, const AttentionArgs& a, const ScaleArgs& s, void* workspace) {
+    const int blocks = step_blocks(dev);
     StepArgs arg{};
     arg.a = a;
     arg.s = s;
@@ -704,12 +810,11 @@ inline StepArgs step_args(const AttentionArgs& a, const ScaleArgs& s, int blocks
 template <class E, class H>
 w4a16_status launch_rows(const DeviceInfo& dev, const AttentionArgs& a, const ScaleArgs& s, int max_rows,
                          void* workspace, cudaStream_t st) {
-    const int blocks = step_blocks(dev);
-    const StepArgs arg = step_args(a, s, blocks, workspace);
+    const StepArgs arg = step_args(dev, a, s, workspace);
     const bool two = max_rows > 8;
     if (a.c.head_dim == 128)
-        return two ? launch<E, H, 128, 2>(dev, arg, blocks, st) : launch<E, H, 128, 1>(dev, arg, blocks, st);
-    return two ? launch<E, H, 64, 2>(dev, arg, blocks, st) : launch<E, H, 64, 1>(dev, arg, blocks, st);
+        return two ? launch<E, H, 128, 2>(dev, arg, st) : launch<E, H, 128, 1>(dev, arg, st);
+    return two ? launch<E, H, 64, 2>(dev, arg, st) : launch<E, H, 64, 1>(dev, arg, st);
 }
 
 }  // namespace
