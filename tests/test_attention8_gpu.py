@@ -431,3 +431,26 @@ def test_wait_times_out_and_next_call_is_correct(hooks, cuda_device, lens, limit
     assert call() == 0
     assert lib.w4a16_device_status(st) == 0
     b.check(out)
+
+
+# ------------------------------------------------------------- many cached heads --
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("H,G,q_len", [(12, 12, 1), (100, 100, 2), (613, 613, 1), (330, 330, 1), (26, 13, 3)])
+def test_head_counts_that_do_not_divide_the_thread_blocks(w4, cuda_device, H, G, q_len, form):  # noqa: F811
+    """Single tokens work on many cached heads side by side, in several turns where there are more of them than
+    thread blocks or a rest would be idle: every head of every sequence, the last turn's missing ones among them."""
+    b = Batch8(cuda_device, "fp16", form, H, G, 64, 16, [(q_len, 200), (q_len, 17), (q_len, 130)], seed=H)
+    b.check(*b.attend(w4, return_lse=True))
+
+
+def test_caches_that_were_never_appended_to(w4, cuda_device):  # noqa: F811
+    """Scales of 0, as of a cache made with torch.zeros, count as rows of zeros: among others, and alone."""
+    for q_len in (1, 40):
+        b = Batch8(cuda_device, "fp16", "int8", 10, 2, 64, 16, [(q_len, 300)], seed=30)
+        for first, last in ((64, 200), (0, 300)):
+            for p in range(first, last):
+                at = b.table[0][p // 16], slice(None), p % 16
+                b.k_scale[at] = 0
+                b.v_scale[at] = 0
+            b.check(*b.attend(w4, return_lse=True))

@@ -94,13 +94,20 @@ struct HeldE4m3 {
     }
 };
 
-// Scale of a row and what its elements are multiplied by, from the bit pattern of its largest |x| (as
-// integers, those of NaN and infinity are the largest). NaN where the row holds either.
+// The larger of two, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Scale of a row and what its elements are multiplied by, from its largest |x| (NaN where one is). NaN
+// where the row holds an infinity or a NaN.
 template <class H>
-__device__ __forceinline__ float scale_of(uint32_t top_bits, float& inv) {
-    const float top = __uint_as_float(max(top_bits, __float_as_uint(kLeastTop)));
-    inv = __fdiv_rn(H::kMost, top);
-    return top_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(top, H::kMost);
+__device__ __forceinline__ float scale_of(float top, float& inv) {
+    const float held = fmaxf(top, kLeastTop);
+    inv = __fdiv_rn(H::kMost, held);
+    return top < INFINITY ? __fdiv_rn(held, H::kMost) : __uint_as_float(0x7FC00000u);
 }
 
 // ------------------------------------------------------------------ host --

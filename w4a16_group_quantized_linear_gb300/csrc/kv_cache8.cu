@@ -14,6 +14,20 @@ namespace w4a16 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 3;
+constexpr int kMostHeads = 8;  // of a token, to a thread
+
+// Which heads a thread takes: `lanes` neighbours (a power of two) share `each` heads of a token. A thread block has the
+// same heads (blockIdx.y) of neighbouring tokens: queries, keys and values take different paths, and warps
+// that hold all three walk them all (9764 tokens of 56 heads: 84 us, and 63 so).
+struct Split {
+    int32_t shift, each;  // lanes = 1 << shift
+    __device__ __forceinline__ int lane() const { return threadIdx.x & ((1 << shift) - 1); }
+    __device__ __forceinline__ int64_t token() const {
+        return (int64_t)blockIdx.x * (kThreads >> shift) + (threadIdx.x >> shift);
+    }
+    __device__ __forceinline__ int head() const { return blockIdx.y * each; }
+};
 
 // The 16 elements of a thread, as 32-bit numbers.
 template <class E>
@@ -32,26 +46,24 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]), E::pack(x[6], x[7]));
 }
 
-// x / sqrt(mean(x^2) + eps) * w over the `lanes` lanes of a head (w: the thread's two pieces).
-__device__ __forceinline__ void normalise(float (&x)[16], int lanes, int head_dim, float eps, const float* w0,
-                                          const float* w1) {
+// 1 / sqrt(mean(x^2) + eps) over the `lanes` lanes of a head; all lanes of the warp.
+__device__ __forceinline__ float inverse_rms(const float (&x)[16], int lanes, float mean, float eps) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum += x[i] * x[i];
     for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float r = rsqrtf(sum / (float)head_dim + eps);
+    return rsqrtf(sum * mean + eps);
+}
+
+// The norm's weights of a thread's two pieces.
+__device__ __forceinline__ void load_weights(float (&w)[16], const float* w0, const float* w1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(w0) + i);
-        const float4 b = __ldg(reinterpret_cast<const float4*>(w1) + i);
-        x[4 * i] *= r * a.x;
-        x[4 * i + 1] *= r * a.y;
-        x[4 * i + 2] *= r * a.z;
-        x[4 * i + 3] *= r * a.w;
-        x[8 + 4 * i] *= r * b.x;
-        x[8 + 4 * i + 1] *= r * b.y;
-        x[8 + 4 * i + 2] *= r * b.z;
-        x[8 + 4 * i + 3] *= r * b.w;
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(i < 2 ? w0 : w1) + (i & 1));
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
     }
 }
 
@@ -82,48 +94,55 @@ struct NormArgs {
     uint16_t* out;
     int64_t out_row_stride, out_head_stride;
     int64_t T;
-    int32_t heads, head_dim, lanes;  // lanes: of a head, a power of two
+    int32_t heads, head_dim;
+    Split split;
     const float* weight;
-    float eps;
+    float eps, mean;  // mean: 1 / head_dim
     unsigned int* err;
     RotaryArgs r;
 };
 
-template <class E, int HPT>
-__global__ void __launch_bounds__(kThreads) rope_norm_kernel(const __grid_constant__ NormArgs a) {
+template <class E>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_norm_kernel(const __grid_constant__ NormArgs a) {
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    const int groups = (a.heads + HPT - 1) / HPT;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int chunk = (int)(i % a.lanes);
-    const int group = (int)(i / a.lanes % groups);
-    const int64_t t = i / a.lanes / groups;
+    const int chunk = a.split.lane();
+    const int64_t t = a.split.token();
     // the lanes of a head, and those past its end, stay together for the sums
     const bool mine = t < a.T && chunk < a.head_dim / 16;
     const Pieces p = pieces_of(a.r, mine ? chunk : 0);
-    uint4 u[HPT], w[HPT];
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = group + k * groups;
-        u[k] = w[k] = make_uint4(0, 0, 0, 0);
-        if (!mine || h >= a.heads) continue;
-        const uint16_t* src = a.x + t * a.x_row_stride + h * a.x_head_stride;
-        u[k] = *reinterpret_cast<const uint4*>(src + p.first);
-        w[k] = *reinterpret_cast<const uint4*>(src + p.second);
-    }
-    float c[8], s[8];
+    const int first = a.split.head(), end = min(first + a.split.each, a.heads);
+    const int real_end = mine ? end : first;
+    const uint16_t* src = a.x + t * a.x_row_stride;
+    auto load = [&](int h, uint4& u, uint4& w) {
+        u = w = make_uint4(0, 0, 0, 0);
+        if (h >= real_end) return;
+        u = *reinterpret_cast<const uint4*>(src + h * a.x_head_stride + p.first);
+        w = *reinterpret_cast<const uint4*>(src + h * a.x_head_stride + p.second);
+    };
+    uint4 u0, w0, u1, w1;
+    load(first, u0, w0);
+    load(first + 1, u1, w1);
+    float c[8], s[8], weight[16];
     const bool rotate = mine && p.pair >= 0 && angles(a.r, a.T, t, 0, p.pair, a.err, c, s);
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = group + k * groups;
+    load_weights(weight, a.weight + p.first, a.weight + p.second);
+    uint16_t* dst = a.out + t * a.out_row_stride;
+    auto head = [&](int h, uint4& u, uint4& w) {
         float x[16];
-        unpack16<E>(u[k], w[k], x);
-        normalise(x, a.lanes, a.head_dim, a.eps, a.weight + p.first, a.weight + p.second);
+        unpack16<E>(u, w, x);
+        load(h + 2, u, w);
+        const float r = inverse_rms(x, 1 << a.split.shift, a.mean, a.eps);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= r * weight[j];
         if (rotate) turn(x, a.r.interleaved, c, s);
-        if (!mine || h >= a.heads) continue;
-        uint16_t* dst = a.out + t * a.out_row_stride + h * a.out_head_stride;
-        *reinterpret_cast<uint4*>(dst + p.first) = pack8<E>(x);
-        *reinterpret_cast<uint4*>(dst + p.second) = pack8<E>(x + 8);
+        if (h >= real_end) return;
+        *reinterpret_cast<uint4*>(dst + h * a.out_head_stride + p.first) = pack8<E>(x);
+        *reinterpret_cast<uint4*>(dst + h * a.out_head_stride + p.second) = pack8<E>(x + 8);
+    };
+#pragma unroll 1
+    for (int h = first; h < end; h += 2) {
+        head(h, u0, w0);
+        if (h + 1 < end) head(h + 1, u1, w1);
     }
 }
 
@@ -136,39 +155,40 @@ struct AppendArgs {
     int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
     uint16_t* q_out;  // [T, heads, head_dim]
     int32_t heads;    // 0: no q
+    Split split;
     const float *q_norm, *k_norm;  // nullptr: left as they are
-    float eps;
+    float eps, mean;               // mean: 1 / head_dim
     RotaryArgs r;
 };
 
 // The heads of a token in one row: queries, then keys, then values.
-template <class E, class H, int HPT>
-__global__ void __launch_bounds__(kThreads) append_ex_kernel(const __grid_constant__ AppendArgs a) {
+template <class E, class H>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_ex_kernel(const __grid_constant__ AppendArgs a) {
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    if (blockIdx.x == 0) check_offsets(a.c);
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a.c);
     const int D = a.c.head_dim, G = a.c.kv_heads;
-    const int chunks = D / 16;  // 4 or 8: a head's lanes are in one warp
+    const int chunks = D / 16;  // 4 or 8
     const int all = a.heads + 2 * G;
-    const int groups = (all + HPT - 1) / HPT;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int chunk = (int)(i % chunks);
-    const int group = (int)(i / chunks % groups);
-    const bool real = i / chunks / groups < a.c.T;  // lanes without a token stay for the sums
-    const int64_t t = real ? i / chunks / groups : a.c.T - 1;
+    const int chunk = a.split.lane();
+    int64_t t = a.split.token();
+    const bool real = t < a.c.T;  // lanes without a token stay for the sums
+    if (!real) t = a.c.T - 1;
     const Pieces p = pieces_of(a.r, chunk);
-    uint4 u[HPT], w[HPT];
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = group + k * groups;
-        u[k] = w[k] = make_uint4(0, 0, 0, 0);
-        if (!real || h >= all) continue;
+    const int begin = a.split.head(), end = min(begin + a.split.each, all);
+    const int real_end = real ? end : begin;
+    auto load = [&](int h, uint4& u, uint4& w) {
+        u = w = make_uint4(0, 0, 0, 0);
+        if (h >= real_end) return;
         const uint16_t* src = h < a.heads ? a.q + t * a.q_row_stride + h * a.q_head_stride
                               : h < a.heads + G ? a.k + t * a.k_row_stride + (h - a.heads) * a.k_head_stride
                                                 : a.v + t * a.v_row_stride + (h - a.heads - G) * a.v_head_stride;
-        u[k] = *reinterpret_cast<const uint4*>(src + p.first);
-        w[k] = *reinterpret_cast<const uint4*>(src + p.second);
-    }
+        u = *reinterpret_cast<const uint4*>(src + p.first);
+        w = *reinterpret_cast<const uint4*>(src + p.second);
+    };
+    uint4 u0, w0, u1, w1;
+    load(begin, u0, w0);
+    load(begin + 1, u1, w1);
     int first, count;
     const int b = sequence_of(a.c, t, first, count);
     // place in the sequence; negative where the sequence is shorter than its new tokens, and where its length
@@ -184,52 +204,62 @@ __global__ void __launch_bounds__(kThreads) append_ex_kernel(const __grid_consta
     if (place >= 0) page = page_of(a.c, b, place);
     const int in_page = place < 0 ? 0 : a.c.by_page.remainder(place);
     const int64_t slot = page * a.c.page_stride + in_page * a.c.slot_stride;
+    const int64_t scale_slot = page * a.s.page_stride + in_page;
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = group + k * groups;
+    float weight[16];
+    const float* held = nullptr;  // whose weights these are
+    auto head = [&](int h, uint4& u, uint4& w) {
         const bool query = h < a.heads, value = h >= a.heads + G;
         const int g = value ? h - a.heads - G : h - a.heads;
         float x[16];
-        unpack16<E>(u[k], w[k], x);
-        const float* norm = query ? a.q_norm : value ? nullptr : a.k_norm;
-        if (__any_sync(0xffffffffu, norm != nullptr)) {
-            float y[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = x[j];
-            const float* any = a.q_norm ? a.q_norm : a.k_norm;
-            normalise(y, chunks, D, a.eps, (norm ? norm : any) + p.first, (norm ? norm : any) + p.second);
+        unpack16<E>(u, w, x);
+        load(h + 2, u, w);
+        if (a.q_norm || a.k_norm) {
+            const float r = inverse_rms(x, chunks, a.mean, a.eps);
+            const float* norm = query ? a.q_norm : value ? nullptr : a.k_norm;
             if (norm) {
+                if (norm != held) load_weights(weight, norm + p.first, norm + p.second);
+                held = norm;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = y[j];
+                for (int j = 0; j < 16; ++j) x[j] *= r * weight[j];
             }
         }
         if (rotate && !value) turn(x, a.r.interleaved, c, s);
+        float top = 0.0f;
         if constexpr (H::kFormat != 0) {
-            uint32_t top = 0;
+            if (__any_sync(0xffffffffu, !query)) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-            for (int o = 1; o < chunks; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (!query && h < all && page >= 0 && real) {
+                for (int j = 0; j < 16; ++j) top = max_nan(top, fabsf(x[j]));
+                for (int o = 1; o < chunks; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+        }
+        if (h >= real_end) return;
+        if (query) {
+            uint16_t* dst = a.q_out + (t * a.heads + h) * D;
+            *reinterpret_cast<uint4*>(dst + p.first) = pack8<E>(x);
+            *reinterpret_cast<uint4*>(dst + p.second) = pack8<E>(x + 8);
+        } else if (page >= 0) {
+            if constexpr (H::kFormat != 0) {
                 float inv;
                 const float scale = scale_of<H>(top, inv);
                 uint8_t* dst = reinterpret_cast<uint8_t*>(value ? a.c.v : a.c.k) + slot + g * a.c.head_stride;
                 *reinterpret_cast<uint2*>(dst + p.first) = make_uint2(H::encode4(x, inv), H::encode4(x + 4, inv));
                 *reinterpret_cast<uint2*>(dst + p.second) =
                     make_uint2(H::encode4(x + 8, inv), H::encode4(x + 12, inv));
-                if (chunk == 0)
-                    (value ? a.s.v : a.s.k)[page * a.s.page_stride + g * a.s.head_stride + in_page] = scale;
+                if (chunk == 0) (value ? a.s.v : a.s.k)[scale_slot + g * a.s.head_stride] = scale;
+            } else {
+                uint16_t* dst = (value ? a.c.v : a.c.k) + slot + g * a.c.head_stride;
+                *reinterpret_cast<uint4*>(dst + p.first) = pack8<E>(x);
+                *reinterpret_cast<uint4*>(dst + p.second) = pack8<E>(x + 8);
             }
-        } else if (!query && h < all && page >= 0 && real) {
-            uint16_t* dst = (value ? a.c.v : a.c.k) + slot + g * a.c.head_stride;
-            *reinterpret_cast<uint4*>(dst + p.first) = pack8<E>(x);
-            *reinterpret_cast<uint4*>(dst + p.second) = pack8<E>(x + 8);
         }
-        if (query && real) {
-            uint16_t* dst = a.q_out + (t * a.heads + h) * D;
-            *reinterpret_cast<uint4*>(dst + p.first) = pack8<E>(x);
-            *reinterpret_cast<uint4*>(dst + p.second) = pack8<E>(x + 8);
-        }
+    };
+#pragma unroll 1
+    for (int h = begin; h < end; h += 2) {
+        head(h, u0, w0);
+        __syncwarp();
+        if (h + 1 < end) head(h + 1, u1, w1);
+        __syncwarp();
     }
 }
 
@@ -238,19 +268,23 @@ __global__ void __launch_bounds__(kThreads) append_ex_kernel(const __grid_consta
 struct ReadArgs {
     CacheArgs c;
     ScaleArgs s;
-    uint16_t *k, *v;  // [T, kv_heads, head_dim]
+    int32_t shift;      // 1 << shift lanes to a head
+    FastDiv by_heads;   // of T * kv_heads,
+    int32_t few;        // if they are fewer than 2^31
+    uint16_t *k, *v;    // [T, kv_heads, head_dim]
 };
 
-// 16 elements of k and of v a thread.
+// 16 elements of k and of v a thread, the heads of a token side by side (their rows are, in the result).
 template <class E, class H>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     if (blockIdx.x == 0) check_offsets(a.c);
-    const int D = a.c.head_dim, G = a.c.kv_heads, chunks = D / 16;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int chunk = (int)(i % chunks), g = (int)(i / chunks % G);
-    const int64_t t = i / chunks / G;
+    const int D = a.c.head_dim, G = a.c.kv_heads;
+    const int chunk = threadIdx.x & ((1 << a.shift) - 1);
+    const int64_t row = (int64_t)blockIdx.x * (kThreads >> a.shift) + (threadIdx.x >> a.shift);
+    const int64_t t = a.few ? a.by_heads.quotient((int)row) : row / G;  // (a division in 64 bits: 60 instructions)
+    const int g = (int)(row - t * G);
     if (t >= a.c.T) return;
     int first, count;
     const int b = sequence_of(a.c, t, first, count);
@@ -291,33 +325,39 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 
 // ------------------------------------------------------------------- host --
 
-w4a16_status blocks_for(int64_t threads, unsigned& blocks) {
-    const int64_t n = (threads + kThreads - 1) / kThreads;
+// The split of T tokens' heads of `chunks` 16-element pieces, and its thread blocks: as many heads to a thread as leave
+// every SM two rounds of blocks (what depends on the token is worked out once a thread), `most` at most.
+w4a16_status split_for(const DeviceInfo& dev, int64_t T, int64_t heads, int chunks, int most, Split& s,
+                       dim3& grid) {
+    s.shift = 0;
+    while ((1 << s.shift) < chunks) ++s.shift;
+    const int64_t per = kThreads >> s.shift, n = (T + per - 1) / per;
+    int64_t each = n * heads / (dev.sms * kBlocksPerSm * 2);
+    each = each > most ? most : each;
+    const int64_t least = (heads + 65534) / 65535;  // what a grid's second dimension takes
+    each = each < least ? least : each;
+    int64_t groups = (heads + each - 1) / each;
+    each = (heads + groups - 1) / groups;
+    groups = (heads + each - 1) / each;
     if (n > 0x7fffffffLL) return W4A16_ERR_UNSUPPORTED;
-    blocks = (unsigned)n;
+    s.each = (int)each;
+    grid = dim3((unsigned)n, (unsigned)groups);
     return W4A16_OK;
 }
 
-// Four heads to a thread once that still leaves every SM several blocks.
-bool wide(const DeviceInfo& dev, int64_t T, int64_t heads, int lanes) {
-    return T * ((heads + 3) / 4) * lanes >= (int64_t)dev.sms * 4 * kThreads;
-}
-
 template <class E>
-w4a16_status rope_norm(bool four, unsigned blocks, const NormArgs& a, cudaStream_t st) {
-    return launch_overlapped("rope", four ? rope_norm_kernel<E, 4> : rope_norm_kernel<E, 1>, dim3(blocks), kThreads, 0,
-                             st, a);
+w4a16_status rope_norm(const dim3& grid, const NormArgs& a, cudaStream_t st) {
+    return launch_overlapped("rope", rope_norm_kernel<E>, grid, kThreads, 0, st, a);
 }
 
 template <class E, class H>
-w4a16_status append(bool four, unsigned blocks, const AppendArgs& a, cudaStream_t st) {
-    return launch_overlapped("kv_append", four ? append_ex_kernel<E, H, 4> : append_ex_kernel<E, H, 1>, dim3(blocks),
-                             kThreads, 0, st, a);
+w4a16_status append(const dim3& grid, const AppendArgs& a, cudaStream_t st) {
+    return launch_overlapped("kv_append", append_ex_kernel<E, H>, grid, kThreads, 0, st, a);
 }
 
 template <class E, class H>
-w4a16_status read(unsigned blocks, const ReadArgs& a, cudaStream_t st) {
-    return launch_overlapped("kv_read", read_kernel<E, H>, dim3(blocks), kThreads, 0, st, a);
+w4a16_status read(const dim3& grid, const ReadArgs& a, cudaStream_t st) {
+    return launch_overlapped("kv_read", read_kernel<E, H>, grid, kThreads, 0, st, a);
 }
 
 }  // namespace
@@ -336,17 +376,15 @@ w4a16_status rope_norm_launch(const DeviceInfo& dev, int dtype, const uint16_t* 
     a.T = T;
     a.heads = heads;
     a.head_dim = head_dim;
-    a.lanes = 1;
-    while (a.lanes * 16 < head_dim) a.lanes *= 2;
     a.weight = weight;
     a.eps = eps;
+    a.mean = 1.0f / (float)head_dim;
     a.err = dev.error_word;
     fill(a.r, rotary);
-    const bool four = wide(dev, T, heads, a.lanes);
-    unsigned blocks;
-    const w4a16_status s = blocks_for(T * (four ? (heads + 3) / 4 : heads) * a.lanes, blocks);
+    dim3 grid;
+    const w4a16_status s = split_for(dev, T, heads, head_dim / 16, kMostHeads, a.split, grid);
     if (s != W4A16_OK) return s;
-    return dtype == W4A16_DTYPE_F16 ? rope_norm<Fp16>(four, blocks, a, st) : rope_norm<Bf16>(four, blocks, a, st);
+    return dtype == W4A16_DTYPE_F16 ? rope_norm<Fp16>(grid, a, st) : rope_norm<Bf16>(grid, a, st);
 }
 
 w4a16_status append_ex_launch(const DeviceInfo& dev, int dtype, int format, const CacheArgs& c, const ScaleArgs& scales,
@@ -371,39 +409,41 @@ w4a16_status append_ex_launch(const DeviceInfo& dev, int dtype, int format, cons
     a.q_norm = norms && a.heads ? norms->q : nullptr;
     a.k_norm = norms ? norms->k : nullptr;
     a.eps = norms ? norms->eps : 0.0f;
+    a.mean = 1.0f / (float)c.head_dim;
     fill(a.r, rotary);
-    const int64_t all = a.heads + 2 * (int64_t)c.kv_heads;
-    const int lanes = c.head_dim / 16;
-    const bool four = wide(dev, c.T, all, lanes);
-    unsigned blocks;
-    const w4a16_status s = blocks_for(c.T * (four ? (all + 3) / 4 : all) * lanes, blocks);
+    dim3 grid;
+    const w4a16_status s = split_for(dev, c.T, a.heads + 2 * (int64_t)c.kv_heads, c.head_dim / 16, kMostHeads,
+                                     a.split, grid);
     if (s != W4A16_OK) return s;
     const bool f16 = dtype == W4A16_DTYPE_F16;
     switch (format) {
         case W4A16_CACHE_INT8:
-            return f16 ? append<Fp16, HeldInt8>(four, blocks, a, st) : append<Bf16, HeldInt8>(four, blocks, a, st);
+            return f16 ? append<Fp16, HeldInt8>(grid, a, st) : append<Bf16, HeldInt8>(grid, a, st);
         case W4A16_CACHE_E4M3:
-            return f16 ? append<Fp16, HeldE4m3>(four, blocks, a, st) : append<Bf16, HeldE4m3>(four, blocks, a, st);
+            return f16 ? append<Fp16, HeldE4m3>(grid, a, st) : append<Bf16, HeldE4m3>(grid, a, st);
         default:
-            return f16 ? append<Fp16, Held16>(four, blocks, a, st) : append<Bf16, Held16>(four, blocks, a, st);
+            return f16 ? append<Fp16, Held16>(grid, a, st) : append<Bf16, Held16>(grid, a, st);
     }
 }
 
-w4a16_status read_launch(const DeviceInfo& dev, int dtype, int format, const CacheArgs& c, const ScaleArgs& scales,
+w4a16_status read_launch(const DeviceInfo&, int dtype, int format, const CacheArgs& c, const ScaleArgs& scales,
                          uint16_t* k, uint16_t* v, cudaStream_t st) {
     ReadArgs a{};
     a.c = c;
     a.s = scales;
     a.k = k;
     a.v = v;
-    unsigned blocks;
-    const w4a16_status s = blocks_for(c.T * c.kv_heads * (c.head_dim / 16), blocks);
-    if (s != W4A16_OK) return s;
+    a.shift = c.head_dim == 128 ? 3 : 2;
+    const int64_t per = kThreads >> a.shift, blocks = (c.T * c.kv_heads + per - 1) / per;
+    if (blocks > 0x7fffffffLL) return W4A16_ERR_UNSUPPORTED;
+    a.by_heads = fast_div(c.kv_heads);
+    a.few = blocks * per < 0x7fffffffLL;
+    const dim3 grid((unsigned)blocks);
     const bool f16 = dtype == W4A16_DTYPE_F16;
     switch (format) {
-        case W4A16_CACHE_INT8: return f16 ? read<Fp16, HeldInt8>(blocks, a, st) : read<Bf16, HeldInt8>(blocks, a, st);
-        case W4A16_CACHE_E4M3: return f16 ? read<Fp16, HeldE4m3>(blocks, a, st) : read<Bf16, HeldE4m3>(blocks, a, st);
-        default: return f16 ? read<Fp16, Held16>(blocks, a, st) : read<Bf16, Held16>(blocks, a, st);
+        case W4A16_CACHE_INT8: return f16 ? read<Fp16, HeldInt8>(grid, a, st) : read<Bf16, HeldInt8>(grid, a, st);
+        case W4A16_CACHE_E4M3: return f16 ? read<Fp16, HeldE4m3>(grid, a, st) : read<Bf16, HeldE4m3>(grid, a, st);
+        default: return f16 ? read<Fp16, Held16>(grid, a, st) : read<Bf16, Held16>(grid, a, st);
     }
 }
 
