@@ -7,9 +7,10 @@ CUDA graph.
 
 Weights are random int4; the script checks itself: what the growing cache gives
 for the last token of each sequence must be what one chunk over the whole
-sequence gives.
+sequence gives. With an 8-bit cache the heads of queries and keys are divided by
+their norms too, in the same launch that rotates and stores them.
 
-    python examples/decoder_attention.py [--steps 8] [--hidden 1024]
+    python examples/decoder_attention.py [--steps 8] [--hidden 1024] [--cache 16 | int8 | e4m3]
 """
 from __future__ import annotations
 
@@ -24,10 +25,13 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import w4a16_group_quantized_linear_gb300 as w4  # noqa: E402
 
 
+CACHES = {"16": torch.float16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
 class AttentionLayer:
     """Quantized projections, a paged cache and the pages of each sequence."""
 
-    def __init__(self, hidden, heads, kv_heads, head_dim, sequences, places, page=16, seed=0):
+    def __init__(self, hidden, heads, kv_heads, head_dim, sequences, places, page=16, seed=0, cache="16"):
         dev = "cuda"
         gen = torch.Generator(device=dev).manual_seed(seed)
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
@@ -37,7 +41,13 @@ class AttentionLayer:
         self.table = w4.rope_table(places, head_dim, device=dev)
         per = -(-places // page)
         shape = (sequences * per, page, kv_heads, head_dim)
-        self.k, self.v = (torch.empty(shape, dtype=torch.float16, device=dev) for _ in range(2))
+        self.k, self.v = (torch.empty(shape, dtype=CACHES[cache], device=dev) for _ in range(2))
+        self.scales, self.norms = {}, {}
+        if cache != "16":
+            shape = (sequences * per, kv_heads, page)
+            self.scales = {name: torch.empty(shape, device=dev) for name in ("k_scale", "v_scale")}
+            self.norms = {name: 1 + 0.1 * torch.randn(head_dim, generator=gen, device=dev)
+                          for name in ("q_norm", "k_norm")}
         # any assignment of pages will do
         self.pages = torch.randperm(sequences * per, generator=gen, device=dev).to(torch.int32).view(sequences, per)
 
@@ -46,8 +56,9 @@ class AttentionLayer:
         H, G, D = self.heads, self.kv_heads, self.head_dim
         qkv = w4.linear(x, *self.w_qkv).unflatten(1, (H + 2 * G, D))
         batch = (self.k, self.v, self.pages[:kv_lens.shape[0]], q_offsets, kv_lens)
-        q = w4.kv_append(qkv[:, H:H + G], qkv[:, H + G:], *batch, q=qkv[:, :H], table=self.table)
-        y = w4.paged_attention(q, *batch, max_q_len)
+        q = w4.kv_append(qkv[:, H:H + G], qkv[:, H + G:], *batch, q=qkv[:, :H], table=self.table, **self.scales,
+                         **self.norms)
+        y = w4.paged_attention(q, *batch, max_q_len, **self.scales)
         return w4.linear(y.flatten(1), *self.w_out)
 
 
@@ -59,12 +70,14 @@ def _offsets(lens):
     return _ints([sum(lens[:i]) for i in range(len(lens) + 1)])
 
 
-def run(prompts=(37, 300, 5), steps=8, hidden=1024, heads=16, kv_heads=4, head_dim=64, chunk=128, seed=0):
+def run(prompts=(37, 300, 5), steps=8, hidden=1024, heads=16, kv_heads=4, head_dim=64, chunk=128, seed=0,
+        cache="16"):
     """Returns (last tokens' outputs from the growing cache, the same from one
     chunk over each whole sequence): fp16 [sequences, hidden] twice."""
     B = len(prompts)
     total = [n + steps for n in prompts]
-    layer, check = (AttentionLayer(hidden, heads, kv_heads, head_dim, B, max(total), seed=seed) for _ in range(2))
+    layer, check = (AttentionLayer(hidden, heads, kv_heads, head_dim, B, max(total), seed=seed, cache=cache)
+                    for _ in range(2))
     gen = torch.Generator(device="cuda").manual_seed(seed + 1)
     tokens = [torch.randn(n, hidden, generator=gen, device="cuda").half() for n in total]
 
@@ -107,8 +120,9 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--hidden", type=int, default=1024)
+    ap.add_argument("--cache", choices=sorted(CACHES), default="16")
     a = ap.parse_args()
-    grown, whole = run(steps=a.steps, hidden=a.hidden)
+    grown, whole = run(steps=a.steps, hidden=a.hidden, cache=a.cache)
     worst = (grown.float() - whole.float()).abs().max().item()
     scale = whole.float().abs().max().item()
     print(f"{grown.shape[0]} sequences, {a.steps} tokens each from one graph: "

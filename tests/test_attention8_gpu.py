@@ -454,3 +454,22 @@ def test_caches_that_were_never_appended_to(w4, cuda_device):  # noqa: F811
                 b.k_scale[at] = 0
                 b.v_scale[at] = 0
             b.check(*b.attend(w4, return_lse=True))
+
+
+@pytest.mark.parametrize("cache", FORMS)
+@pytest.mark.parametrize("steps", [1, 5])
+def test_example(cuda_device, steps, cache):
+    """The decoder example over an 8-bit cache: chunks and single tokens see the same rows. Their kernels' outputs differ by the
+    roundings of the bounds above, of values that the two quantized projections leave near 1."""
+    import importlib.util
+    import os
+
+    from conftest import ROOT
+
+    spec = importlib.util.spec_from_file_location("decoder_attention",
+                                                  os.path.join(ROOT, "examples", "decoder_attention.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    grown, whole = example.run(steps=steps, cache=cache)
+    assert grown.shape == whole.shape and bool(grown.isfinite().all())
+    assert float((grown.float() - whole.float()).abs().max()) <= 0.01 * float(whole.float().abs().max())
