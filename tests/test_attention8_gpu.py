@@ -459,8 +459,8 @@ def test_caches_that_were_never_appended_to(w4, cuda_device):  # noqa: F811
 @pytest.mark.parametrize("cache", FORMS)
 @pytest.mark.parametrize("steps", [1, 5])
 def test_example(cuda_device, steps, cache):
-    """The decoder example over an 8-bit cache: chunks and single tokens see the same rows. Their kernels' outputs differ by the
-    roundings of the bounds above, of values that the two quantized projections leave near 1."""
+    """The decoder example over an 8-bit cache: chunks and single tokens see the same rows. Their kernels' outputs
+    differ by the roundings of the bounds above, of values that the two quantized projections leave near 1."""
     import importlib.util
     import os
 

@@ -160,8 +160,8 @@ LENS = {
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("form", [None, *FORMS])
 @pytest.mark.parametrize("lens", sorted(LENS))
-@pytest.mark.parametrize("H,G,D,page,layout", [(5, 1, 128, 16, "token"), (8, 8, 64, 48, "head"), (9, 3, 64, 16, "token"),
-                                               (40, 8, 128, 32, "head")])
+@pytest.mark.parametrize("H,G,D,page,layout", [(5, 1, 128, 16, "token"), (8, 8, 64, 48, "head"),
+                                               (9, 3, 64, 16, "token"), (40, 8, 128, 32, "head")])
 def test_append(w4, cuda_device, H, G, D, page, layout, lens, form, dtype):  # noqa: F811
     r = Rows(w4, cuda_device, dtype, form, H, G, D, page, LENS[lens], seed=D + H, layout=layout)
     qw, kw = ((1 + _normals((D,), s)).to(cuda_device) for s in (7, 8))

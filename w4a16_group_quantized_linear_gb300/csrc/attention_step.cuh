@@ -28,11 +28,23 @@
 // real, and the rows fill the 8-wide side: one of them for up to 8 rows, two for
 // 16. p reaches the second product's operand layout by an 8x8 register transpose.
 //
+// Over an 8-bit cache (HeldInt8, HeldE4m3) a step has half the bytes. The rows come to fp16 as they are
+// held, exactly, on their way from shared memory to the products: integers by three integer
+// operations and a subtraction for four, e4m3 by the hardware's conversion. A lane reads keys 16 bytes
+// at a time in whatever order of elements that gives, and the queries in the same one;
+// values come by the transposing load in pairs of bytes, which are two output rows. The scale
+// of a key multiplies its scores and that of a value its softmax weights, both in fp32. bf16
+// queries go to fp16 divided by a power of two. What bounds it is still the cache's bytes, but
+// the products' preparation is close behind (issue slots 47 to 53% busy, the integer pipe 43 to
+// 50%): three thread blocks an SM with 12 warps were 2% faster on short sequences and 6% slower on long ones.
+//
 // Measured (heads of 128, 8 cached): one token each of 64 sequences of 300 to
 // 8000 places, 1.10 GB: 171 us, 6.4 TB/s, 95% of the copy rate; two of 125000
 // and 133000 places, 1.06 GB: 167 us, 6.3 TB/s; one of 777 places 10 us, which is
 // latency: 2 us of launch, 1 to find the run, 2 for page entries and then k and
 // v, 1 for a block's products with instructions not yet cached, 4 for the join.
+// Over 8 bits: 64 such sequences, 0.574 GB: 109 us, 5.3 TB/s, 79% of the copy rate; two of 120 to
+// 150 thousand places in e4m3, 0.559 GB: 97 us, 5.8 TB/s, 87%; one of 777 places 12 us.
 #pragma once
 
 #include <type_traits>
@@ -225,9 +237,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp = lane >> 2, quad = lane & 3;
     const int ratio = a.ratio;
-    // Over an 8-bit cache a run of blocks is that of `lanes` thread blocks, a cached head each: the rows of a place's heads
-    // are neighbours in memory, and so are read at the same time. (As runs of one head after another, whose
-    // 128 bytes of a place are read alone, two sequences of 120 to 150 thousand places took 118 us.)
+    // Over an 8-bit cache a run of blocks is that of `lanes` thread blocks, a cached head each: the rows of a place's
+    // heads are neighbours in memory, and so are read at the same time. (With runs of one head after another, whose
+    // 128 bytes of a place are read alone, 64 sequences took 119 us and two long ones 118, where these runs
+    // took 113 and 106 with three thread blocks an SM; 127 and 111, 118 and 101 with two.)
     const int lanes = kHeld8 ? arg.lanes : 1, turns = kHeld8 ? arg.turns : a.c.kv_heads;
     const unsigned run = blockIdx.x / lanes, runs = gridDim.x / lanes;
     const int head0 = kHeld8 ? (int)(blockIdx.x - run * lanes) : 0;
