@@ -477,7 +477,8 @@ typedef struct {
  * w4a16_kv_append into an 8-bit cache (scales; NULL: the 16-bit one), with the
  * heads of q and k divided by their root mean squares and weighted before they are turned
  * (norms; NULL: as they are). What is computed is rounded once, to q_out's type, the
- * cache's, or the 8 bits. Rows that are not stored leave their scales as they were.
+ * cache's, or the 8 bits. Rows that are not stored leave their scales as they were. No two
+ * rows of a call may have the same page and slot: what is stored of such two is mixed.
  */
 W4A16_API w4a16_status w4a16_kv_append_ex(const w4a16_paged_cache* cache, const w4a16_cache_scales* scales, int64_t T,
                                           const uint16_t* k, int64_t k_row_stride, int64_t k_head_stride,
