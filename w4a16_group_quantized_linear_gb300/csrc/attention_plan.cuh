@@ -6,7 +6,9 @@
 // of that kernel are what it waits for (with a variant for 32 rows, 25 rows of
 // 16 sequences took 94 us, where the tiles take 87, and 32 of 64 sequences 132
 // against 130), and attention_tile.cu takes 256 rows to a tile on the tensor
-// cores. The lengths are on the device, so where a batch may hold both kinds
+// cores. Over an 8-bit cache the tiles' conversion costs more than reading half as many bytes
+// twice: there the step kernel takes up to 32 rows, in two groups side by side (the 25 rows: @@ us,
+// 143 in tiles). The lengths are on the device, so where a batch may hold both kinds
 // both kernels are launched, and each passes over the other's.
 #pragma once
 
@@ -19,14 +21,15 @@ struct Plan {
     int step_rows;  // most rows of a sequence of the step kernel
 };
 
-inline Plan plan_for(int64_t T, int64_t batch, int heads, int kv_heads, int64_t max_q_len) {
+// most_rows: of a sequence of the step kernel.
+inline Plan plan_for(int64_t T, int64_t batch, int heads, int kv_heads, int64_t max_q_len, int most_rows) {
     const int64_t ratio = heads / kv_heads, most = (max_q_len < T ? max_q_len : T) * ratio;
     Plan p;
-    p.tile = most > kStepRows;
+    p.tile = most > most_rows;
     // every sequence has max_q_len new tokens, as one alone has: no second kind
     const bool alike = T == batch * max_q_len || batch == 1;
-    p.step = !p.tile || (ratio <= kStepRows && !alike);
-    p.step_rows = (int)(most < kStepRows ? most : kStepRows);
+    p.step = !p.tile || (ratio <= most_rows && !alike);
+    p.step_rows = (int)(most < most_rows ? most : most_rows);
     return p;
 }
 

@@ -168,6 +168,7 @@ struct StepArgs {
     // of an 8-bit cache:
     ScaleArgs s;
     int lanes, turns;  // cached heads that are worked on side by side, and how many times that makes them all
+    int row_groups;    // of a head's rows, side by side too
 };
 
 // A sequence as this kernel sees it; blocks == 0: not one of its own.
@@ -177,12 +178,14 @@ struct Sequence {
     int block, blocks;  // its 64-place blocks: the first, and how many (one at least, so that empty rows are written)
 };
 
-__device__ __forceinline__ void load_sequence(const AttentionArgs& a, int b, int max_rows, Sequence& s) {
+// A sequence with rows from row0 on, and no more than max_rows.
+__device__ __forceinline__ void load_sequence(const AttentionArgs& a, int b, int row0, int max_rows, Sequence& s) {
     const int first = __ldg(a.c.q_offsets + b), next = __ldg(a.c.q_offsets + b + 1), length = __ldg(a.c.kv_lens + b);
     s.first = first;
     s.count = next - first;
     s.blocks = 0;
     if (first < 0 || next > a.c.T || s.count <= 0 || s.count > a.max_q_len || s.count * a.ratio > max_rows) return;
+    if (s.count * a.ratio <= row0) return;
     s.length = cache_length(a.c, length);
     s.low = first_seen(a, s.length - s.count);
     s.block = s.low / kBlock;
@@ -205,7 +208,7 @@ struct Cursor {
 };
 
 // turns: of the cached heads of a sequence (each, or `lanes` of them, is an item)
-__device__ __forceinline__ void next_item(const AttentionArgs& a, int max_rows, int turns, Cursor& c) {
+__device__ __forceinline__ void next_item(const AttentionArgs& a, int row0, int max_rows, int turns, Cursor& c) {
     if (++c.g == turns) {
         c.g = 0;
         do {
@@ -213,7 +216,7 @@ __device__ __forceinline__ void next_item(const AttentionArgs& a, int max_rows, 
                 c.s.blocks = 0;
                 break;
             }
-            load_sequence(a, c.b, max_rows, c.s);
+            load_sequence(a, c.b, row0, max_rows, c.s);
         } while (c.s.blocks == 0);
     }
     c.block = c.s.block;
@@ -241,9 +244,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     // heads are neighbours in memory, and so are read at the same time. (With runs of one head after another, whose
     // 128 bytes of a place are read alone, 64 sequences took 119 us and two long ones 118, where these runs
     // took 113 and 106 with three thread blocks an SM; 127 and 111, 118 and 101 with two.)
+    // Of more rows than one thread block takes, groups of them go side by side as well.
     const int lanes = kHeld8 ? arg.lanes : 1, turns = kHeld8 ? arg.turns : a.c.kv_heads;
-    const unsigned run = blockIdx.x / lanes, runs = gridDim.x / lanes;
-    const int head0 = kHeld8 ? (int)(blockIdx.x - run * lanes) : 0;
+    const int side = kHeld8 ? lanes * arg.row_groups : 1, max_rows = kHeld8 ? kRows * arg.row_groups : kRows;
+    const unsigned run = blockIdx.x / side, runs = gridDim.x / side;
+    const int member = kHeld8 ? (int)(blockIdx.x - run * side) : 0;
+    const int head0 = kHeld8 ? member % lanes : 0, row0 = kHeld8 ? member / lanes * kRows : 0;
     auto head_of = [&](int g) { return kHeld8 ? min(g * lanes + head0, a.c.kv_heads - 1) : g; };
 
     ptx::grid_dependency_wait();
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             Sequence s;
             int64_t n = 0;
             if (b0 + tid < a.c.batch) {
-                load_sequence(a, b0 + tid, kRows, s);
+                load_sequence(a, b0 + tid, row0, max_rows, s);
                 n = (int64_t)s.blocks * turns;
                 if (blockIdx.x == 0 && s.count > a.max_q_len) raise_device_error(a.c.err, W4A16_ERR_BAD_OFFSETS);
             }
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
 
     Cursor at;  // of the computation
     at.b = s_found[0];
-    load_sequence(a, at.b, kRows, at.s);
+    load_sequence(a, at.b, row0, max_rows, at.s);
     at.g = s_found[1] / at.s.blocks;
     at.block = at.s.block + s_found[1] % at.s.blocks;
     at.end = at.s.block + at.s.blocks;
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                 ptx::cp_async_16(dst + L::kHalfStage + L::at(row, chunk), a.c.v + off, size);
             }
             --to_load;
-            if (++to.block == to.end && to_load > 0) next_item(a, kRows, turns, to);
+            if (++to.block == to.end && to_load > 0) next_item(a, row0, max_rows, turns, to);
         }
         cp_async_commit();
     };
@@ -370,16 +376,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             const int p0 = to.block * kBlock + warp * kStep;
             const uint32_t dst = ring_u + stage * L::kStage;
             constexpr int kRowsPer = 32 / L::kChunks;
-            const int chunk = lane % L::kChunks, row0 = lane / L::kChunks;
+            const int chunk = lane % L::kChunks, first_row = lane / L::kChunks;
             const uint8_t *k8 = reinterpret_cast<const uint8_t*>(a.c.k), *v8 = reinterpret_cast<const uint8_t*>(a.c.v);
             const int g = head_of(to.g);
-            const int64_t first = rows + (int64_t)g * a.c.head_stride + row0 * a.c.slot_stride + chunk * 16;
+            const int64_t first = rows + (int64_t)g * a.c.head_stride + first_row * a.c.slot_stride + chunk * 16;
             const int64_t stride = kRowsPer * a.c.slot_stride;
             const uint8_t *k_row = k8 + first, *v_row = v8 + first;
             if (rows >= 0 && p0 >= to.s.low && p0 + kStep <= to.s.length) {
 #pragma unroll
                 for (int i = 0; i < kStep / kRowsPer; ++i) {
-                    const uint32_t at = dst + L::at(i * kRowsPer + row0, chunk);
+                    const uint32_t at = dst + L::at(i * kRowsPer + first_row, chunk);
                     ptx::cp_async_16(at, k_row, 16u);
                     ptx::cp_async_16(at + L::kHalfStage, v_row, 16u);
                     k_row += stride;
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                 // places outside the sequence or before every row's window: zeros, nothing read
 #pragma unroll
                 for (int i = 0; i < kStep / kRowsPer; ++i) {
-                    const int row = i * kRowsPer + row0;
+                    const int row = i * kRowsPer + first_row;
                     const bool real = rows >= 0 && p0 + row >= to.s.low && p0 + row < to.s.length;
                     const uint32_t at = dst + L::at(row, chunk);
                     ptx::cp_async_16(at, real ? k_row : k8, real ? 16u : 0u);
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                                  any ? 16u : 0u);
             }
             --to_load;
-            if (++to.block == to.end && to_load > 0) next_item(a, kRows, turns, to);
+            if (++to.block == to.end && to_load > 0) next_item(a, row0, max_rows, turns, to);
         }
         cp_async_commit();
     };
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     auto start_item = [&]() {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = n * 8 + grp;
+            const int r = row0 + n * 8 + grp;
             const bool real = r < at.s.count * ratio;
             const int64_t t = at.s.first + a.by_ratio.quotient(r);
             const uint16_t* q =
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int row = n * 8 + quad * 2 + j;
+                const int row = row0 + n * 8 + quad * 2 + j;
                 const int place = at.s.length - at.s.count + a.by_ratio.quotient(row);
                 low[n][j] = first_seen(a, place);
                 high[n][j] = row < at.s.count * ratio ? (a.causal ? min(at.s.length, place + 1) : at.s.length) : 0;
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    if (n * 8 + quad * 2 + j < at.s.count * ratio) {
+                    if (row0 + n * 8 + quad * 2 + j < at.s.count * ratio) {
                         lowest = max(lowest, low[n][j]);
                         highest = min(highest, high[n][j]);
                     }
@@ -615,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     float* join = reinterpret_cast<float*>(smem + kWarps * kRingBytes);
     auto write_row = [&](int r, int d, float (&acc)[8], float top, float sum) {
         if (kHeld8 && at.g * lanes + head0 >= a.c.kv_heads) return;  // (a head too many in the last turn)
-        const int64_t row = (int64_t)(at.s.first + a.by_ratio.quotient(r)) * a.heads + head_of(at.g) * ratio +
-                            a.by_ratio.remainder(r);
+        const int64_t row = (int64_t)(at.s.first + a.by_ratio.quotient(row0 + r)) * a.heads +
+                            head_of(at.g) * ratio + a.by_ratio.remainder(row0 + r);
         const float inv = sum > 0.0f || sum != sum ? (kHeld8 ? 1.0f / kWeightUp : 1.0f) / sum : 0.0f;
         uint4 w;
         w.x = E::pack(acc[0] * inv, acc[1] * inv);
@@ -629,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     auto finish_item = [&](int64_t item_begin, int64_t item_end) {
         const int c0 = shares.owner(item_begin, run), c1 = shares.owner(item_end - 1, run);
         const int64_t slot = 2 * (int64_t)blockIdx.x + (c0 == (int)run ? 1 : 0);
-        int* counter = arg.counters + c0 * lanes + head0;
-        const int rows = at.s.count * ratio;
+        int* counter = arg.counters + c0 * side + member;
+        const int rows = min(at.s.count * ratio - row0, kRows);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             for (int p0 = c0; p0 <= c1; p0 += 64) {
                 const int n = min(64, c1 + 1 - p0);
                 auto slot_of = [&](int k) {
-                    return (int64_t)(2 * ((p0 + k) * lanes + head0) + (p0 + k == c0));
+                    return (int64_t)(2 * ((p0 + k) * side + member) + (p0 + k == c0));
                 };
                 __syncthreads();
                 for (int k = tid; k < n * rows; k += kThreads) {
@@ -770,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
         }
         finish_item(item_begin, item_end);
         if (unit == run_end) break;
-        next_item(a, kRows, turns, at);
+        next_item(a, row0, max_rows, turns, at);
     }
 }
 
@@ -788,7 +794,7 @@ w4a16_status launch(const DeviceInfo& dev, StepArgs arg, cudaStream_t st) {
         double best = 0.0;
         for (int turns = 1; turns <= heads && best < 0.97; ++turns) {
             const int lanes = (heads + turns - 1) / turns;
-            const double busy = (double)(blocks / lanes) * heads / turns / blocks;
+            const double busy = (double)(blocks / (lanes * arg.row_groups)) * arg.row_groups * heads / turns / blocks;
             if (busy <= best) continue;
             best = busy;
             arg.lanes = lanes;
@@ -823,8 +829,9 @@ inline StepArgs step_args(const DeviceInfo& dev, const AttentionArgs& a, const S
 template <class E, class H>
 w4a16_status launch_rows(const DeviceInfo& dev, const AttentionArgs& a, const ScaleArgs& s, int max_rows,
                          void* workspace, cudaStream_t st) {
-    const StepArgs arg = step_args(dev, a, s, workspace);
+    StepArgs arg = step_args(dev, a, s, workspace);
     const bool two = max_rows > 8;
+    arg.row_groups = (max_rows + kStepRows - 1) / kStepRows;
     if (a.c.head_dim == 128)
         return two ? launch<E, H, 128, 2>(dev, arg, st) : launch<E, H, 128, 1>(dev, arg, st);
     return two ? launch<E, H, 64, 2>(dev, arg, st) : launch<E, H, 64, 1>(dev, arg, st);
