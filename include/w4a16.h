@@ -538,13 +538,13 @@ W4A16_API w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int
 /*
  * w4a16_paged_attention over an 8-bit cache (scales; NULL: the 16-bit one), with the
  * same workspace. The products run in fp16, whatever the element type. Sequences of
- * up to 16 rows per cached head: q as it is held, exact; a key's scale multiplies
- * its fp32 scores, a value's its softmax weights. More rows: q s, divided by a power of two for each 128
- * places and rounded to fp16 (places whose scale is less than 2^-21 of the largest of
- * their 128 lose bits; scales outside 2^-60 to 2^60 do too). bf16 queries are divided by a power of two for each
+ * up to 48 rows per cached head: q as it is held, exact; a key's scale multiplies
+ * its fp32 scores, a value's its softmax weights. More rows: of values q s, divided by a power
+ * of two for each 32 places and rounded to fp16 (places whose scale is less than 2^-21 of the largest of
+ * their 32 lose bits; scales outside 2^-60 to 2^60 do too). bf16 queries are divided by a power of two for each
  * row: elements below 2^-14 of the row's largest keep 2^-25 of that. Of a
  * place that no row of a sequence sees the scales are not multiplied in; a place with the scale
- * NaN makes the rows that see it NaN, as with more rows than 16 those of the same 128 rows that do not.
+ * NaN makes the rows that see it NaN, as with more rows than 48 those of the same 128 rows that do not.
  */
 W4A16_API w4a16_status w4a16_paged_attention_ex(const w4a16_paged_cache* cache, const w4a16_cache_scales* scales,
                                                 int64_t T, const uint16_t* q, int64_t q_row_stride,

@@ -14,7 +14,7 @@ from test_paged_attention_gpu import DTYPES, HEADS, LENS, Batch, _np, _status_st
 
 pytestmark = pytest.mark.gpu
 
-STEP_ROWS = 32  # past these rows of a cached head the values are rounded to 16 bits
+STEP_ROWS = 48  # past these rows of a cached head the values are rounded to 16 bits
 
 
 class Batch8(Batch):

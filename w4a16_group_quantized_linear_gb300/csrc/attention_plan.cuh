@@ -7,8 +7,8 @@
 // 16 sequences took 94 us, where the tiles take 87, and 32 of 64 sequences 132
 // against 130), and attention_tile.cu takes 256 rows to a tile on the tensor
 // cores. Over an 8-bit cache the tiles' conversion costs more than reading half as many bytes
-// twice: there the step kernel takes up to 32 rows, in two groups side by side (the 25 rows: @@ us,
-// 143 in tiles). The lengths are on the device, so where a batch may hold both kinds
+// two or three times: there the step kernel takes up to 48 rows, in groups of 16 side by side (25
+// rows 93 us and 143 in tiles, 45 rows 129 and 150; of bf16 94 and 167, 131 and 184). The lengths are on the device, so where a batch may hold both kinds
 // both kernels are launched, and each passes over the other's.
 #pragma once
 

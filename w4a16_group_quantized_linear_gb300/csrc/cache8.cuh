@@ -125,7 +125,7 @@ w4a16_status append_ex_launch(const DeviceInfo& dev, int dtype, int format, cons
 w4a16_status read_launch(const DeviceInfo& dev, int dtype, int format, const CacheArgs& c, const ScaleArgs& s,
                          uint16_t* k, uint16_t* v, cudaStream_t st);
 // Sequences of up to kStepRows8 rows per cached head, in groups of kStepRows.
-constexpr int kStepRows8 = 2 * kStepRows;
+constexpr int kStepRows8 = 3 * kStepRows;
 w4a16_status attention8_step_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
                                     const ScaleArgs& s, int max_rows, void* workspace, cudaStream_t st);
 w4a16_status attention8_tile_launch(const DeviceInfo& dev, int dtype, int format, const AttentionArgs& a,
