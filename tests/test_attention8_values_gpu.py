@@ -1,0 +1,70 @@
+"""Attention over an 8-bit cache whose rows are not all ordinary numbers, on the GPU, against the 64-bit oracle
+(oracle/attention.py derives the bounds): rows with an infinity or a NaN."""
+import numpy as np
+import pytest
+
+from oracle import attention as oa
+from test_attention8_gpu import STEP_ROWS, Batch8
+from test_kv_cache8_gpu import FORMS, _normals, _numbers
+from test_paged_attention_gpu import DTYPES, _np, _status_stays_clean, _t, w4  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _agrees(b, out, lse, where, **kw):
+    """out and lse of the rows and heads of `where` [T, H] are the oracle's."""
+    tiles = b.max_q * b.H // b.G > STEP_ROWS
+    with np.errstate(invalid="ignore"):
+        ref, lse_ref, parts = oa.attention8(_np(b.q), _numbers(b.k8), _numbers(b.v8), _np(b.k_scale), _np(b.v_scale),
+                                            b.table, b.offsets, b.kv, **kw)
+        tol = oa.attention8_tolerance(ref, parts, b.dtype, tiles)
+        lse_tol = oa.lse8_tolerance(lse_ref, b.D, parts, b.dtype)
+        assert (np.abs(_np(out) - ref) <= tol)[where].all()
+        assert (np.abs(_np(lse) - lse_ref) <= lse_tol)[where].all()
+
+
+def _append_one(w4, b, place, k, v):  # noqa: F811
+    """Rows k and v [1, G, D] at a place of the first sequence."""
+    import torch
+
+    i32 = dict(dtype=torch.int32, device=k.device)
+    w4.kv_append(k, v, b.k8, b.v8, b.page_table[:1], torch.tensor([0, 1], **i32), torch.tensor([place + 1], **i32),
+                 k_scale=b.k_scale, v_scale=b.v_scale)
+
+
+def _with_a_bad_row(w4, dev, H, G, D, form, dtype, bad, q_len, length, window, back):  # noqa: F811
+    """(batch, result with ordinary rows, result where head 0's row at place length - back has no number, which
+    rows and heads see it)"""
+    b = Batch8(dev, dtype, form, H, G, D, 16, [(q_len, length), (1, 50)], seed=H + D + q_len)
+    place = length - back
+    k, v = (_normals((1, G, D), s, _t(dtype), dev) for s in (31, 32))
+    _append_one(w4, b, place, k, v)
+    good = b.attend(w4, window=window, return_lse=True)
+    (k if "key" in bad else v)[0, 0, 7] = float("nan") if "NaN" in bad else -float("inf")
+    _append_one(w4, b, place, k, v)
+    _, at = oa.places(b.offsets, b.kv)
+    sees = np.zeros((q_len + 1, H), bool)
+    row_sees = (at >= place) & ((at - window < place) if window else True)
+    sees[:q_len, :H // G] = row_sees[:q_len, None]
+    assert sees.any() and not sees.all()
+    return b, good, b.attend(w4, window=window, return_lse=True), sees
+
+
+BAD = ["NaN value", "infinite value", "NaN key"]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len,window,back", [(3, 0, 1), (9, 0, 1), (9, 0, 5), (9, 20, 25)])
+def test_few_rows_that_do_not_see_a_bad_row_keep_their_bits(w4, cuda_device, q_len, window, back, D, bad, form,  # noqa: F811
+                                                            dtype):
+    """The row of a later token, or one before some rows' window."""
+    import torch
+
+    _, good, got, sees = _with_a_bad_row(w4, cuda_device, 10, 2, D, form, dtype, bad, q_len, 200, window, back)
+    sees = torch.from_numpy(sees).to(cuda_device)
+    assert bool(got[0][sees].isnan().all())
+    for x, y in zip(got, good):
+        assert torch.equal(x[~sees], y[~sees])

@@ -590,6 +590,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             pf[n][0] = transpose_8x8(M::pack(p[0], p[1]));
             pf[n][1] = transpose_8x8(M::pack(p[2], p[3]));
         }
+        if constexpr (kEdge && H::kFormat == W4A16_CACHE_E4M3) {
+            // The bytes of a row whose scale is NaN may be e4m3's NaN, and 0 times that is not 0: they are cleared.
+            // The rows that see the place have a weight of NaN.
+            bool bad[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) bad[j] = value_scale[j] != value_scale[j];
+            if (__any_sync(0xffffffffu, bad[0] || bad[1])) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    for (int c = quad; bad[j] && c < L::kChunks; c += 4)
+                        *reinterpret_cast<uint4*>(ring + stage * L::kStage + L::kHalfStage + L::at(grp + 8 * j, c)) =
+                            make_uint4(0, 0, 0, 0);
+                __syncwarp();
+            }
+        }
         if constexpr (kHeld8) {
             // Two adjacent elements of a place are one 16-bit unit of the transposing load: bytes 0 and 2 of a
             // register are one element of places 2 quad and 2 quad + 1, bytes 1 and 3 the next. Row grp of tile ks is
