@@ -543,8 +543,9 @@ W4A16_API w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int
  * of two for each 32 places and rounded to fp16 (places whose scale is less than 2^-21 of the largest of
  * their 32 lose bits; scales outside 2^-60 to 2^60 do too). bf16 queries are divided by a power of two for each
  * row: elements below 2^-14 of the row's largest keep 2^-25 of that. Of a
- * place that no row of a sequence sees the scales are not multiplied in; a place with the scale
- * NaN makes the rows that see it NaN, as with more rows than 48 those of the same 128 rows that do not.
+ * place that no row of a sequence sees the scales are not multiplied in. A place with the scale
+ * NaN makes the rows that see it NaN, whatever its bytes, and no others; lse is NaN too, but for a
+ * value's scale with up to 48 rows, where it is what it is without.
  */
 W4A16_API w4a16_status w4a16_paged_attention_ex(const w4a16_paged_cache* cache, const w4a16_cache_scales* scales,
                                                 int64_t T, const uint16_t* q, int64_t q_row_stride,

@@ -68,3 +68,15 @@ def test_few_rows_that_do_not_see_a_bad_row_keep_their_bits(w4, cuda_device, q_l
     assert bool(got[0][sees].isnan().all())
     for x, y in zip(got, good):
         assert torch.equal(x[~sees], y[~sees])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("form,D", [("int8", 128), ("e4m3", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("q_len,window,back", [(20, 0, 1), (20, 30, 40), (130, 0, 1), (130, 0, 70), (130, 64, 150)])
+def test_tiles_keep_a_bad_row_to_the_rows_that_see_it(w4, cuda_device, q_len, window, back, bad, form, D,  # noqa: F811
+                                                      dtype):
+    """Rows of the same tile, and of others that work on the same block of places, do not meet it."""
+    b, _, got, sees = _with_a_bad_row(w4, cuda_device, 10, 2, D, form, dtype, bad, q_len, 300, window, back)
+    assert all(np.isnan(_np(x))[sees].all() for x in got)
+    _agrees(b, *got, ~sees, window=window)

@@ -707,7 +707,9 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
         } else if (kHeld8 && warp >= kConvert) {
             // -------------------------------------------------------- conversion
             // Each warp brings 32 places of every block to fp16, a lane each, k and then v, as soon as there is room:
-            // keys as they are held, values times their scales. A place that is not seen becomes zeros.
+            // keys as they are held, values times their scales. A place that is not seen becomes zeros. One with a
+            // scale of NaN becomes a key of NaN, which the masks keep from the rows that do not see it, and a
+            // value of zeros: what is masked has a weight of 0, and 0 times NaN is NaN.
             if constexpr (kHeld8) {
                 constexpr int kPieces = D / 16;
                 const int place = (warp - kConvert) * 32 + lane;  // of the block
@@ -723,6 +725,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     return ok;
                 };
                 float value_scale = 0.0f;
+                bool bad = false;                   // one of the place's scales is NaN
                 int st = 0, rst = 0;                // stages of the two rings
                 uint32_t parity = 1, rparity = 0;   // of the one's empty and the other's full barriers
                 auto half = [&](int64_t h, auto is_value) {
@@ -737,10 +740,15 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         key_scale = seen ? scales[place] * a.scale_log2 : 1.0f;
                         if (key_scale == 0.0f) key_scale = power_of_2(-126);  // times minus infinity, not NaN
                         value_scale = seen ? scales[kBlock + place] : 0.0f;
+                        bad = key_scale != key_scale || value_scale != value_scale;
+                        if (bad) {
+                            key_scale = 1.0f;
+                            value_scale = 0.0f;
+                        }
                     }
                     // The power of two that takes the largest of 32 rows' values to fp16's last ones, 2^15 to 2^16,
                     // held to what leaves room on either side: what is 2^21 times smaller than that is still
-                    // rounded as fp16 is. (The largest of the scales' bits: not of NaN.)
+                    // rounded as fp16 is. (The largest of the scales' bits.)
                     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(value_scale, 0.0f)));
                     const int log2 = min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
                     RowFactor rf{};
@@ -749,10 +757,11 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     if constexpr (!kValue) {
                         const int at = (int)(h >> 1) % kFactors;
                         bars8->key_scale[at][place] = key_scale;
-                            if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
+                        if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
                     }
                     unsigned char* dst = ring + st * L::kStageBytes + place * 128;
-                    const bool whole = __all_sync(0xffffffffu, seen);
+                    const bool used = seen && !(kValue && bad);
+                    const bool whole = __all_sync(0xffffffffu, used);
                     // A loop: straight code for all pieces is longer than the instruction cache has room for beside
                     // the softmax's (2048 tokens over 30048 places: 8, 4, 2, 1 pieces at once 1303, 1153, 1176,
                     // 1243 us; 14 sequences of heads of 64 with a window of 1024: 4, 2 pieces 208, 201).
@@ -766,7 +775,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         if (!whole) {
 #pragma unroll
                             for (int i = 0; i < kAtOnce; ++i)
-                                if (!seen) held[i] = make_uint4(0, 0, 0, 0);
+                                if (!used) held[i] = make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
                         for (int i = 0; i < kAtOnce; ++i) {
@@ -780,6 +789,11 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                             *reinterpret_cast<uint4*>(to + ((chunk ^ 1) << 4)) = hi;
                         }
                     }
+                    if (!kValue && bad)
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kSlabBytes + ((c & 7) << 4)) =
+                                make_uint4(0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u);  // fp16's NaN
                     ptx::fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
