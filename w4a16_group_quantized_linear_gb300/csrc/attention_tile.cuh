@@ -725,26 +725,24 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     return ok;
                 };
                 float value_scale = 0.0f;
-                bool bad = false;                   // one of the place's scales is NaN
+                bool used = false;                  // the place is seen and has scales
                 int st = 0, rst = 0;                // stages of the two rings
                 uint32_t parity = 1, rparity = 0;   // of the one's empty and the other's full barriers
                 auto half = [&](int64_t h, auto is_value) {
                     constexpr bool kValue = decltype(is_value)::value;
                     if (!wait(&bars8->raw_full[rst], rparity)) return;
                     const unsigned char* src = smem + L::kRawAt + rst * L::kRawBytes;
-                    const int2 span = bars8->span[rst];
-                    const bool seen = place >= span.x && place < span.y;
                     float key_scale = 0.0f;
+                    bool seen = true;
                     if constexpr (!kValue) {
+                        const int2 span = bars8->span[rst];
+                        seen = place >= span.x && place < span.y;
                         const float* scales = reinterpret_cast<const float*>(src + L::kRawBlock);
-                        key_scale = seen ? scales[place] * a.scale_log2 : 1.0f;
+                        const float of_key = scales[place], of_value = scales[kBlock + place];
+                        used = seen && of_key < INFINITY && of_value < INFINITY;  // (NaN: neither)
+                        key_scale = used ? of_key * a.scale_log2 : 1.0f;
                         if (key_scale == 0.0f) key_scale = power_of_2(-126);  // times minus infinity, not NaN
-                        value_scale = seen ? scales[kBlock + place] : 0.0f;
-                        bad = key_scale != key_scale || value_scale != value_scale;
-                        if (bad) {
-                            key_scale = 1.0f;
-                            value_scale = 0.0f;
-                        }
+                        value_scale = used ? of_value : 0.0f;
                     }
                     // The power of two that takes the largest of 32 rows' values to fp16's last ones, 2^15 to 2^16,
                     // held to what leaves room on either side: what is 2^21 times smaller than that is still
@@ -760,7 +758,6 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
                     }
                     unsigned char* dst = ring + st * L::kStageBytes + place * 128;
-                    const bool used = seen && !(kValue && bad);
                     const bool whole = __all_sync(0xffffffffu, used);
                     // A loop: straight code for all pieces is longer than the instruction cache has room for beside
                     // the softmax's (2048 tokens over 30048 places: 8, 4, 2, 1 pieces at once 1303, 1153, 1176,
@@ -789,7 +786,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                             *reinterpret_cast<uint4*>(to + ((chunk ^ 1) << 4)) = hi;
                         }
                     }
-                    if (!kValue && bad)
+                    if (!kValue && !whole && seen && !used)
 #pragma unroll 1
                         for (int c = 0; c < D / 8; ++c)
                             *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kSlabBytes + ((c & 7) << 4)) =
