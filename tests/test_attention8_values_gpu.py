@@ -1,5 +1,5 @@
 """Attention over an 8-bit cache whose rows are not all ordinary numbers, on the GPU, against the 64-bit oracle
-(oracle/attention.py derives the bounds): rows with an infinity or a NaN."""
+(oracle/attention.py derives the bounds): rows with an infinity or a NaN, and rows of zeros."""
 import numpy as np
 import pytest
 
@@ -80,3 +80,32 @@ def test_tiles_keep_a_bad_row_to_the_rows_that_see_it(w4, cuda_device, q_len, wi
     b, _, got, sees = _with_a_bad_row(w4, cuda_device, 10, 2, D, form, dtype, bad, q_len, 300, window, back)
     assert all(np.isnan(_np(x))[sees].all() for x in got)
     _agrees(b, *got, ~sees, window=window)
+
+
+LEAST = {"appended": oa.LEAST / 127, "never appended": 0.0}
+
+
+def _zeros_and_large(dev, lens, D, form, least, e, drop, first):
+    """Zero rows and rows of scale 2^e, half of each sequence's places each, the zero rows' scores lower by `drop`."""
+    import torch
+
+    b = Batch8(dev, "bf16", form, 10, 2, D, 16, lens, seed=41)
+    b.q.copy_(torch.ones_like(b.q))
+    b.k8.copy_(torch.ones(b.k8.shape, device=dev).to(b.k8.dtype))
+    b.k_scale.fill_(drop / D ** 0.5)
+    b.v_scale.fill_(2.0 ** e)
+    at = [(b.table[s][p // 16], p % 16) for s, m in enumerate(b.kv) for p in range(m) if (p < m // 2) == first]
+    pages, slots = torch.tensor(at, device=dev).unbind(1)
+    b.v8.view(torch.uint8)[pages, slots] = 0
+    b.v_scale[pages, :, slots] = LEAST[least]
+    b.k_scale[pages, :, slots] = 0
+    return b
+
+
+@pytest.mark.parametrize("lens", [[(1, 700)], [(3, 300), (9, 640)], [(1, 400)] * 160])
+@pytest.mark.parametrize("form,least", [("int8", "appended"), ("e4m3", "never appended")])
+@pytest.mark.parametrize("e,drop", [(10, 8.0), (20, 0.0), (45, 8.0), (90, 0.0)])
+@pytest.mark.parametrize("first", [True, False])
+def test_rows_of_zeros_count_in_the_sum(w4, cuda_device, first, e, drop, least, form, lens):  # noqa: F811
+    b = _zeros_and_large(cuda_device, lens, 64, form, least, e, drop, first)
+    b.check(*b.attend(w4, return_lse=True))

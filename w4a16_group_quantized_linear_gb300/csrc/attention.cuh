@@ -193,6 +193,16 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// x 2^d for d <= 0, for a large x that is not to be lost with a 2^d below the normal range.
+__device__ __forceinline__ float times_exp2(float x, float d) {
+    float f = fast_exp2(d);
+    if (d < -100.0f) {
+        x *= 7.8886090522101181e-31f;  // 2^-100
+        f = fast_exp2(d + 100.0f);
+    }
+    return x * f;
+}
+
 // Equal runs of a work list over the thread blocks: the first `more` take base + 1 units.
 struct Shares {
     int64_t base;

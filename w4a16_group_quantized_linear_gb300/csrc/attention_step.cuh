@@ -161,6 +161,9 @@ __device__ __forceinline__ float to_fp16_row(uint32_t (&qf)[KS][NT][2], int n) {
 // What the weights of the second product over an 8-bit cache are multiplied by: the largest is then at 2^14, and
 // fp16 holds what is 2^-38 of it.
 constexpr float kWeightUp = 16384.0f;
+// What the logarithm of a value's scale is taken for if it is less (of zeros 2^-100 / most, or 0): the sum's terms are
+// then at most 2^96, and 2^30 of them inside 32 bits.
+constexpr float kLeastLog2 = -96.0f;
 
 struct StepArgs {
     AttentionArgs a;
@@ -252,6 +255,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
     const unsigned run = blockIdx.x / side, runs = gridDim.x / side;
     const int member = kHeld8 ? (int)(blockIdx.x - run * side) : 0;
     const int head0 = kHeld8 ? member % lanes : 0, row0 = kHeld8 ? member / lanes * kRows : 0;
+    // A sum to the maximum m brought to the larger one `top` (a sum of NaN stays one).
+    auto rescaled = [](float sum, float m, float top) {
+        const float d = m == -INFINITY ? m : m - top;
+        return kHeld8 ? times_exp2(sum, d) : sum * fast_exp2(d);
+    };
     auto head_of = [&](int g) { return kHeld8 ? min(g * lanes + head0, a.c.kv_heads - 1) : g; };
 
     ptx::grid_dependency_wait();
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             for (int j = 0; j < 2; ++j) {
                 key_scale[j] = sc[grp + 8 * j];
                 value_scale[j] = sc[kStep + grp + 8 * j];
-                value_log2[j] = fmaxf(__log2f(value_scale[j]), -107.0f);  // of 0 too, in a cache never appended to
+                value_log2[j] = fmaxf(__log2f(value_scale[j]), kLeastLog2);  // of 0 too, in a cache never appended to
             }
 #pragma unroll
             for (int c = 0; c < kKs / 4; ++c) {
@@ -537,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             }
         }
         // With an 8-bit cache the maximum is of s_j + log2(v_j), v_j the value's scale: it is the weights of the
-        // second product, 2^(s_j - m) v_j, that have to stay in range. The sum takes 2^(s_j - m), at most 2^107 each.
+        // second product, 2^(s_j - m) v_j, that have to stay in range. The sum takes 2^(s_j - m), at most 2^96 each.
         bool rise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -562,8 +570,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                     for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                     top = fmaxf(top, m[n][j]);
                     const float keep = m[n][j] == -INFINITY ? 0.0f : fast_exp2(m[n][j] - top);
+                    l[n][j] = rescaled(l[n][j], m[n][j], top);
                     m[n][j] = top;
-                    l[n][j] *= keep;
 #pragma unroll
                     for (int ks = 0; ks < kKs; ++ks) {
                         o[ks][n][j] *= keep;
@@ -691,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 st = s_stats[w][r];
-                    sum += st.y * (st.x == -INFINITY ? 0.0f : fast_exp2(st.x - top));  // a sum of NaN stays one
+                    sum += rescaled(st.y, st.x, top);
                     const float4* src = reinterpret_cast<const float4*>(join + L::join_at(w, col, d));
                     const float4 x = src[0], y = src[1];
                     acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
@@ -749,8 +757,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                 float higher = top;
                 for (int k = 0; k < n; ++k) higher = fmaxf(higher, stats[k * kRows + r].x);
                 const float keep = top == -INFINITY ? 0.0f : fast_exp2(top - higher);
+                sum = rescaled(sum, top, higher);
                 top = higher;
-                sum *= keep;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) acc[k] *= keep;
 #pragma unroll 8
@@ -759,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
                     const float4 x = __ldcg(src), y = __ldcg(src + 1);
                     const float2 st = stats[k * kRows + r];
                     const float f = st.x == -INFINITY ? 0.0f : fast_exp2(st.x - top);
-                    sum += st.y * f;
+                    sum += rescaled(st.y, st.x, top);
                     acc[0] += x.x * f; acc[1] += x.y * f; acc[2] += x.z * f; acc[3] += x.w * f;
                     acc[4] += y.x * f; acc[5] += y.y * f; acc[6] += y.z * f; acc[7] += y.w * f;
                 }
