@@ -539,7 +539,8 @@ W4A16_API w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int
  * w4a16_paged_attention over an 8-bit cache (scales; NULL: the 16-bit one), with the
  * same workspace. The products run in fp16, whatever the element type. Sequences of
  * up to 48 rows per cached head: q as it is held, exact; a key's scale multiplies
- * its fp32 scores, a value's its softmax weights. More rows: of values q s, divided by a power
+ * its fp32 scores, a value's its softmax weights (weights below 2^-126 s of the largest are lost, s the largest
+ * value scale: for values past 2^100 that counts). More rows: of values q s, divided by a power
  * of two for each 32 places and rounded to fp16 (places whose scale is less than 2^-21 of the largest of
  * their 32 lose bits; scales outside 2^-60 to 2^60 do too). bf16 queries are divided by a power of two for each
  * row: elements below 2^-14 of the row's largest keep 2^-25 of that. Of a

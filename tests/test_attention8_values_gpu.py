@@ -1,5 +1,6 @@
 """Attention over an 8-bit cache whose rows are not all ordinary numbers, on the GPU, against the 64-bit oracle
-(oracle/attention.py derives the bounds): rows with an infinity or a NaN, and rows of zeros."""
+(oracle/attention.py derives the bounds): rows with an infinity or a NaN, rows of zeros, and values as large as
+32 bits hold."""
 import numpy as np
 import pytest
 
@@ -108,4 +109,27 @@ def _zeros_and_large(dev, lens, D, form, least, e, drop, first):
 @pytest.mark.parametrize("first", [True, False])
 def test_rows_of_zeros_count_in_the_sum(w4, cuda_device, first, e, drop, least, form, lens):  # noqa: F811
     b = _zeros_and_large(cuda_device, lens, 64, form, least, e, drop, first)
+    b.check(*b.attend(w4, return_lse=True))
+
+
+def _of_scale(dev, q_len, D, form, e, spread=0.0):
+    """Values of scales between 2^(e - spread) and 2^e."""
+    import torch
+
+    b = Batch8(dev, "bf16", form, 10, 2, D, 16, [(q_len, 600), (1, 40)], seed=42)
+    down = spread * torch.rand(b.v_scale.shape, generator=torch.Generator().manual_seed(43))
+    b.v_scale.copy_(2.0 ** (e - down))
+    return b
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len", [1, 9])
+@pytest.mark.parametrize("e", [61, 64, 90, 103, 114, 118])
+def test_few_rows_over_large_values(w4, cuda_device, e, q_len, D, form):  # noqa: F811
+    """Up to the largest that 32 bits hold: the scores differ by little there, as weights below 2^-(126 - e) are lost."""
+    e = min(e, 116) if form == "e4m3" else e
+    b = _of_scale(cuda_device, q_len, D, form, e)
+    if e > 110:
+        b.q.mul_(2.0 ** -6)
     b.check(*b.attend(w4, return_lse=True))

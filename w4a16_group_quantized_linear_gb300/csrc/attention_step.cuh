@@ -592,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) step_kernel(const __gr
             l[n][1] += p[1] + p[3];
             if constexpr (kHeld8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)  // (a place that is not seen may have any scale)
-                    p[i] = kEdge && s[0][n][i] == -INFINITY ? 0.0f : p[i] * (value_scale[i >> 1] * kWeightUp);
+                for (int i = 0; i < 4; ++i)  // (a place that is not seen may have any scale; the first product is at most 1)
+                    p[i] = kEdge && s[0][n][i] == -INFINITY ? 0.0f : p[i] * value_scale[i >> 1] * kWeightUp;
             }
             pf[n][0] = transpose_8x8(M::pack(p[0], p[1]));
             pf[n][1] = transpose_8x8(M::pack(p[2], p[3]));
