@@ -542,7 +542,7 @@ W4A16_API w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int
  * its fp32 scores, a value's its softmax weights (weights below 2^-126 s of the largest are lost, s the largest
  * value scale: for values past 2^100 that counts). More rows: of values q s, divided by a power
  * of two for each 32 places and rounded to fp16 (places whose scale is less than 2^-21 of the largest of
- * their 32 lose bits; scales outside 2^-60 to 2^60 do too). bf16 queries are divided by a power of two for each
+ * their 32 lose bits; scales below 2^-81 do too). bf16 queries are divided by a power of two for each
  * row: elements below 2^-14 of the row's largest keep 2^-25 of that. Of a
  * place that no row of a sequence sees the scales are not multiplied in. A place with the scale
  * NaN makes the rows that see it NaN, whatever its bytes, and no others; lse is NaN too, but for a

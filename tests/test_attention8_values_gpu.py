@@ -133,3 +133,11 @@ def test_few_rows_over_large_values(w4, cuda_device, e, q_len, D, form):  # noqa
     if e > 110:
         b.q.mul_(2.0 ** -6)
     b.check(*b.attend(w4, return_lse=True))
+
+
+@pytest.mark.parametrize("form,D", [("int8", 128), ("e4m3", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("q_len", [20, 40, 130])
+@pytest.mark.parametrize("e,spread", [(62, 0), (64, 10), (70, 0), (90, 30), (116, 0)])
+def test_tiles_over_large_values(w4, cuda_device, e, spread, q_len, form, D):  # noqa: F811
+    b = _of_scale(cuda_device, q_len, D, form, e, spread)
+    b.check(*b.attend(w4, return_lse=True))

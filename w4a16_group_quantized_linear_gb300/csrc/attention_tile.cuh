@@ -89,6 +89,9 @@ constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 // weight reaches 2^14, inside fp16's 2^16, and o, not divided by l yet, that many times the values'
 // sum: with bf16's range it has to stay small. (2^40 was no faster, and lost values past 2^87.)
 constexpr float kMaxSlack = 14.0f;
+// Powers of two that the scales of 32 places' values are taken to: zeros (2^-100 / most, or 0) count as the least of
+// them, and no scale of a row of 32-bit numbers passes the largest.
+constexpr int kLeastValue = -60, kMostValue = 121;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutCol = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -745,10 +748,10 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         value_scale = used ? of_value : 0.0f;
                     }
                     // The power of two that takes the largest of 32 rows' values to fp16's last ones, 2^15 to 2^16,
-                    // held to what leaves room on either side: what is 2^21 times smaller than that is still
+                    // held to kLeastValue and kMostValue: what is 2^21 times smaller than that is still
                     // rounded as fp16 is. (The largest of the scales' bits.)
                     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(value_scale, 0.0f)));
-                    const int log2 = min(max((int)(top >> 23) - 127, -60), 60) - H::kRoom;
+                    const int log2 = min(max((int)(top >> 23) - 127, kLeastValue), kMostValue) - H::kRoom;
                     RowFactor rf{};
                     if constexpr (kValue) rf = row_factor(value_scale * power_of_2(-log2), H::kRoom);
                     if (!wait(&bars->empty[st], parity)) return;  // (the first round's, before any: done)
