@@ -16,6 +16,8 @@
 // 4.6 TB/s, 69% of the copy rate (28.7 without a norm and wholly turned); 9764 tokens of 40
 // query and 8 cached heads into e4m3, 266 MB: 55 us, 4.8 TB/s, 72%; reading 30011 places of 8
 // heads back from int8, 186 MB: 33 us, 5.7 TB/s, 85%; one token appended 6.2 us.
+#include <type_traits>
+
 #include "cache8.cuh"
 #include "rotary.cuh"
 
@@ -56,13 +58,35 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]), E::pack(x[6], x[7]));
 }
 
-// 1 / sqrt(mean(x^2) + eps) over the `lanes` lanes of a head; all lanes of the warp.
-__device__ __forceinline__ float inverse_rms(const float (&x)[16], int lanes, float mean, float eps) {
+// Heads are worked on twice: as they are, and once more those (of bf16) whose squares leave 32 bits. The second
+// time the lanes of a head may be alone; x is multiplied by a power of two.
+using Once = std::false_type;
+using Again = std::true_type;
+
+// mean(x^2) + eps over the `lanes` lanes of a head, which are among those of `mask`.
+__device__ __forceinline__ float mean_square(const float (&x)[16], int lanes, unsigned mask, float mean, float eps) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum += x[i] * x[i];
-    for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return rsqrtf(sum * mean + eps);
+    for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+    return sum * mean + eps;
+}
+
+// Whether a mean square is one that the squares it came from are held in (it is not where an element passes 2^59, or
+// all and eps are as small as 2^-80).
+__device__ __forceinline__ bool in_range(float square) { return square < INFINITY && square >= 8.2718061255302767e-25f; }
+
+// x and eps times a power of two that takes their squares into range.
+__device__ __forceinline__ void into_range(float (&x)[16], float& eps, float square) {
+    const float f = square < 1.0f ? 1.2379400392853803e27f : 8.4703294725430034e-22f;  // 2^90, 2^-70
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] *= f;
+    eps = eps * f * f;
+}
+
+// The lanes of the thread's head in its warp.
+__device__ __forceinline__ unsigned head_mask(int lanes) {
+    return (0xffffffffu >> (32 - lanes)) << (threadIdx.x & 31 & -lanes);
 }
 
 // x times r and the weights of the thread's two pieces. (In shared memory: the 16 registers that they would take
@@ -140,22 +164,39 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_norm_kernel(const
     const bool rotate = mine && p.pair >= 0 && angles(a.r, a.T, t, 0, p.pair, a.err, c, s);
     __syncthreads();
     uint16_t* dst = a.out + t * a.out_row_stride;
-    auto head = [&](int h, uint4& u, uint4& w) {
+    const int lanes = 1 << a.split.shift;
+    bool left = false;  // heads to be worked on again
+    auto head = [&](int h, uint4& u, uint4& w, auto again) {
+        constexpr bool kAgain = decltype(again)::value;
+        const unsigned mask = kAgain ? head_mask(lanes) : 0xffffffffu;
         float x[16];
         unpack16<E>(u, w, x);
-        load(h + 2, u, w);
-        const float r = inverse_rms(x, 1 << a.split.shift, a.mean, a.eps);
-        weigh(x, r, s_weight + p.first, s_weight + p.second);
+        load(kAgain ? h + 1 : h + 2, u, w);
+        float square = mean_square(x, lanes, mask, a.mean, a.eps);
+        const bool mine_now = kAgain != in_range(square);
+        if constexpr (kAgain) {
+            if (!mine_now) return;
+            float eps = a.eps;
+            into_range(x, eps, square);
+            square = mean_square(x, lanes, mask, a.mean, eps);
+        } else {
+            left = left || !mine_now;
+        }
+        weigh(x, rsqrtf(square), s_weight + p.first, s_weight + p.second);
         if (rotate) turn(x, a.r.interleaved, c, s);
-        if (h >= real_end) return;
+        if (h >= real_end || !mine_now) return;
         *reinterpret_cast<uint4*>(dst + h * a.out_head_stride + p.first) = pack8<E>(x);
         *reinterpret_cast<uint4*>(dst + h * a.out_head_stride + p.second) = pack8<E>(x + 8);
     };
 #pragma unroll 1
     for (int h = first; h < end; h += 2) {
-        head(h, u0, w0);
-        if (h + 1 < end) head(h + 1, u1, w1);
+        head(h, u0, w0, Once{});
+        if (h + 1 < end) head(h + 1, u1, w1, Once{});
     }
+    if (!left) return;
+    load(first, u0, w0);
+#pragma unroll 1
+    for (int h = first; h < end; ++h) head(h, u0, w0, Again{});
 }
 
 // ----------------------------------------------------------------- append --
@@ -221,27 +262,40 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_ex_kernel(const
     const int64_t slot = page * a.c.page_stride + in_page * a.c.slot_stride;
     const int64_t scale_slot = page * a.s.page_stride + in_page;
     __syncthreads();
-    auto head = [&](int h, uint4& u, uint4& w) {
+    bool left = false;  // heads to be worked on again
+    auto head = [&](int h, uint4& u, uint4& w, auto again) {  // (h is that of the whole thread block)
+        constexpr bool kAgain = decltype(again)::value;
+        const unsigned mask = kAgain ? head_mask(chunks) : 0xffffffffu;
         const bool query = h < a.heads, value = h >= a.heads + G;
         const int g = value ? h - a.heads - G : h - a.heads;
         float x[16];
         unpack16<E>(u, w, x);
-        load(h + 2, u, w);
-        if (a.q_norm || a.k_norm) {
-            const float r = inverse_rms(x, chunks, a.mean, a.eps);
-            if (query ? a.q_norm != nullptr : !value && a.k_norm != nullptr)
-                weigh(x, r, s_weight[!query] + p.first, s_weight[!query] + p.second);
+        load(kAgain ? h + 1 : h + 2, u, w);
+        bool mine_now = !kAgain;
+        if (query ? a.q_norm != nullptr : !value && a.k_norm != nullptr) {
+            float square = mean_square(x, chunks, mask, a.mean, a.eps);
+            mine_now = kAgain != in_range(square);
+            if constexpr (kAgain) {
+                if (!mine_now) return;
+                float eps = a.eps;
+                into_range(x, eps, square);
+                square = mean_square(x, chunks, mask, a.mean, eps);
+            } else {
+                left = left || !mine_now;
+            }
+            weigh(x, rsqrtf(square), s_weight[!query] + p.first, s_weight[!query] + p.second);
         }
+        if (kAgain && !mine_now) return;
         if (rotate && !value) turn(x, a.r.interleaved, c, s);
         float top = 0.0f;
         if constexpr (H::kFormat != 0) {
-            if (__any_sync(0xffffffffu, !query)) {
+            if (!query) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) top = max_nan(top, fabsf(x[j]));
-                for (int o = 1; o < chunks; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+                for (int o = 1; o < chunks; o <<= 1) top = max_nan(top, __shfl_xor_sync(mask, top, o));
             }
         }
-        if (h >= real_end) return;
+        if (h >= real_end || !mine_now) return;
         if (query) {
             uint16_t* dst = a.q_out + (t * a.heads + h) * D;
             *reinterpret_cast<uint4*>(dst + p.first) = pack8<E>(x);
@@ -264,11 +318,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_ex_kernel(const
     };
 #pragma unroll 1
     for (int h = begin; h < end; h += 2) {
-        head(h, u0, w0);
+        head(h, u0, w0, Once{});
         __syncwarp();
-        if (h + 1 < end) head(h + 1, u1, w1);
+        if (h + 1 < end) head(h + 1, u1, w1, Once{});
         __syncwarp();
     }
+    if (!left) return;
+    load(begin, u0, w0);
+#pragma unroll 1
+    for (int h = begin; h < end; ++h) head(h, u0, w0, Again{});
 }
 
 // ------------------------------------------------------------------- read --
