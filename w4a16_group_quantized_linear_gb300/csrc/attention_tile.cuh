@@ -1099,8 +1099,11 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     // for like all else (its second part follows from the same pass). The stream
                     // behind can always go on, and that is enough: all of the other's products of the tiles
                     // before it are issued, so its half gets past them, fetches its queries and
-                    // announces p; and its blocks are loaded, as the ring holds the two blocks that the
-                    // other may be ahead.
+                    // announces p; and the ring's entry that it needs next is the oldest that has not been
+                    // given back (all before it are used by both), so that it is loaded whatever the ring's
+                    // length. (With three entries, over 8 bits and heads of 128, the other is an entry and a half
+                    // ahead at most, and the next scores of a tile that the halves share, whose entry is
+                    // the one in use, are formed in another round.)
                     struct Stream {
                         int k = -1, j = 0, to = 0;          // entry, block, and the end of the entry's blocks
                         int begin = 0, end = 0, step = 1;   // the half's blocks of the entry
@@ -1170,7 +1173,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         // Where the half goes on in the same tile and the blocks up to its next one are
                         // here, that is found out before the wait for p, and the next scores follow
                         // the products at once.
-                        const int ahead = n - 1 + 2 * s.step;  // the next block's k
+                        const int ahead = n - 1 + 2 * s.step;  // the next block's k (n's own entry where they are three)
                         bool on =
                             s.j + s.step < s.end && (!other.more || s.at() + s.step <= other.at() + 2) && here(ahead);
                         if (s.step == 2) on = on && here(n + 1) && here(n + 2);
