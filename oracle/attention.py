@@ -39,12 +39,12 @@ Bounds. With u the half-spacing of the element type (2^-11 fp16, 2^-8 bf16):
   products run in fp16 whatever the type. bf16 queries go to fp16 divided by a power
   of two of the row's largest element m_q: exact above 2^-14 of it, else off by 2^-25
   of it, a score by r = 2^-24 scale m_q max_j sum_d |k_jd|, and a weight by twice that
-  (it and the sum). Where values are brought to fp16 as q s first (whole tiles), divided
-  by a power of two that takes the largest of 32 places past 2^14, each is off by w = 2^-11 of
-  itself, or by twice 2^-25 in fp16's own units (a product and a sum), of which 2^6
-  at least make the largest scale: below 2^-30 of the sequence's largest scale s_v:
-      |y - ref| <= u |ref| + (w + e + 2 r + w) A + 2^-30 s_v + ...,   |lse - ref| <= ... + r
-  and the weights' factor is that of 32 places, so tiny takes 2 s_v sum_j |q_jd|.
+  (it and the sum):
+      |y - ref| <= u |ref| + (w + e + 2 r) A + ...,   |lse - ref| <= ... + r
+  with w = 2^-11, the rounding of the weights. In whole tiles their factor is that of 32 places, which some of the
+  rows may not see, so tiny takes 2 s_v sum_j |q_jd|, s_v the sequence's largest scale. There the bound
+  has room besides for values that are rounded to fp16 as q s, each off by w of itself or by twice 2^-25 in
+  fp16's own units, of which 2^6 at least make the largest scale: w A + 2^-30 s_v.
 """
 from __future__ import annotations
 
@@ -233,7 +233,7 @@ def attention8(q, k, v, k_scale, v_scale, page_table, q_offsets, kv_lens, **kw):
 
 
 def attention8_tolerance(out, parts, dtype, rounded=False):
-    """rounded: values are brought to fp16 as q s first."""
+    """rounded: whole tiles, with room for values that are brought to fp16 as q s first."""
     u, w = UNIT[dtype], UNIT["fp16"]
     r = parts["Q"] if dtype == "bf16" else 0.0
     e = (_slack(out.shape[2], parts) + 2 * r + (w if rounded else 0.0))[..., None]

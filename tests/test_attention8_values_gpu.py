@@ -150,3 +150,18 @@ def test_tiles_over_large_values(w4, cuda_device, e, spread, q_len, form, D):  #
 def test_rows_of_zeros_count_in_the_sum_of_tiles(w4, cuda_device, first, e, drop, least, form, D, lens):  # noqa: F811
     b = _zeros_and_large(cuda_device, lens, D, form, least, e, drop, first)
     b.check(*b.attend(w4, return_lse=True))
+
+
+@pytest.mark.parametrize("form,D", [("int8", 64), ("int8", 128), ("e4m3", 128)])
+@pytest.mark.parametrize("q_len", [20, 60])
+def test_tiles_round_the_weights_and_the_result_alone(w4, cuda_device, q_len, D, form):  # noqa: F811
+    """Errors of fp16's rounding are alike and independent, of the weights (each of a random value: as large a part of
+    the result's size as of theirs) and of the result: together sqrt(2) times the latter. A third rounding would make
+    it sqrt(3); the limit is between them."""
+    b = Batch8(cuda_device, "fp16", form, 10, 2, D, 16, [(q_len, 1500)], seed=51)
+    out, lse = b.attend(w4, return_lse=True)
+    b.check(out, lse, tiles=False)
+    ref, _, _ = oa.attention8(_np(b.q), _numbers(b.k8), _numbers(b.v8), _np(b.k_scale), _np(b.v_scale), b.table,
+                              b.offsets, b.kv)
+    alone = np.sqrt(((ref.astype(np.float16) - ref) ** 2).mean())
+    assert np.sqrt(((_np(out) - ref) ** 2).mean()) <= 1.56 * alone

@@ -46,15 +46,12 @@
 // are held, and their scales, into a ring of their own, and four more bring them into the
 // ring of the products:
 //
-//   warps 12-15     conversion: 32 places of each block, a lane each. Keys as they are held, which is
-//                   exact; values times their scales, divided by a power of two of 32 places and
-//                   rounded once. (Keys so rounded would leave 2^-11 of a score's parts, which the logarithms
-//                   of sums show.)
+//   warps 12-15     conversion: 32 places of each block, a lane each, as they are held, which is exact.
 //
-// The softmax warps multiply the scores by the keys' scales, 128 of them that all rows share, from shared
-// memory, 16 columns ahead of their use. The register file is divided between the roles. Measured, the
-// chunk above: 1155 us, 1050 TFLOP/s, 54% of the burst: without the conversion's arithmetic
-// 1068, without the scales' loads and products too about 930. The 14 sequences above 198 us.
+// The softmax warps multiply the scores by the keys' scales and the weights by the values', 128 of each that all
+// rows share, from shared memory. (Values brought to fp16 as q s instead: 1.67 times the error of rounding the result
+// alone, where this leaves 1.38, and no faster.) The register file is divided between the roles. Measured, the
+// chunk above: 1135 us, 1070 TFLOP/s, 55% of the burst. The 14 sequences above 204 us.
 //
 // TMEM: scores (and p) of the halves in columns [0, 128) and [128, 256), o in
 // [256, 256 + D) and [256 + D, 256 + 2 D).
@@ -82,13 +79,16 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;      // places per block: MMA N of the scores, K of the output
 constexpr int kLoadK = 8, kMmaWarp = 9, kPlanWarp = 10, kLoadV = 11;
 constexpr int kConvert = 12, kConverters = 4;  // warps that bring an 8-bit cache's blocks to fp16
-constexpr int kBarBytes = 1792, kBar8Bytes = 4608;  // struct Bars, struct Bars8
+constexpr int kBarBytes = 1792, kBar8Bytes = 8704;  // struct Bars, struct Bars8
 constexpr int kFactors = 8;      // blocks whose scales are kept: more than the converters can be ahead of the softmax
 constexpr int kEntries = 4;      // tiles of the work that are laid out ahead
 // How far (log2) a score may pass the running maximum of a whole tile before the maximum moves. A
 // weight reaches 2^14, inside fp16's 2^16, and o, not divided by l yet, that many times the values'
 // sum: with bf16's range it has to stay small. (2^40 was no faster, and lost values past 2^87.)
 constexpr float kMaxSlack = 14.0f;
+// Over an 8-bit cache weights go up to 2^(kMaxSlack8 + kRoom + 1), the value scales multiplied in.
+constexpr float kMaxSlack8 = 7.0f;
+constexpr int kRoom = 7;  // (log2) where the largest of 32 value scales is taken to
 // Powers of two that the scales of 32 places' values are taken to: zeros (2^-100 / most, or 0) count as the least of
 // them, and no scale of a row of 32-bit numbers passes the largest. The sum's terms are weights times the power, so
 // that beside values of scale 2^e those of zeros are lost below 2^-(86 - e) of the largest: 2^-40 for 2^46. (Terms
@@ -175,7 +175,8 @@ static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 // And those of an 8-bit cache.
 struct Bars8 {
     float key_scale[kFactors][kBlock];  // of blocks, by their place in the run, times that of the softmax in base 2
-    int4 value_log2[kFactors];          // what their values are divided by, of 32 places each
+    float value_scale[kFactors][kBlock];  // of their values, divided by a power of two of 32 places each
+    int4 value_log2[kFactors];            // and that power's logarithm
     uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
     int2 span[kMaxRaw];      // places from a block's first to the first that is seen, and past the last
 };
@@ -539,24 +540,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return *reinterpret_cast<float2*>(&d);
 }
 
-// What a row's elements are multiplied by, f = g 2^-h, for products that are rounded once: with G = fp16(g) and
-// d = fp16(g - G),  q f = (q 2^-h) G + (q 2^-h) d.  2^-h, up to 2^-15, keeps g and d normal where f is far
-// below the block's largest; q 2^-h is exact.
-struct RowFactor {
-    uint32_t gd;  // G, d
-    uint32_t pc;  // 2^-h, and -1152 2^-h
-};
-
-__device__ __forceinline__ RowFactor row_factor(float f, int room) {
-    const int h = min(max(room + 127 - (int)((__float_as_uint(f) >> 23) & 0xFF), 0), 15);
-    const float g = f * power_of_2(h), down = power_of_2(-h);
-    const float rounded = __half2float(__float2half_rn(g));
-    return RowFactor{Fp16::pack(g, g - rounded), Fp16::pack(down, -1152.0f * down)};
-}
-
-__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
-__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
-
 // 16 held elements to fp16, exactly.
 template <class H>
 __device__ __forceinline__ void exact16(const uint4& u, uint4& lo, uint4& hi) {
@@ -564,27 +547,6 @@ __device__ __forceinline__ void exact16(const uint4& u, uint4& lo, uint4& hi) {
     H::to_fp16(u.y, lo.z, lo.w);
     H::to_fp16(u.z, hi.x, hi.y);
     H::to_fp16(u.w, hi.z, hi.w);
-}
-
-// And times their row's factor.
-template <class H>
-__device__ __forceinline__ void scaled16(const uint4& u, const RowFactor& r, uint4& lo, uint4& hi) {
-    const __half2 g = as_half2(__byte_perm(r.gd, 0, 0x1010)), d = as_half2(__byte_perm(r.gd, 0, 0x3232));
-    const __half2 p = as_half2(__byte_perm(r.pc, 0, 0x1010)), c = as_half2(__byte_perm(r.pc, 0, 0x3232));
-    auto two = [&](uint32_t v) {
-        const __half2 q = H::kFormat == W4A16_CACHE_INT8 ? __hfma2(as_half2(v), p, c) : __hmul2(as_half2(v), p);
-        return as_u32(__hfma2(q, g, __hmul2(q, d)));
-    };
-    auto four = [&](uint32_t v, uint32_t& a, uint32_t& b) {
-        if constexpr (H::kFormat == W4A16_CACHE_INT8) H::to_fp16_plus_1152(v, a, b);
-        else H::to_fp16(v, a, b);
-        a = two(a);
-        b = two(b);
-    };
-    four(u.x, lo.x, lo.y);
-    four(u.y, lo.z, lo.w);
-    four(u.z, hi.x, hi.y);
-    four(u.w, hi.z, hi.w);
 }
 
 template <class E, class H, int D, bool PAIRED>
@@ -712,8 +674,8 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
             if (!ok && lane == 0) fail(x, bars);
         } else if (kHeld8 && warp >= kConvert) {
             // -------------------------------------------------------- conversion
-            // Each warp brings 32 places of every block to fp16, a lane each, k and then v, as soon as there is room:
-            // keys as they are held, values times their scales. A place that is not seen becomes zeros. One with a
+            // Each warp brings 32 places of every block to fp16, a lane each, k and then v, as soon as there is room,
+            // as they are held. A place that is not seen becomes zeros. One with a
             // scale of NaN becomes a key of NaN, which the masks keep from the rows that do not see it, and a
             // value of zeros: what is masked has a weight of 0, and 0 times NaN is NaN.
             if constexpr (kHeld8) {
@@ -730,45 +692,36 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     ok = __all_sync(0xffffffffu, ok);
                     return ok;
                 };
-                float value_scale = 0.0f;
                 bool used = false;                  // the place is seen and has scales
                 int st = 0, rst = 0;                // stages of the two rings
                 uint32_t parity = 1, rparity = 0;   // of the one's empty and the other's full barriers
-                auto half = [&](int64_t h, auto is_value) {
-                    constexpr bool kValue = decltype(is_value)::value;
-                    if (!wait(&bars8->raw_full[rst], rparity)) return;
+#pragma unroll 1
+                for (int64_t h = 0; h < halves; ++h) {
+                    if (!wait(&bars8->raw_full[rst], rparity)) break;
                     const unsigned char* src = smem + L::kRawAt + rst * L::kRawBytes;
-                    float key_scale = 0.0f;
-                    bool seen = true;
-                    if constexpr (!kValue) {
+                    const bool keys = (h & 1) == 0;
+                    float key_scale = 0.0f, value_scale = 0.0f;
+                    bool bad = false;
+                    uint32_t top = 0;
+                    if (keys) {
                         const int2 span = bars8->span[rst];
-                        seen = place >= span.x && place < span.y;
+                        const bool seen = place >= span.x && place < span.y;
                         const float* scales = reinterpret_cast<const float*>(src + L::kRawBlock);
                         const float of_key = scales[place], of_value = scales[kBlock + place];
                         used = seen && of_key < INFINITY && of_value < INFINITY;  // (NaN: neither)
+                        bad = seen && !used;
                         key_scale = used ? of_key * a.scale_log2 : 1.0f;
                         if (key_scale == 0.0f) key_scale = power_of_2(-126);  // times minus infinity, not NaN
                         value_scale = used ? of_value : 0.0f;
+                        top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(value_scale, 0.0f)));
                     }
-                    // The power of two that takes the largest of 32 rows' values to fp16's last ones, 2^15 to 2^16,
-                    // held to kLeastValue and kMostValue: what is 2^21 times smaller than that is still
-                    // rounded as fp16 is. (The largest of the scales' bits.)
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(value_scale, 0.0f)));
-                    const int log2 = min(max((int)(top >> 23) - 127, kLeastValue), kMostValue) - H::kRoom;
-                    RowFactor rf{};
-                    if constexpr (kValue) rf = row_factor(value_scale * power_of_2(-log2), H::kRoom);
-                    if (!wait(&bars->empty[st], parity)) return;  // (the first round's, before any: done)
-                    if constexpr (!kValue) {
-                        const int at = (int)(h >> 1) % kFactors;
-                        bars8->key_scale[at][place] = key_scale;
-                        if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
-                    }
+                    if (!wait(&bars->empty[st], parity)) break;  // (the first round's, before any: done)
                     unsigned char* dst = ring + st * L::kStageBytes + place * 128;
                     const bool whole = __all_sync(0xffffffffu, used);
-                    // A loop: straight code for all pieces is longer than the instruction cache has room for beside
-                    // the softmax's (2048 tokens over 30048 places: 8, 4, 2, 1 pieces at once 1303, 1153, 1176,
-                    // 1243 us; 14 sequences of heads of 64 with a window of 1024: 4, 2 pieces 208, 201).
-                    constexpr int kAtOnce = D / 32;
+                    // One loop for keys and values: the instruction cache is the softmax's too (one for each and 4 pieces
+                    // at once: 2048 tokens over 30048 places 1222 us, where this takes 1130). Pieces at once: 8, 4, 2
+                    // there 1130, 1136, 1163 us; 14 sequences of heads of 64 with a window of 1024: 4, 2, 1 204, 203, 203.
+                    constexpr int kAtOnce = D == 128 ? 8 : 2;
 #pragma unroll 1
                     for (int i0 = 0; i0 < kPieces; i0 += kAtOnce) {
                         uint4 held[kAtOnce];  // all before the first store: it could be to the same place
@@ -783,8 +736,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
 #pragma unroll
                         for (int i = 0; i < kAtOnce; ++i) {
                             uint4 lo, hi;
-                            if constexpr (kValue) scaled16<H>(held[i], rf, lo, hi);
-                            else exact16<H>(held[i], lo, hi);
+                            exact16<H>(held[i], lo, hi);
                             const int piece = (i0 + i) ^ turn;
                             unsigned char* to = dst + (piece >> 2) * L::kSlabBytes;
                             const int chunk = ((piece & 3) * 2) ^ r;
@@ -792,7 +744,17 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                             *reinterpret_cast<uint4*>(to + ((chunk ^ 1) << 4)) = hi;
                         }
                     }
-                    if (!kValue && !whole && seen && !used)
+                    if (keys) {
+                        // The power of two that takes the largest of 32 value scales to 2^kRoom, held to kLeastValue and
+                        // kMostValue: what is 2^21 times smaller than that is still a normal number of fp16. (The
+                        // largest of the scales' bits.)
+                        const int log2 = min(max((int)(top >> 23) - 127, kLeastValue), kMostValue) - kRoom;
+                        const int at = (int)(h >> 1) % kFactors;
+                        bars8->key_scale[at][place] = key_scale;
+                        bars8->value_scale[at][place] = value_scale * power_of_2(-log2);
+                        if (lane == 0) reinterpret_cast<int*>(&bars8->value_log2[at])[warp - kConvert] = log2;
+                    }
+                    if (bad)
 #pragma unroll 1
                         for (int c = 0; c < D / 8; ++c)
                             *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kSlabBytes + ((c & 7) << 4)) =
@@ -811,12 +773,6 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         rst = 0;
                         rparity ^= 1u;
                     }
-                };
-#pragma unroll 1
-                for (int64_t h = 0; h < halves; h += 2) {
-                    half(h, std::false_type{});
-                    if (ok) half(h + 1, std::true_type{});
-                    if (!ok) break;
                 }
                 if (!ok && lane == 0) fail(x, bars);
                 __syncwarp();
@@ -1229,7 +1185,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
         // that of rounding the result alone, where they are up to 1.7 times). For whole tiles
         // it would cost 11% (2048 tokens over 30048 places 870 against 786 us) for errors of
         // 1.1 instead of 1.4 times.
-        constexpr float kSlack = PAIRED ? 0.0f : kMaxSlack;
+        constexpr float kSlack = PAIRED ? 0.0f : kHeld8 ? kMaxSlack8 : kMaxSlack;
         const int w = warp >> 2;
         const int row = tid & (kHalf - 1);
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -1327,11 +1283,11 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     }
                     ptx::tmem_st_wait();
                 }
-                // Over an 8-bit cache the keys' scales multiply the scores, and the values are divided by powers of
-                // two, of 32 places each: the maximum and the weights are those of 2^s times that power, by which the
-                // sum is divided again.
+                // Over an 8-bit cache the keys' scales multiply the scores, and the values' the weights, divided by a
+                // power of two of 32 places each: the maximum and the weights before are those of 2^s times that
+                // power, by which the sum is divided again.
                 int4 value_log2 = make_int4(0, 0, 0, 0);
-                uint32_t key_scale = 0;
+                uint32_t key_scale = 0, value_scale = 0;
                 float4 k0[4], k1[4];  // scales of 16 columns each
                 auto load_scales = [&](float4 (&k)[4], int c) {
 #pragma unroll
@@ -1341,6 +1297,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     const int at = (e.ordinal + j - e.from) % kFactors;
                     value_log2 = bars8->value_log2[at];
                     key_scale = ptx::smem_u32(bars8->key_scale[at]);
+                    value_scale = ptx::smem_u32(bars8->value_scale[at]);
                 }
                 float top;
                 uint32_t s0[32], s1[32];
@@ -1433,6 +1390,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         part = make_float2(0.0f, 0.0f);
                     }
                     uint32_t p[16];
+                    [[maybe_unused]] float4 f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 v = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
@@ -1447,6 +1405,10 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                         v.x = fast_exp2(v.x);
                         v.y = fast_exp2(v.y);
                         part = add2(part, v);
+                        if constexpr (kHeld8) {
+                            if (i % 2 == 0) f = lds_float4(value_scale + (c + 2 * i) * 4);
+                            v = mul2(v, i % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
+                        }
                         p[i] = M::pack(v.x, v.y);
                     }
                     ptx::tmem_st_32x32b_x16(s_addr + (c >> 1), p);

@@ -27,7 +27,6 @@ struct Held16 {
 struct HeldInt8 {
     static constexpr int kFormat = W4A16_CACHE_INT8;
     static constexpr float kMost = 127.0f;
-    static constexpr int kRoom = 7;  // 2 kMost 2^kRoom is below fp16's 65504
     // x inv, |x inv| <= 127 but for rounding, to the nearest integers (ties to even): with
     // 1.5 * 2^23 added, an integer's two's complement is in the low bits of the sum
     __device__ static __forceinline__ uint32_t encode4(const float* x, float inv) {
@@ -47,15 +46,10 @@ struct HeldInt8 {
                                   __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
         return *reinterpret_cast<const uint32_t*>(&h);
     }
-    __device__ static __forceinline__ void to_fp16_plus_1152(uint32_t v, uint32_t& b01, uint32_t& b23) {
-        v ^= 0x80808080u;
-        b01 = __byte_perm(v, 0x64646464u, 0x4140);
-        b23 = __byte_perm(v, 0x64646464u, 0x4342);
-    }
     __device__ static __forceinline__ void to_fp16(uint32_t v, uint32_t& b01, uint32_t& b23) {
-        to_fp16_plus_1152(v, b01, b23);
-        b01 = minus_1152(b01);
-        b23 = minus_1152(b23);
+        v ^= 0x80808080u;
+        b01 = minus_1152(__byte_perm(v, 0x64646464u, 0x4140));
+        b23 = minus_1152(__byte_perm(v, 0x64646464u, 0x4342));
     }
     __device__ static __forceinline__ void to_fp16_apart(uint32_t v, uint32_t& b02, uint32_t& b13) {
         v ^= 0x80808080u;
@@ -67,7 +61,6 @@ struct HeldInt8 {
 struct HeldE4m3 {
     static constexpr int kFormat = W4A16_CACHE_E4M3;
     static constexpr float kMost = 448.0f;
-    static constexpr int kRoom = 6;
     __device__ static __forceinline__ uint32_t encode4(const float* x, float inv) {
         uint16_t lo, hi;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
