@@ -542,12 +542,10 @@ W4A16_API w4a16_status w4a16_paged_attention(const w4a16_paged_cache* cache, int
  * 2^-25 of that.
  *
  * Keys and values take part as they are held, exact; a key's scale multiplies its fp32
- * scores, a value's its softmax weights, which are then rounded to fp16. With s the largest
- * value scale, of sequences of up to 48 rows per cached head weights below 2^-126 s of the
- * largest are lost: for values past 2^100 that counts. Of more rows, products of weight and value
- * scale below 2^-21 of the largest of 32 places lose bits, and scales below 2^-61 do. Of places
- * whose scale is below 2^-40 (of rows of zeros, say) weights below 2^-86 s of the largest are
- * lost: beside values past 2^50 that counts.
+ * scores, a value's its softmax weights, which are then rounded to fp16. Of sequences of up to
+ * 48 rows per cached head, weights below 2^-126 s of the largest are lost, with s the largest value
+ * scale: for values past 2^100 that counts. Of more rows, products of weight and value
+ * scale below 2^-21 of the largest of 32 places lose bits, and scales below 2^-61 do.
  *
  * The scales of a place that no row of a sequence sees are not multiplied in. A place with the
  * scale NaN makes the rows that see it NaN, whatever its bytes, and no others; lse is NaN

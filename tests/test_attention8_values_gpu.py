@@ -145,7 +145,7 @@ def test_tiles_over_large_values(w4, cuda_device, e, spread, q_len, form, D):  #
 
 @pytest.mark.parametrize("lens", [[(20, 700)], [(40, 700), (1, 90)], [(130, 2000)]])
 @pytest.mark.parametrize("form,least,D", [("int8", "appended", 128), ("e4m3", "never appended", 64)])
-@pytest.mark.parametrize("e,drop", [(45, 8.0), (60, 8.0), (70, 0.0)])
+@pytest.mark.parametrize("e,drop", [(45, 8.0), (60, 8.0), (90, 8.0), (110, 0.0)])
 @pytest.mark.parametrize("first", [True, False])
 def test_rows_of_zeros_count_in_the_sum_of_tiles(w4, cuda_device, first, e, drop, least, form, D, lens):  # noqa: F811
     b = _zeros_and_large(cuda_device, lens, D, form, least, e, drop, first)

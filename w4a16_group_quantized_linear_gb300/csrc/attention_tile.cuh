@@ -90,11 +90,11 @@ constexpr float kMaxSlack = 14.0f;
 constexpr float kMaxSlack8 = 7.0f;
 constexpr int kRoom = 7;  // (log2) where the largest of 32 value scales is taken to
 // Powers of two that the scales of 32 places' values are taken to: zeros (2^-100 / most, or 0) count as the least of
-// them, and no scale of a row of 32-bit numbers passes the largest. The sum's terms are weights times the power, so
-// that beside values of scale 2^e those of zeros are lost below 2^-(86 - e) of the largest: 2^-40 for 2^46. (Terms
-// formed apart for such places, or a least power that follows the largest scale, were built: 1 to 10% slower on data
-// that has none.)
+// them, and no scale of a row of 32-bit numbers passes the largest.
 constexpr int kLeastValue = -40, kMostValue = 121;
+// Beside values of 2^80 times their power of two or more, weights times that power may be below the normal range (and so
+// 0) though they count in the softmax's sum: from here on they are looked for.
+constexpr int kFarPower = kLeastValue - kRoom + 80;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOutCol = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -386,6 +386,15 @@ __device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
                    "+r"(r[30]), "+r"(r[31]));
 }
 
+// Four columns of the lane's row, waited for.
+__device__ __forceinline__ void tmem_ld_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(addr)
+        : "memory");
+}
+
 __device__ __forceinline__ float4 lds_float4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
@@ -547,6 +556,31 @@ __device__ __forceinline__ void exact16(const uint4& u, uint4& lo, uint4& hi) {
     H::to_fp16(u.y, lo.z, lo.w);
     H::to_fp16(u.z, hi.x, hi.y);
     H::to_fp16(u.w, hi.z, hi.w);
+}
+
+// The terms of a row's sum, 2^(s - m), of a block that are 0 as the weights times their values' power of two. (A
+// function: its code in the loop costs calls that never come here 2%. A least power that follows the tile's largest, in
+// place of it, costs them 3 to 10%, whichever warps find it.)
+__device__ __noinline__ float lost_terms(uint32_t s_addr, uint32_t key_scale, uint32_t value_log2, float up, float base) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < kBlock; c += 4) {
+        int log2;
+        asm volatile("ld.shared.s32 %0, [%1];" : "=r"(log2) : "r"(value_log2 + c / 32 * 4));
+        uint32_t s[4];
+        tmem_ld_x4(s_addr + c, s);
+        const float4 k = lds_float4(key_scale + c * 4);
+        const float by[4] = {k.x, k.y, k.z, k.w};
+        float part = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float v = fmaf(__uint_as_float(s[u]) * up, by[u], base + (float)log2);
+            if (fast_exp2(v) == 0.0f) part += fast_exp2(v + 100.0f);
+        }
+        sum += part * power_of_2(-log2) * 7.8886090522101181e-31f;  // 2^-100
+    }
+    __syncwarp();
+    return sum;
 }
 
 template <class E, class H, int D, bool PAIRED>
@@ -1226,6 +1260,11 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 }
             }
         };
+        // A sum to the maximum m brought to the larger one `top` (a sum of NaN stays one).
+        auto rescaled = [](float sum, float m, float top) {
+            const float d = m == -INFINITY ? m : m - top;
+            return kHeld8 ? times_exp2(sum, d) : sum * fast_exp2(d);
+        };
         auto q_ready = [&] {
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_shared();
@@ -1253,6 +1292,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
             up = next_up;
             float m = -INFINITY;
             float2 sum = make_float2(0.0f, 0.0f);
+            [[maybe_unused]] bool far = false;  // values of more than 2^kFarPower among the tile's
             for (int j = begin; j < end; j += step) {
                 if (!wait_bar(&bars->s_full[w], ns & 1, abort, wait_limit())) ok = false;
                 ++ns;
@@ -1366,9 +1406,14 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {
                     top = fmaxf(top, m);
                     const float keep = m == -INFINITY ? 0.0f : fast_exp2(m - top);
-                    m = top;
+                    const float2 before = sum;
                     sum.x *= keep;
                     sum.y *= keep;
+                    if (kHeld8 && m - top < -100.0f) [[unlikely]] {
+                        sum.x = rescaled(before.x, m, top);
+                        sum.y = rescaled(before.y, m, top);
+                    }
+                    m = top;
                     if (j > begin) {  // p v of the block before is done: these scores were formed after it
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
@@ -1383,6 +1428,15 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     }
                 }
                 const float base = m == -INFINITY ? 0.0f : -m;
+                if constexpr (kHeld8) {
+                    far = far || max(max(value_log2.x, value_log2.y), max(value_log2.z, value_log2.w)) > kFarPower;
+                    if (far) [[unlikely]] {
+                        const int at = (e.ordinal + j - e.from) % kFactors;
+                        tmem_ld_wait(s0);
+                        sum.x += lost_terms(s_addr, key_scale, ptx::smem_u32(&bars8->value_log2[at]), up, base);
+                        ptx::tmem_ld_32x32b_x32(s_addr, s0);
+                    }
+                }
                 auto weights = [&](int c, uint32_t (&s)[32], int log2) {
                     float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(base, base), part = sum;
                     if constexpr (kHeld8) {
@@ -1469,11 +1523,11 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     continue;
                 }
                 const float2 other = bars->pair_stats[row];
-                const float top = fmaxf(m, other.x);
+                const float top = fmaxf(m, other.x), before = m;
                 scale = m == -INFINITY ? 0.0f : fast_exp2(m - top);
                 scale0 = other.x == -INFINITY ? 0.0f : fast_exp2(other.x - top);
                 m = top;
-                l = l * scale + other.y * scale0;
+                l = rescaled(l, before, m) + rescaled(other.y, other.x, m);
             }
             const int at = first_row + row;
             const int token = a.by_ratio.quotient(at);
@@ -1550,7 +1604,7 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
 #pragma unroll 4
                     for (int i = 0; i < parts; ++i) {
                         const float2 v = stats(i);
-                        total += v.y * (v.x == -INFINITY ? 0.0f : fast_exp2(v.x - top));  // a sum of NaN stays one
+                        total += rescaled(v.y, v.x, top);
                     }
                     const float inv_total = total > 0.0f || total != total ? 1.0f / total : 0.0f;
 #pragma unroll 1
