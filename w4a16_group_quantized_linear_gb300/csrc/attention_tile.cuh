@@ -50,8 +50,9 @@
 //
 // The softmax warps multiply the scores by the keys' scales and the weights by the values', 128 of each that all
 // rows share, from shared memory. (Values brought to fp16 as q s instead: 1.67 times the error of rounding the result
-// alone, where this leaves 1.38, and no faster.) The register file is divided between the roles. Measured, the
-// chunk above: 1135 us, 1070 TFLOP/s, 55% of the burst. The 14 sequences above 204 us.
+// alone, where this leaves 1.4.) The register file is divided between the roles. Measured, the chunk above: 1112 us,
+// 1090 TFLOP/s, 56% of the burst. The 14 sequences above 206 us; heads of 64, 32 on 4, 2048 tokens over
+// 16048 places 427 us, 590 TFLOP/s.
 //
 // TMEM: scores (and p) of the halves in columns [0, 128) and [128, 256), o in
 // [256, 256 + D) and [256 + D, 256 + 2 D).
@@ -752,10 +753,10 @@ __global__ void __launch_bounds__(threads_of<H>(), 1)
                     if (!wait(&bars->empty[st], parity)) break;  // (the first round's, before any: done)
                     unsigned char* dst = ring + st * L::kStageBytes + place * 128;
                     const bool whole = __all_sync(0xffffffffu, used);
-                    // One loop for keys and values: the instruction cache is the softmax's too (one for each and 4 pieces
-                    // at once: 2048 tokens over 30048 places 1222 us, where this takes 1130). Pieces at once: 8, 4, 2
-                    // there 1130, 1136, 1163 us; 14 sequences of heads of 64 with a window of 1024: 4, 2, 1 204, 203, 203.
-                    constexpr int kAtOnce = D == 128 ? 8 : 2;
+                    // One loop for keys and values: the instruction cache is the softmax's too (one for each took 1222 us
+                    // for 2048 tokens over 30048 places, where this took 1136 with 4 pieces at once, 1130 with 8 and 1163
+                    // with 2). Of heads of 64, bf16, 2048 tokens over 16048 places: 4, 2, 1 pieces 459, 458, 446 us.
+                    constexpr int kAtOnce = D == 128 ? 8 : 1;
 #pragma unroll 1
                     for (int i0 = 0; i0 < kPieces; i0 += kAtOnce) {
                         uint4 held[kAtOnce];  // all before the first store: it could be to the same place
