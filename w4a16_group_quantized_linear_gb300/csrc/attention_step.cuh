@@ -45,8 +45,9 @@
 // latency: 2 us of launch, 1 to find the run, 2 for page entries and then k and
 // v, 1 for a block's products with instructions not yet cached, 4 for the join.
 // Over 8 bits: 64 such sequences, 0.574 GB: 109 us, 5.3 TB/s, 79% of the copy rate; two of 120 to
-// 150 thousand places in e4m3, 0.559 GB: 97 us, 5.8 TB/s, 87%; one of 777 places 12 us; 3 and 5
-// tokens (15 and 25 rows) of 16 sequences of 2000 to 9000 places, 0.175 GB: 55 and 93 us.
+// 150 thousand places in e4m3, 0.559 GB: 97 us, 5.8 TB/s, 87%; one of 777 places 10 us; 3 and 5
+// tokens (15 and 25 rows) of 16 sequences of 2000 to 9000 places, 0.175 GB: 55 and 93 us, where
+// reading them once is 26.
 #pragma once
 
 #include <type_traits>

@@ -7,15 +7,16 @@
 // of 16 elements each, by shuffles: their order is fixed.
 //
 // They move bytes, and the arithmetic is not far behind: some 200 instructions for 32 lanes of a
-// query head, 300 of a key's (issue slots 55 to 65% busy). So a thread takes up to eight heads
+// query head, 300 of a key's (issue slots 54 to 67% busy). So a thread takes up to eight heads
 // of a token, two of them loaded ahead, with the token's place, page and angles worked out once.
 // The norm's weights are in shared memory; the scales of a page lie beside each other by
 // head, [head][slot], so that the attention reads those of 4 places at once.
 //
-// Measured: 15360 tokens of 18 heads of 128 in bf16, normed and half turned by 3 axes, 146 MB: 31.5 us,
-// 4.6 TB/s, 69% of the copy rate (28.7 without a norm and wholly turned); 9764 tokens of 40
-// query and 8 cached heads into e4m3, 266 MB: 55 us, 4.8 TB/s, 72%; reading 30011 places of 8
-// heads back from int8, 186 MB: 33 us, 5.7 TB/s, 85%; one token appended 6.2 us.
+// Measured: 15360 tokens of 18 heads of 128 in bf16, normed and half turned by 3 axes, 146 MB: 32.5 us,
+// 4.5 TB/s, 67% of the copy rate (28.7 without a norm and wholly turned); 9764 tokens of 40
+// query and 8 cached heads into e4m3, 266 MB: 53.5 us, 5.0 TB/s, 74%, and into 16 bits, 280 MB: 52 us;
+// reading 30011 places of 8 heads back from int8, 186 MB: 33 us, 5.7 TB/s, 85%; one token
+// appended 2.8 us (a call among others in a graph).
 #include <type_traits>
 
 #include "cache8.cuh"
