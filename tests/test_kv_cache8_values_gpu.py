@@ -47,3 +47,17 @@ def test_append_norms_heads_of_any_size(w4, cuda_device, form):  # noqa: F811
                 got, _ = r.stored(cache, scale)
                 tol = oa.held_tolerance(ref, form, off)[0] if form else oa.UNIT["bf16"] * np.abs(ref) + off
             assert (np.abs(got - ref) <= tol).all()
+
+
+def test_heads_are_worked_on_once_in_place(w4, cuda_device):  # noqa: F811
+    """Heads that share a thread with one too large to be squared, written over themselves: results whose squares are
+    too small in turn (weights of 2^-50, no eps) are not taken for rows."""
+    import torch
+
+    x = _normals((20000, 8, 64), 25, torch.bfloat16, cuda_device)
+    x[::3, 1::2] *= 2.0 ** 70
+    weight = _normals((64,), 26).to(cuda_device) * 2.0 ** -50
+    table, places = w4.rope_table(4, 64, device=cuda_device), torch.zeros(20000, dtype=torch.int32, device=cuda_device)
+    apart = w4.rope(x, places, table, norm=weight, eps=0.0)
+    w4.rope(x, places, table, norm=weight, eps=0.0, out=x)
+    assert torch.equal(x, apart)

@@ -12,9 +12,9 @@
 // The norm's weights are in shared memory; the scales of a page lie beside each other by
 // head, [head][slot], so that the attention reads those of 4 places at once.
 //
-// Measured: 15360 tokens of 18 heads of 128 in bf16, normed and half turned by 3 axes, 146 MB: 32.5 us,
+// Measured: 15360 tokens of 18 heads of 128 in bf16, normed and half turned by 3 axes, 146 MB: 32.0 us,
 // 4.5 TB/s, 67% of the copy rate (28.7 without a norm and wholly turned); 9764 tokens of 40
-// query and 8 cached heads into e4m3, 266 MB: 53.5 us, 5.0 TB/s, 74%, and into 16 bits, 280 MB: 52 us;
+// query and 8 cached heads into e4m3, 266 MB: 53.2 us, 5.0 TB/s, 74%, and into 16 bits, 280 MB: 52 us;
 // reading 30011 places of 8 heads back from int8, 186 MB: 33 us, 5.7 TB/s, 85%; one token
 // appended 2.8 us (a call among others in a graph).
 #include <type_traits>
@@ -166,26 +166,29 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_norm_kernel(const
     __syncthreads();
     uint16_t* dst = a.out + t * a.out_row_stride;
     const int lanes = 1 << a.split.shift;
-    bool left = false;  // heads to be worked on again
+    unsigned left = 0;  // heads to be worked on again, a bit each
     auto head = [&](int h, uint4& u, uint4& w, auto again) {
         constexpr bool kAgain = decltype(again)::value;
         const unsigned mask = kAgain ? head_mask(lanes) : 0xffffffffu;
         float x[16];
         unpack16<E>(u, w, x);
         load(kAgain ? h + 1 : h + 2, u, w);
+        const int bit = (h - first) & 31;
+        if (kAgain && !(left >> bit & 1)) return;
         float square = mean_square(x, lanes, mask, a.mean, a.eps);
-        const bool mine_now = kAgain != in_range(square);
+        bool done = true;
         if constexpr (kAgain) {
-            if (!mine_now) return;
+            if (in_range(square)) return;  // (another head of the bit, of more than 32)
             float eps = a.eps;
             into_range(x, eps, square);
             square = mean_square(x, lanes, mask, a.mean, eps);
         } else {
-            left = left || !mine_now;
+            done = in_range(square);
+            left |= (done ? 0u : 1u) << bit;
         }
         weigh(x, rsqrtf(square), s_weight + p.first, s_weight + p.second);
         if (rotate) turn(x, a.r.interleaved, c, s);
-        if (h >= real_end || !mine_now) return;
+        if (h >= real_end || !done) return;
         *reinterpret_cast<uint4*>(dst + h * a.out_head_stride + p.first) = pack8<E>(x);
         *reinterpret_cast<uint4*>(dst + h * a.out_head_stride + p.second) = pack8<E>(x + 8);
     };
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_ex_kernel(const
     const int64_t slot = page * a.c.page_stride + in_page * a.c.slot_stride;
     const int64_t scale_slot = page * a.s.page_stride + in_page;
     __syncthreads();
-    bool left = false;  // heads to be worked on again
+    unsigned left = 0;  // heads to be worked on again, a bit each
     auto head = [&](int h, uint4& u, uint4& w, auto again) {  // (h is that of the whole thread block)
         constexpr bool kAgain = decltype(again)::value;
         const unsigned mask = kAgain ? head_mask(chunks) : 0xffffffffu;
@@ -272,21 +275,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_ex_kernel(const
         float x[16];
         unpack16<E>(u, w, x);
         load(kAgain ? h + 1 : h + 2, u, w);
-        bool mine_now = !kAgain;
+        const int bit = (h - begin) & 31;
+        if (kAgain && !(left >> bit & 1)) return;
+        bool done = true;
         if (query ? a.q_norm != nullptr : !value && a.k_norm != nullptr) {
             float square = mean_square(x, chunks, mask, a.mean, a.eps);
-            mine_now = kAgain != in_range(square);
             if constexpr (kAgain) {
-                if (!mine_now) return;
+                if (in_range(square)) return;  // (another head of the bit, of more than 32)
                 float eps = a.eps;
                 into_range(x, eps, square);
                 square = mean_square(x, chunks, mask, a.mean, eps);
             } else {
-                left = left || !mine_now;
+                done = in_range(square);
+                left |= (done ? 0u : 1u) << bit;
             }
             weigh(x, rsqrtf(square), s_weight[!query] + p.first, s_weight[!query] + p.second);
         }
-        if (kAgain && !mine_now) return;
         if (rotate && !value) turn(x, a.r.interleaved, c, s);
         float top = 0.0f;
         if constexpr (H::kFormat != 0) {
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_ex_kernel(const
                 for (int o = 1; o < chunks; o <<= 1) top = max_nan(top, __shfl_xor_sync(mask, top, o));
             }
         }
-        if (h >= real_end || !mine_now) return;
+        if (h >= real_end || !done) return;
         if (query) {
             uint16_t* dst = a.q_out + (t * a.heads + h) * D;
             *reinterpret_cast<uint4*>(dst + p.first) = pack8<E>(x);
